@@ -72,6 +72,10 @@ extern "C" {
 #define MOE_OUT_BF16 0 /* layer output as bf16 (round to nearest even)     */
 #define MOE_OUT_F32 1  /* layer output as fp32 (same sum, before rounding)  */
 
+#define MOE_GATE_NONE 0    /* no gate (1)                                   */
+#define MOE_GATE_TOKEN 1   /* gate fp32 [T], one factor per token           */
+#define MOE_GATE_CHANNEL 2 /* gate fp32 [d], one factor per channel         */
+
 #define MOE_PATH_AUTO 0    /* DECODE if T*k <= 8*E or T <= 16, else PREFILL */
 #define MOE_PATH_DECODE 1  /* weight-streaming kernels (small batches)     */
 #define MOE_PATH_PREFILL 2 /* LDS-tiled grouped MFMA kernels               */
@@ -483,6 +487,135 @@ int moe_retile_w4(const uint8_t *codes_canonical, int E, int N, int K, uint8_t *
                   void *stream);
 int moe_retile_bitplane8(const uint8_t *planes_canonical, int E, int N, int K,
                          uint8_t *planes, void *stream);
+
+/* ---------------------------------------------------------------------
+ * Around the routed experts: the dense 4-bit linear map, the norms before
+ * and after a block, and the token sort with its gradient.  [ExactMoE]
+ * Abstract: the routed experts are one part of a layer whose other parts run
+ * next to them; these calls take and return what the calls above do.
+ * Dtype arguments are MOE_OUT_BF16 or MOE_OUT_F32.  Arrays are dense and
+ * row-major; arrays of rows, gains and channel gates are 16-byte aligned, all
+ * others (and the gradients of gains and gates) 4-byte.  Unless said otherwise outputs must not overlap inputs.  T == 0 writes only the
+ * gradients of gains and channel gates (zeros).
+ *
+ * moe_linear_w4 -- y = x W'^T + bias with symmetric group-128 int4 weights.
+ *   out[t][n] = sum_g s[n][g] sum_{i in group g} q[n][i] x[t][i] + bias[n]
+ * x bf16 [T][K]; codes as moe_quantize_w4 writes them for a matrix [N][K]
+ * (E = 1: the tiled int4 layout of moe_expert_ffn_wq), scales fp16
+ * [N][K/128]; bias fp32 [N] or NULL; out [T][N] of out_dtype.  Products and
+ * sums are fp32 (codes enter the matrix cores exactly, weights are never
+ * rounded), rounded once on store.  A row of x that holds an infinity or NaN
+ * gives a row of infinities and NaN; finite values must be below 2^119 (their
+ * group sums are scaled by 192 in fp32).
+ * Requires N % 16 == 0, K % 128 == 0, T * K and T * N below 2^40.
+ * ws / ws_bytes: at least moe_linear_w4_ws_bytes(T, N, K) (may be 0), 256-byte
+ * aligned, no contents carried between calls.
+ * ------------------------------------------------------------------- */
+size_t moe_linear_w4_ws_bytes(int T, int N, int K);
+int moe_linear_w4(const void *x_bf16, int T, int N, int K, int group_size,
+                  const uint8_t *codes, const uint16_t *scales_f16,
+                  const float *bias, void *out, int out_dtype, void *ws,
+                  size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------
+ * moe_rmsnorm -- the norm in front of a block.
+ *   out = x * rstd * gain,  rstd = (mean_i x[t][i]^2 + eps)^(-1/2)
+ * x [T][d] of x_dtype, gain fp32 [d] or NULL (ones), out [T][d] of out_dtype.
+ * moe_rmsnorm_bwd -- its gradient, joined with the gradient dres that reaches
+ * x past the norm (NULL: none).  With u = dout * gain and h = x * rstd:
+ *   dx = dres + rstd * (u - h * mean_i(u h)),  dgain = sum_t dout * h
+ * dout [T][d] of dout_dtype; x, dres and dx of x_dtype; dgain fp32 [d] or NULL.
+ * dx may be dres.  rstd is computed again from x.
+ * ws / ws_bytes: at least moe_rmsnorm_bwd_ws_bytes(T, d), 16-byte aligned
+ * (NULL if dgain is NULL).  Sums are fp32 in a fixed order.
+ * Both require d % 8 == 0, d <= 8192, eps > 0 and finite.
+ * ------------------------------------------------------------------- */
+int moe_rmsnorm(const void *x, int x_dtype, const float *gain, int T, int d,
+                float eps, void *out, int out_dtype, void *stream);
+size_t moe_rmsnorm_bwd_ws_bytes(int T, int d);
+int moe_rmsnorm_bwd(const void *dout, int dout_dtype, const void *x, int x_dtype,
+                    const float *gain, const void *dres, int T, int d, float eps,
+                    void *dx, float *dgain, void *ws, size_t ws_bytes,
+                    void *stream);
+
+/* ---------------------------------------------------------------------
+ * moe_combine_residual -- end of a block in one pass: moe_combine, the norm
+ * after the block, its gate, the scaled residual and the next block's norm.
+ *   o    = sum_{j<k} topk_w[t][j] * y_pairs[pair_pos[t*k+j]] + add[t]
+ *   n    = o * rstd(o) * post_gain     (post_gain NULL: no norm, n = o)
+ *   v    = res_scale * residual[t] + gate * n
+ *   out  = v;   next_out = v * rstd(v) * next_gain
+ * y_pairs fp32 [T*k][d], pair_pos int32 [T*k], topk_w fp32 [T][k] as for
+ * moe_combine.  A pair whose pair_pos is outside [0, T*k) (e.g. -1, a padding
+ * token's) is dropped: its weight and row are not read.  k = 0: no routed
+ * pairs (y_pairs, pair_pos, topk_w NULL), the block's output is add alone.
+ * add [T][d] (a shared expert's or dense block's output) or NULL; residual,
+ * add and out are of `dtype`; gate fp32 [T] or [d] by gate_mode, NULL for
+ * MOE_GATE_NONE.  next_out bf16 [T][d] or NULL; next_gain fp32 [d] or NULL
+ * (ones); the next norm takes v before it is rounded to `dtype`.  out may be
+ * residual (in place).
+ *
+ * moe_combine_residual_bwd -- the gradient for dout [T][d] of `dtype`, the
+ * gradient of out (that of next_out is moe_rmsnorm_bwd's, with out as its x
+ * and dout joined through dres).  Outputs, each NULL if not wanted:
+ *   dy_pairs [T*k][d] of dy_dtype: w_j do in the rows that pairs own; rows
+ *     that no pair owns keep what they held.  Rows must be owned once.
+ *   dtopk_w fp32 [T][k]: <do, y_j>, 0 for a dropped pair.
+ *   dadd [T][d] of `dtype`: do.     dresidual [T][d]: res_scale * dout
+ *     (may be dout).
+ *   dpost_gain fp32 [d];  dgate fp32 [T] or [d] by gate_mode.
+ * where do is the gradient of o.  ws / ws_bytes: at least
+ * moe_combine_residual_bwd_ws_bytes(T, d), 16-byte aligned (NULL if neither
+ * dpost_gain nor a channel gate's dgate is wanted).
+ * Both require d % 8 == 0, d <= 8192, 0 <= k <= 16 (k + add not both absent),
+ * eps > 0, finite eps and res_scale.  Sums are fp32 in a fixed order.
+ * ------------------------------------------------------------------- */
+int moe_combine_residual(const void *residual, int dtype, const float *y_pairs,
+                         const int32_t *pair_pos, const float *topk_w, int k,
+                         const void *add, const float *post_gain,
+                         const float *gate, int gate_mode, float res_scale,
+                         float eps, const float *next_gain, int T, int d,
+                         void *out, void *next_out_bf16, void *stream);
+size_t moe_combine_residual_bwd_ws_bytes(int T, int d);
+int moe_combine_residual_bwd(const void *dout, int dtype, const float *y_pairs,
+                             const int32_t *pair_pos, const float *topk_w, int k,
+                             const void *add, const float *post_gain,
+                             const float *gate, int gate_mode, float res_scale,
+                             float eps, int T, int d, void *dy_pairs,
+                             int dy_dtype, float *dtopk_w, void *dadd,
+                             void *dresidual, float *dpost_gain, float *dgate,
+                             void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------
+ * Tokens into expert order and back, for experts that a caller runs itself
+ * between the two, and the gradients.  Pair p = t*k + j owns row pair_pos[p]
+ * of the grouped arrays (as moe_permute returns it); a pair whose pair_pos is
+ * outside [0, T*k) is dropped, and rows that no pair owns keep what they held.
+ * For the writing calls each row must be owned at most once.
+ * moe_dispatch:      xs[pair_pos[t*k+j]] = topk_w[t][j] * x[t]
+ *   (topk_w NULL: copies).  x [T][d] and xs [T*k][d] of `dtype`.
+ * moe_dispatch_bwd:  dx[t] = sum_j topk_w[t][j] * dxs[pair_pos[t*k+j]]
+ *                    dtopk_w[t][j] = <x[t], dxs[pair_pos[t*k+j]]>
+ *   dxs, x and dx of `dtype`; dtopk_w fp32 [T][k] or NULL, with it x and
+ *   topk_w are needed; x is not read without it.
+ * moe_combine_bwd, the gradient of moe_combine:
+ *                    dy_pairs[pair_pos[t*k+j]] = topk_w[t][j] * dout[t]
+ *                    dtopk_w[t][j] = <dout[t], y_pairs[pair_pos[t*k+j]]>
+ *   dout [T][d] of dout_dtype, y_pairs fp32 [T*k][d], dy_pairs [T*k][d] of
+ *   dy_dtype; either output may be NULL (y_pairs is read for dtopk_w alone,
+ *   topk_w for dy_pairs alone).
+ * dtopk_w of a dropped pair is 0.  Sums are fp32, ranks ascending.
+ * All require d % 8 == 0, d <= 8192, 1 <= k <= 16.
+ * ------------------------------------------------------------------- */
+int moe_dispatch(const void *x, int dtype, const int32_t *pair_pos,
+                 const float *topk_w, int T, int k, int d, void *xs, void *stream);
+int moe_dispatch_bwd(const void *dxs, int dtype, const void *x,
+                     const int32_t *pair_pos, const float *topk_w, int T, int k,
+                     int d, void *dx, float *dtopk_w, void *stream);
+int moe_combine_bwd(const void *dout, int dout_dtype, const float *y_pairs,
+                    const int32_t *pair_pos, const float *topk_w, int T, int k,
+                    int d, void *dy_pairs, int dy_dtype, float *dtopk_w,
+                    void *stream);
 
 #ifdef __cplusplus
 }

@@ -11,7 +11,9 @@ first two also as one call, moe_route_permute).
 """
 from __future__ import annotations
 
+import collections
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,7 @@ MOE_FMT_W4_SYM, MOE_FMT_BITPLANE8 = 0, 1
 MOE_BITS_NONE, MOE_BITS_PER_PAIR, MOE_BITS_PER_EXPERT, MOE_BITS_RANK_RULE = 0, 1, 2, 3
 MOE_OUT_BF16, MOE_OUT_F32 = 0, 1
 MOE_PATH_AUTO, MOE_PATH_DECODE, MOE_PATH_PREFILL = 0, 1, 2
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL = 0, 1, 2
 MOE_GROUP = 128
 
 # Every symbol the header declares (checked by the CPU tests).
@@ -34,7 +37,11 @@ EXPORTS = ("moe_status_str", "moe_last_error", "moe_route_ws_bytes", "moe_route"
            "moe_bp_distortion_ws_bytes",
            "moe_bp_distortion", "moe_allocate_bits", "moe_cache_create", "moe_cache_destroy",
            "moe_cache_ws_bytes", "moe_cache_forward", "moe_cache_stats", "moe_cache_slots",
-           "moe_cache_reset", "moe_cache_plan", "moe_retile_w4", "moe_retile_bitplane8")
+           "moe_cache_reset", "moe_cache_plan", "moe_retile_w4", "moe_retile_bitplane8",
+           "moe_linear_w4_ws_bytes", "moe_linear_w4", "moe_rmsnorm",
+           "moe_rmsnorm_bwd_ws_bytes", "moe_rmsnorm_bwd", "moe_combine_residual",
+           "moe_combine_residual_bwd_ws_bytes", "moe_combine_residual_bwd", "moe_dispatch",
+           "moe_dispatch_bwd", "moe_combine_bwd")
 
 
 class MoeError(RuntimeError):
@@ -100,6 +107,26 @@ def load_library():
     lib.moe_cache_reset.argtypes = [vp]
     lib.moe_cache_plan.argtypes = [i32, i32, i32, vp, vp, vp, ctypes.c_int64, vp, vp, vp, i32,
                                    vp, vp, i32, vp, vp]
+    f32 = ctypes.c_float
+    lib.moe_linear_w4_ws_bytes.argtypes, lib.moe_linear_w4_ws_bytes.restype = [i32] * 3, sz
+    lib.moe_linear_w4.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, sz, vp]
+    lib.moe_rmsnorm.argtypes = [vp, i32, vp, i32, i32, f32, vp, i32, vp]
+    lib.moe_rmsnorm_bwd_ws_bytes.argtypes = [i32, i32]
+    lib.moe_rmsnorm_bwd_ws_bytes.restype = sz
+    lib.moe_rmsnorm_bwd.argtypes = [vp, i32, vp, i32, vp, vp, i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.moe_combine_residual.argtypes = [vp, i32, vp, vp, vp, i32, vp, vp, vp, i32, f32, f32, vp,
+                                         i32, i32, vp, vp, vp]
+    lib.moe_combine_residual_bwd_ws_bytes.argtypes = [i32, i32]
+    lib.moe_combine_residual_bwd_ws_bytes.restype = sz
+    lib.moe_combine_residual_bwd.argtypes = [vp, i32, vp, vp, vp, i32, vp, vp, vp, i32, f32, f32,
+                                             i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_dispatch.argtypes = [vp, i32, vp, vp, i32, i32, i32, vp, vp]
+    lib.moe_dispatch_bwd.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp]
+    lib.moe_combine_bwd.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp]
+    for name in ("moe_linear_w4", "moe_rmsnorm", "moe_rmsnorm_bwd", "moe_combine_residual",
+                 "moe_combine_residual_bwd", "moe_dispatch", "moe_dispatch_bwd",
+                 "moe_combine_bwd"):
+        getattr(lib, name).restype = i32
     for name in ("moe_route", "moe_permute", "moe_route_permute", "moe_expert_ffn_wq",
                  "moe_combine", "moe_layer_forward_wq", "moe_layer_forward_wq_noalloc",
                  "moe_bp_distortion",
@@ -442,6 +469,385 @@ def moe_set_ffn_events(gateup_begin=None, gateup_end=None, down_begin=None,
         return None if e is None else ctypes.c_void_p(e)
     _check("moe_set_ffn_events", load_library().moe_set_ffn_events(
         h(gateup_begin), h(gateup_end), h(down_begin), h(down_end)))
+
+
+# ------------------------------------------- around the routed experts
+# These calls check shapes, types, layout and device before they touch a
+# pointer (ValueError), launch on the device their tensors are on, and take
+# outputs and workspaces that they create from the memory of the stream they
+# launch on.
+
+def _on_device(fn):
+    """Runs fn with the first tensor's device current and, when the keyword
+    `stream` is given, with that stream current; fn launches on the current
+    stream."""
+
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        import torch
+        if not isinstance(first, torch.Tensor):
+            raise ValueError(f"{fn.__name__}: a tensor is needed, got {type(first).__name__}")
+        if stream is None:
+            if not first.is_cuda or first.get_device() == torch.cuda.current_device():
+                return fn(first, *args, **kw)
+            with torch.cuda.device(first.device):
+                return fn(first, *args, **kw)
+        if first.is_cuda and stream.device != first.device:
+            raise ValueError(f"{fn.__name__}: stream of {stream.device}, tensors on "
+                             f"{first.device}")
+        with torch.cuda.stream(stream):
+            if not torch.cuda.is_current_stream_capturing():
+                for t in (first, *args, *kw.values()):
+                    if isinstance(t, torch.Tensor) and t.is_cuda:
+                        t.record_stream(stream)
+            return fn(first, *args, **kw)
+
+    return call
+
+
+def _raw_stream(t):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(fn, name, t, shape, dtypes, like=None):
+    """Checks one tensor: its shape, that its dtype is one of `dtypes`, that it
+    is dense, and that it is on like's device (its own, a GPU, without)."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not contiguous")
+    if like is None:
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: {name} is on {t.device}, expected a GPU")
+    elif t.device != like.device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, expected {like.device}")
+    return t
+
+
+def _types():
+    """(bf16 as torch has it or as its bits, bf16 or fp32, fp32, int32)."""
+    global _type_sets
+    if _type_sets is None:
+        import torch
+        _type_sets = ((torch.bfloat16, torch.int16), (torch.bfloat16, torch.int16, torch.float32),
+                      (torch.float32,), (torch.int32,))
+    return _type_sets
+
+
+_type_sets = None
+
+
+def _code(t):
+    """The ABI's dtype code of a row tensor."""
+    return MOE_OUT_F32 if t.element_size() == 4 else MOE_OUT_BF16
+
+
+def _out_rows(fn, name, t, shape, code, like):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=torch.float32 if code == MOE_OUT_F32 else torch.bfloat16,
+                           device=like.device)
+    bf, _, f32, _ = _types()
+    return _rows(fn, name, t, shape, f32 if code == MOE_OUT_F32 else bf, like)
+
+
+def _out_f32(fn, name, t, shape, like):
+    return _out_rows(fn, name, t, shape, MOE_OUT_F32, like)
+
+
+def _workspace(fn, ws, need, like):
+    import torch
+    if ws is None:
+        return torch.empty((need,), dtype=torch.uint8, device=like.device) if need else None
+    if not ws.is_contiguous() or ws.device != like.device:
+        raise ValueError(f"{fn}: ws must be contiguous and on {like.device}")
+    return ws
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def moe_linear_w4_ws_bytes(T, N, K):
+    return int(load_library().moe_linear_w4_ws_bytes(T, N, K))
+
+
+@_on_device
+def moe_linear_w4(x, codes, scales, bias=None, out=None, out_dtype=MOE_OUT_BF16, ws=None):
+    """x bf16 [T][K] times an int4 matrix -> [T][N] (bf16 or fp32).
+
+    codes u8 [N][K/2] and scales fp16 (or their bits) [N][K/128] as
+    moe_quantize_w4 returns them for one matrix (its leading axis of length 1
+    may stay); bias fp32 [N] or None.
+    """
+    import torch
+    fn = "moe_linear_w4"
+    bf, _, f32, _ = _types()
+    if x.dim() != 2 or codes.dim() not in (2, 3):
+        raise ValueError(f"{fn}: x must be [T][K] and codes [N][K/2]")
+    T, K = x.shape
+    N = codes.shape[-2]
+    lead = (1,) * (codes.dim() - 2)
+    _rows(fn, "x", x, (T, K), bf)
+    _rows(fn, "codes", codes, lead + (N, K // 2), (torch.uint8,), x)
+    _rows(fn, "scales", scales, (1,) * (scales.dim() - 2) + (N, K // MOE_GROUP),
+          (torch.int16, torch.float16), x)
+    if bias is not None:
+        _rows(fn, "bias", bias, (N,), f32, x)
+    out = _out_rows(fn, "out", out, (T, N), out_dtype, x)
+    lib = _lib or load_library()
+    ws = _workspace(fn, ws, lib.moe_linear_w4_ws_bytes(T, N, K), x)
+    rc = lib.moe_linear_w4(x.data_ptr(), T, N, K, MOE_GROUP, codes.data_ptr(), scales.data_ptr(),
+                           _addr(bias), out.data_ptr(), out_dtype, *_ws_args(ws), _raw_stream(x))
+    if rc:
+        _check(fn, rc)
+    return out
+
+
+@_on_device
+def moe_rmsnorm(x, gain=None, eps=1e-6, out=None, out_dtype=MOE_OUT_BF16):
+    """The norm in front of a block: x [T][d] (bf16 or fp32), gain fp32 [d]."""
+    fn = "moe_rmsnorm"
+    _, row, f32, _ = _types()
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: x must be [T][d]")
+    T, d = x.shape
+    _rows(fn, "x", x, (T, d), row)
+    if gain is not None:
+        _rows(fn, "gain", gain, (d,), f32, x)
+    out = _out_rows(fn, "out", out, (T, d), out_dtype, x)
+    rc = (_lib or load_library()).moe_rmsnorm(x.data_ptr(), _code(x), _addr(gain), T, d, eps,
+                                              out.data_ptr(), out_dtype, _raw_stream(x))
+    if rc:
+        _check(fn, rc)
+    return out
+
+
+@_on_device
+def moe_rmsnorm_bwd(dout, x, gain=None, eps=1e-6, dres=None, dx=None, dgain=None, ws=None):
+    """Gradient of moe_rmsnorm, plus dres (the gradient of x past the norm)
+    -> (dx in x's type, dgain fp32 [d]; None when there is no gain)."""
+    fn = "moe_rmsnorm_bwd"
+    _, row, f32, _ = _types()
+    if dout.dim() != 2:
+        raise ValueError(f"{fn}: dout must be [T][d]")
+    T, d = dout.shape
+    _rows(fn, "dout", dout, (T, d), row)
+    _rows(fn, "x", x, (T, d), row, dout)
+    if dres is not None:
+        _rows(fn, "dres", dres, (T, d), (x.dtype,), dout)
+    dx = _out_rows(fn, "dx", dx, (T, d), _code(x), dout)
+    if gain is not None:
+        _rows(fn, "gain", gain, (d,), f32, dout)
+        dgain = _out_f32(fn, "dgain", dgain, (d,), dout)
+    elif dgain is not None:
+        raise ValueError(f"{fn}: dgain without gain")
+    lib = _lib or load_library()
+    ws = _workspace(fn, ws, lib.moe_rmsnorm_bwd_ws_bytes(T, d) if dgain is not None else 0, dout)
+    rc = lib.moe_rmsnorm_bwd(dout.data_ptr(), _code(dout), x.data_ptr(), _code(x), _addr(gain),
+                             _addr(dres), T, d, eps, dx.data_ptr(), _addr(dgain), *_ws_args(ws),
+                             _raw_stream(dout))
+    if rc:
+        _check(fn, rc)
+    return dx, dgain
+
+
+def _block_inputs(fn, rows, y_pairs, pair_pos, topk_w, add, post_gain, gate, gate_mode):
+    """Checks the inputs that moe_combine_residual and its gradient share;
+    rows: the residual or its gradient.  Returns (T, d, k)."""
+    _, row, f32, i32 = _types()
+    if rows.dim() != 2:
+        raise ValueError(f"{fn}: the residual and its gradient must be [T][d]")
+    T, d = rows.shape
+    _rows(fn, "residual" if fn == "moe_combine_residual" else "dout", rows, (T, d), row)
+    k = 0
+    if y_pairs is not None:
+        if pair_pos is None or topk_w is None or topk_w.dim() != 2:
+            raise ValueError(f"{fn}: y_pairs needs pair_pos [T*k] and topk_w [T][k]")
+        k = topk_w.shape[1]
+        _rows(fn, "topk_w", topk_w, (T, k), f32, rows)
+        _rows(fn, "y_pairs", y_pairs, (T * k, d), f32, rows)
+        if pair_pos.numel() != T * k:
+            raise ValueError(f"{fn}: pair_pos has {pair_pos.numel()} entries, expected {T * k}")
+        _rows(fn, "pair_pos", pair_pos, tuple(pair_pos.shape), i32, rows)
+    elif pair_pos is not None or topk_w is not None:
+        raise ValueError(f"{fn}: pair_pos and topk_w without y_pairs")
+    if add is not None:
+        _rows(fn, "add", add, (T, d), (rows.dtype,), rows)
+    if post_gain is not None:
+        _rows(fn, "post_gain", post_gain, (d,), f32, rows)
+    if gate is not None:
+        shape = {MOE_GATE_TOKEN: (T,), MOE_GATE_CHANNEL: (d,)}.get(gate_mode)
+        if shape is None:
+            raise ValueError(f"{fn}: gate does not fit gate_mode {gate_mode}")
+        _rows(fn, "gate", gate, shape, f32, rows)
+    elif gate_mode != MOE_GATE_NONE:
+        raise ValueError(f"{fn}: gate_mode {gate_mode} needs a gate")
+    return T, d, k
+
+
+@_on_device
+def moe_combine_residual(residual, y_pairs=None, pair_pos=None, topk_w=None, add=None,
+                         post_gain=None, gate=None, gate_mode=MOE_GATE_NONE, res_scale=1.0,
+                         eps=1e-6, next_gain=None, out=None, next_out=None, next_norm=None):
+    """End of a block: combine (+ add), norm after the block (with post_gain),
+    gate, scaled residual and the next block's norm -> (out, next_out).
+
+    residual [T][d] (bf16 or fp32; add and out have its type); y_pairs,
+    pair_pos, topk_w as for moe_combine, or all None for a block whose output
+    is `add` alone; pairs with a pair_pos of -1 are dropped.  next_out (bf16)
+    is computed when next_gain or next_out is given or next_norm is true,
+    otherwise it is None.  out may be residual.
+    """
+    fn = "moe_combine_residual"
+    T, d, k = _block_inputs(fn, residual, y_pairs, pair_pos, topk_w, add, post_gain, gate,
+                            gate_mode)
+    code = _code(residual)
+    out = _out_rows(fn, "out", out, (T, d), code, residual)
+    if next_gain is not None:
+        _rows(fn, "next_gain", next_gain, (d,), _types()[2], residual)
+    if next_gain is not None or next_out is not None or next_norm:
+        next_out = _out_rows(fn, "next_out", next_out, (T, d), MOE_OUT_BF16, residual)
+    rc = (_lib or load_library()).moe_combine_residual(
+        residual.data_ptr(), code, _addr(y_pairs), _addr(pair_pos), _addr(topk_w), k, _addr(add),
+        _addr(post_gain), _addr(gate), gate_mode, res_scale, eps, _addr(next_gain), T, d,
+        out.data_ptr(), _addr(next_out), _raw_stream(residual))
+    if rc:
+        _check(fn, rc)
+    return out, next_out
+
+
+CombineResidualGrads = collections.namedtuple(
+    "CombineResidualGrads", "dy_pairs dtopk_w dadd dresidual dpost_gain dgate")
+
+
+@_on_device
+def moe_combine_residual_bwd(dout, y_pairs=None, pair_pos=None, topk_w=None, add=None,
+                             post_gain=None, gate=None, gate_mode=MOE_GATE_NONE, res_scale=1.0,
+                             eps=1e-6, dy_dtype=MOE_OUT_F32, dy_pairs=None, dtopk_w=None,
+                             dadd=None, dresidual=None, dpost_gain=None, dgate=None, ws=None):
+    """Gradient of moe_combine_residual's `out` against each of its inputs, as
+    a CombineResidualGrads (None for inputs that are absent).
+
+    dout [T][d] in the residual's type.  Rows of dy_pairs that no pair owns
+    are not written.  dresidual may be dout.
+    """
+    fn = "moe_combine_residual_bwd"
+    T, d, k = _block_inputs(fn, dout, y_pairs, pair_pos, topk_w, add, post_gain, gate, gate_mode)
+    code = _code(dout)
+    for name, g, given in (("dy_pairs", dy_pairs, y_pairs), ("dtopk_w", dtopk_w, topk_w),
+                           ("dadd", dadd, add), ("dpost_gain", dpost_gain, post_gain),
+                           ("dgate", dgate, gate)):
+        if g is not None and given is None:
+            raise ValueError(f"{fn}: {name} without its input")
+    if y_pairs is not None:
+        dy_pairs = _out_rows(fn, "dy_pairs", dy_pairs, (T * k, d), dy_dtype, dout)
+        dtopk_w = _out_f32(fn, "dtopk_w", dtopk_w, (T, k), dout)
+    if add is not None:
+        dadd = _out_rows(fn, "dadd", dadd, (T, d), code, dout)
+    dresidual = _out_rows(fn, "dresidual", dresidual, (T, d), code, dout)
+    if post_gain is not None:
+        dpost_gain = _out_f32(fn, "dpost_gain", dpost_gain, (d,), dout)
+    if gate is not None:
+        dgate = _out_f32(fn, "dgate", dgate, tuple(gate.shape), dout)
+    lib = _lib or load_library()
+    colsum = post_gain is not None or gate_mode == MOE_GATE_CHANNEL
+    ws = _workspace(fn, ws, lib.moe_combine_residual_bwd_ws_bytes(T, d) if colsum else 0, dout)
+    rc = lib.moe_combine_residual_bwd(
+        dout.data_ptr(), code, _addr(y_pairs), _addr(pair_pos), _addr(topk_w), k, _addr(add),
+        _addr(post_gain), _addr(gate), gate_mode, res_scale, eps, T, d, _addr(dy_pairs), dy_dtype,
+        _addr(dtopk_w), _addr(dadd), _addr(dresidual), _addr(dpost_gain), _addr(dgate),
+        *_ws_args(ws), _raw_stream(dout))
+    if rc:
+        _check(fn, rc)
+    return CombineResidualGrads(dy_pairs, dtopk_w, dadd, dresidual, dpost_gain, dgate)
+
+
+def _sort_inputs(fn, T, k, pair_pos, topk_w, like):
+    _, _, f32, i32 = _types()
+    if pair_pos.numel() != T * k:
+        raise ValueError(f"{fn}: pair_pos has {pair_pos.numel()} entries, expected {T * k}")
+    _rows(fn, "pair_pos", pair_pos, tuple(pair_pos.shape), i32, like)
+    if topk_w is not None:
+        _rows(fn, "topk_w", topk_w, (T, k), f32, like)
+
+
+@_on_device
+def moe_dispatch(x, pair_pos, k, topk_w=None, out=None):
+    """Tokens into expert order: row pair_pos[t*k+j] of the result [T*k][d] is
+    x[t] (times topk_w[t][j] when given), in x's type.  Rows that no pair owns
+    are not written."""
+    fn = "moe_dispatch"
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: x must be [T][d]")
+    T, d = x.shape
+    _rows(fn, "x", x, (T, d), _types()[1])
+    _sort_inputs(fn, T, k, pair_pos, topk_w, x)
+    out = _out_rows(fn, "out", out, (T * k, d), _code(x), x)
+    rc = (_lib or load_library()).moe_dispatch(
+        x.data_ptr(), _code(x), pair_pos.data_ptr(), _addr(topk_w), T, k, d, out.data_ptr(),
+        _raw_stream(x))
+    if rc:
+        _check(fn, rc)
+    return out
+
+
+@_on_device
+def moe_dispatch_bwd(dxs, pair_pos, k, x=None, topk_w=None, dx=None, dtopk_w=None):
+    """Gradient of moe_dispatch -> (dx [T][d] in dxs's type, dtopk_w [T][k]).
+    dtopk_w is computed when topk_w and x are given, otherwise it is None."""
+    fn = "moe_dispatch_bwd"
+    _, row, _, _ = _types()
+    if dxs.dim() != 2 or k < 1 or dxs.shape[0] % k:
+        raise ValueError(f"{fn}: dxs must be [T*k][d]")
+    T, d = dxs.shape[0] // k, dxs.shape[1]
+    _rows(fn, "dxs", dxs, (T * k, d), row)
+    _sort_inputs(fn, T, k, pair_pos, topk_w, dxs)
+    dx = _out_rows(fn, "dx", dx, (T, d), _code(dxs), dxs)
+    if x is not None:
+        _rows(fn, "x", x, (T, d), (dxs.dtype,), dxs)
+    if x is not None and topk_w is not None:
+        dtopk_w = _out_f32(fn, "dtopk_w", dtopk_w, (T, k), dxs)
+    elif dtopk_w is not None:
+        raise ValueError(f"{fn}: dtopk_w needs x and topk_w")
+    rc = (_lib or load_library()).moe_dispatch_bwd(
+        dxs.data_ptr(), _code(dxs), _addr(x), pair_pos.data_ptr(), _addr(topk_w), T, k, d,
+        dx.data_ptr(), _addr(dtopk_w), _raw_stream(dxs))
+    if rc:
+        _check(fn, rc)
+    return dx, dtopk_w
+
+
+@_on_device
+def moe_combine_bwd(dout, y_pairs, pair_pos, topk_w, dy_dtype=MOE_OUT_F32, dy_pairs=None,
+                    dtopk_w=None):
+    """Gradient of moe_combine for dout [T][d] (bf16 or fp32) -> (dy_pairs
+    [T*k][d] of dy_dtype, dtopk_w fp32 [T][k]).  Rows of dy_pairs that no pair
+    owns are not written."""
+    fn = "moe_combine_bwd"
+    _, row, f32, _ = _types()
+    if dout.dim() != 2 or topk_w.dim() != 2:
+        raise ValueError(f"{fn}: dout must be [T][d] and topk_w [T][k]")
+    T, d = dout.shape
+    k = topk_w.shape[1]
+    _rows(fn, "dout", dout, (T, d), row)
+    _rows(fn, "y_pairs", y_pairs, (T * k, d), f32, dout)
+    _sort_inputs(fn, T, k, pair_pos, topk_w, dout)
+    dy_pairs = _out_rows(fn, "dy_pairs", dy_pairs, (T * k, d), dy_dtype, dout)
+    dtopk_w = _out_f32(fn, "dtopk_w", dtopk_w, (T, k), dout)
+    rc = (_lib or load_library()).moe_combine_bwd(
+        dout.data_ptr(), _code(dout), y_pairs.data_ptr(), pair_pos.data_ptr(), topk_w.data_ptr(),
+        T, k, d, dy_pairs.data_ptr(), dy_dtype, dtopk_w.data_ptr(), _raw_stream(dout))
+    if rc:
+        _check(fn, rc)
+    return dy_pairs, dtopk_w
 
 
 # ------------------------------------------------------ expert slot cache

@@ -491,3 +491,242 @@ int moe_allocate_bits(const double* dist, const int32_t* counts, int E, int d, i
                     "moe_allocate_bits");
 }
 
+// ------------------------------------------ around the routed experts
+
+static bool known_dtype(int t) { return t == MOE_OUT_BF16 || t == MOE_OUT_F32; }
+
+// Checks common to the row kernels (k = 0 where there are no pairs).
+static int row_check(const char* what, int T, int d, int k, int kmin, int dtype1, int dtype2) {
+  if (T < 0 || d <= 0 || k < kmin)
+    return fail(MOE_ERR_INVALID_ARG, "%s: bad size (T=%d d=%d k=%d)", what, T, d, k);
+  if (!known_dtype(dtype1) || !known_dtype(dtype2))
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype", what);
+  if (d % 8) return fail(MOE_ERR_UNSUPPORTED, "%s: d=%d not a multiple of 8", what, d);
+  if (d > MOE_MAX_D) return fail(MOE_ERR_UNSUPPORTED, "%s: d=%d > %d", what, d, MOE_MAX_D);
+  if (k > MOE_MAX_TOPK)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: k=%d > %d", what, k, MOE_MAX_TOPK);
+  if ((long long)T * k >= (1LL << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: T*k must be below 2^31", what);
+  return MOE_OK;
+}
+
+static int eps_check(const char* what, float eps) {
+  if (!(eps > 0.0f) || !(eps <= 3.4028235e38f))
+    return fail(MOE_ERR_INVALID_ARG, "%s: eps must be positive and finite", what);
+  return MOE_OK;
+}
+
+// Workspace of the column sums, needed when one of them is wanted.
+static int colsum_ws_check(const char* what, bool wanted, size_t need, const void* ws,
+                           size_t ws_bytes) {
+  if (!wanted || need == 0) return MOE_OK;
+  if (!ws || ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", what,
+                ws ? ws_bytes : (size_t)0, need);
+  if (!aligned(ws, 16)) return fail(MOE_ERR_INVALID_ARG, "%s: misaligned workspace", what);
+  return MOE_OK;
+}
+
+size_t moe_linear_w4_ws_bytes(int T, int N, int K) {
+  if (T < 0 || N <= 0 || K <= 0) return 0;
+  return moe::linear_w4_ws_bytes(T, N, K);
+}
+
+int moe_linear_w4(const void* x_bf16, int T, int N, int K, int group_size, const uint8_t* codes,
+                  const uint16_t* scales_f16, const float* bias, void* out, int out_dtype,
+                  void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0 || N <= 0 || K <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: bad size (T=%d N=%d K=%d)", T, N, K);
+  if (!known_dtype(out_dtype))
+    return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: unknown out_dtype %d", out_dtype);
+  if (group_size != MOE_GROUP)
+    return fail(MOE_ERR_UNSUPPORTED, "group_size=%d (only 128)", group_size);
+  if (K % MOE_GROUP) return fail(MOE_ERR_UNSUPPORTED, "K=%d not a multiple of 128", K);
+  if (N % 16) return fail(MOE_ERR_UNSUPPORTED, "N=%d not a multiple of 16", N);
+  if ((long long)T * K >= (1LL << 40) || (long long)T * N >= (1LL << 40))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_linear_w4: T*K and T*N must be below 2^40");
+  if (T == 0) return ok();
+  if (!x_bf16 || !codes || !scales_f16 || !out)
+    return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: null pointer");
+  if (!aligned(x_bf16, 16) || !aligned(codes, 16) || !aligned(scales_f16, 4) ||
+      !aligned(out, 16) || !aligned(bias, 4))
+    return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: misaligned pointer");
+  const size_t need = moe::linear_w4_ws_bytes(T, N, K);
+  if (need && (!ws || ws_bytes < need))
+    return fail(MOE_ERR_WORKSPACE, "moe_linear_w4: workspace %zu < %zu bytes",
+                ws ? ws_bytes : (size_t)0, need);
+  if (need && !aligned(ws, 256))
+    return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: workspace not 256-byte aligned");
+  return hip_status(moe::launch_linear_w4((const uint16_t*)x_bf16, codes, scales_f16, bias, T, N,
+                                          K, out, out_dtype == MOE_OUT_F32, ws,
+                                          (hipStream_t)stream),
+                    "moe_linear_w4");
+}
+
+int moe_rmsnorm(const void* x, int x_dtype, const float* gain, int T, int d, float eps, void* out,
+                int out_dtype, void* stream) {
+  int rc = row_check("moe_rmsnorm", T, d, 0, 0, x_dtype, out_dtype);
+  if (!rc) rc = eps_check("moe_rmsnorm", eps);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if (!x || !out) return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: null pointer");
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(gain, 16))
+    return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: misaligned pointer");
+  return hip_status(moe::launch_rmsnorm(x, x_dtype == MOE_OUT_F32, gain, T, d, eps, out,
+                                        out_dtype == MOE_OUT_F32, (hipStream_t)stream),
+                    "moe_rmsnorm");
+}
+
+size_t moe_rmsnorm_bwd_ws_bytes(int T, int d) {
+  if (T < 0 || d <= 0) return 0;
+  return moe::rmsnorm_bwd_ws_bytes(T, d);
+}
+
+int moe_rmsnorm_bwd(const void* dout, int dout_dtype, const void* x, int x_dtype,
+                    const float* gain, const void* dres, int T, int d, float eps, void* dx,
+                    float* dgain, void* ws, size_t ws_bytes, void* stream) {
+  const char* what = "moe_rmsnorm_bwd";
+  int rc = row_check(what, T, d, 0, 0, dout_dtype, x_dtype);
+  if (!rc) rc = eps_check(what, eps);
+  if (!rc) rc = colsum_ws_check(what, dgain, moe_rmsnorm_bwd_ws_bytes(T, d), ws, ws_bytes);
+  if (rc) return rc;
+  if (T > 0 && (!dout || !x || !dx)) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(dout, 16) || !aligned(x, 16) || !aligned(dres, 16) || !aligned(dx, 16) ||
+      !aligned(gain, 16) || !aligned(dgain, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  if (T == 0 && !dgain) return ok();
+  return hip_status(moe::launch_rmsnorm_bwd(dout, dout_dtype == MOE_OUT_F32, x,
+                                            x_dtype == MOE_OUT_F32, gain, dres, T, d, eps, dx,
+                                            dgain, ws, (hipStream_t)stream),
+                    what);
+}
+
+// Checks shared by moe_combine_residual and its gradient.
+static int block_out_check(const char* what, const moe::BlockOutArgs& a, int dtype, int dtype2) {
+  int rc = row_check(what, a.T, a.d, a.k, 0, dtype, dtype2);
+  if (!rc) rc = eps_check(what, a.eps);
+  if (rc) return rc;
+  if (!(a.res_scale >= -3.4028235e38f && a.res_scale <= 3.4028235e38f))
+    return fail(MOE_ERR_INVALID_ARG, "%s: res_scale must be finite", what);
+  if (a.gate_mode < MOE_GATE_NONE || a.gate_mode > MOE_GATE_CHANNEL)
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown gate_mode %d", what, a.gate_mode);
+  if (a.gate_mode == MOE_GATE_NONE ? a.gate != nullptr
+                                   : !a.gate && (a.T > 0 || a.gate_mode == MOE_GATE_CHANNEL))
+    return fail(MOE_ERR_INVALID_ARG, "%s: gate does not fit gate_mode", what);
+  if (a.k == 0 && (a.y || a.pair_pos || a.topk_w))
+    return fail(MOE_ERR_INVALID_ARG, "%s: pairs given with k = 0", what);
+  if (a.T > 0 && a.k > 0 && (!a.y || !a.pair_pos || !a.topk_w))
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (a.T > 0 && a.k == 0 && !a.add)
+    return fail(MOE_ERR_INVALID_ARG, "%s: neither pairs nor add", what);
+  if (!aligned(a.y, 16) || !aligned(a.pair_pos, 4) || !aligned(a.topk_w, 4) ||
+      !aligned(a.add, 16) || !aligned(a.post_gain, 16) ||
+      !aligned(a.gate, a.gate_mode == MOE_GATE_CHANNEL ? 16 : 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  return MOE_OK;
+}
+
+int moe_combine_residual(const void* residual, int dtype, const float* y_pairs,
+                         const int32_t* pair_pos, const float* topk_w, int k, const void* add,
+                         const float* post_gain, const float* gate, int gate_mode,
+                         float res_scale, float eps, const float* next_gain, int T, int d,
+                         void* out, void* next_out_bf16, void* stream) {
+  const char* what = "moe_combine_residual";
+  const moe::BlockOutArgs a{y_pairs, pair_pos, topk_w,    k,   add, post_gain, gate,
+                            gate_mode, res_scale, eps, T, d, dtype == MOE_OUT_F32};
+  int rc = block_out_check(what, a, dtype, dtype);
+  if (rc) return rc;
+  if (next_gain && !next_out_bf16 && T > 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: next_gain without next_out", what);
+  if (T == 0) return ok();
+  if (!residual || !out) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(residual, 16) || !aligned(out, 16) || !aligned(next_out_bf16, 16) ||
+      !aligned(next_gain, 16))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  return hip_status(moe::launch_combine_residual(a, residual, next_gain, out, next_out_bf16,
+                                                 (hipStream_t)stream),
+                    what);
+}
+
+size_t moe_combine_residual_bwd_ws_bytes(int T, int d) {
+  if (T < 0 || d <= 0) return 0;
+  return moe::combine_residual_bwd_ws_bytes(T, d);
+}
+
+int moe_combine_residual_bwd(const void* dout, int dtype, const float* y_pairs,
+                             const int32_t* pair_pos, const float* topk_w, int k,
+                             const void* add, const float* post_gain, const float* gate,
+                             int gate_mode, float res_scale, float eps, int T, int d,
+                             void* dy_pairs, int dy_dtype, float* dtopk_w, void* dadd,
+                             void* dresidual, float* dpost_gain, float* dgate, void* ws,
+                             size_t ws_bytes, void* stream) {
+  const char* what = "moe_combine_residual_bwd";
+  const moe::BlockOutArgs a{y_pairs, pair_pos, topk_w,    k,   add, post_gain, gate,
+                            gate_mode, res_scale, eps, T, d, dtype == MOE_OUT_F32};
+  int rc = block_out_check(what, a, dtype, dy_dtype);
+  const bool colsum = dpost_gain || (dgate && gate_mode == MOE_GATE_CHANNEL);
+  if (!rc)
+    rc = colsum_ws_check(what, colsum, moe_combine_residual_bwd_ws_bytes(T, d), ws, ws_bytes);
+  if (rc) return rc;
+  if ((dgate && gate_mode == MOE_GATE_NONE) || (dpost_gain && !post_gain) || (dadd && !add) ||
+      (k == 0 && (dy_pairs || dtopk_w)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: gradient of an absent input", what);
+  if (T > 0 && !dout) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(dout, 16) || !aligned(dy_pairs, 16) || !aligned(dtopk_w, 4) ||
+      !aligned(dadd, 16) || !aligned(dresidual, 16) || !aligned(dpost_gain, 4) ||
+      !aligned(dgate, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  if (T == 0 && !colsum) return ok();
+  return hip_status(moe::launch_combine_residual_bwd(a, dout, dy_pairs, dy_dtype == MOE_OUT_F32,
+                                                     dtopk_w, dadd, dresidual, dpost_gain, dgate,
+                                                     ws, (hipStream_t)stream),
+                    what);
+}
+
+int moe_dispatch(const void* x, int dtype, const int32_t* pair_pos, const float* topk_w, int T,
+                 int k, int d, void* xs, void* stream) {
+  int rc = row_check("moe_dispatch", T, d, k, 1, dtype, dtype);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if (!x || !pair_pos || !xs) return fail(MOE_ERR_INVALID_ARG, "moe_dispatch: null pointer");
+  if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(pair_pos, 4) || !aligned(topk_w, 4))
+    return fail(MOE_ERR_INVALID_ARG, "moe_dispatch: misaligned pointer");
+  return hip_status(moe::launch_dispatch(x, dtype == MOE_OUT_F32, pair_pos, topk_w, T, k, d, xs,
+                                         (hipStream_t)stream),
+                    "moe_dispatch");
+}
+
+int moe_dispatch_bwd(const void* dxs, int dtype, const void* x, const int32_t* pair_pos,
+                     const float* topk_w, int T, int k, int d, void* dx, float* dtopk_w,
+                     void* stream) {
+  const char* what = "moe_dispatch_bwd";
+  int rc = row_check(what, T, d, k, 1, dtype, dtype);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if (!dxs || !pair_pos || !dx || (dtopk_w && (!x || !topk_w)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(dxs, 16) || !aligned(x, 16) || !aligned(dx, 16) || !aligned(pair_pos, 4) ||
+      !aligned(topk_w, 4) || !aligned(dtopk_w, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  return hip_status(moe::launch_dispatch_bwd(dxs, dtype == MOE_OUT_F32, x, pair_pos, topk_w, T,
+                                             k, d, dx, dtopk_w, (hipStream_t)stream),
+                    what);
+}
+
+int moe_combine_bwd(const void* dout, int dout_dtype, const float* y_pairs,
+                    const int32_t* pair_pos, const float* topk_w, int T, int k, int d,
+                    void* dy_pairs, int dy_dtype, float* dtopk_w, void* stream) {
+  const char* what = "moe_combine_bwd";
+  int rc = row_check(what, T, d, k, 1, dout_dtype, dy_dtype);
+  if (rc) return rc;
+  if (T == 0 || (!dy_pairs && !dtopk_w)) return ok();
+  if (!dout || !pair_pos || (dtopk_w && !y_pairs) || (dy_pairs && !topk_w))
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(dout, 16) || !aligned(y_pairs, 16) || !aligned(dy_pairs, 16) ||
+      !aligned(pair_pos, 4) || !aligned(topk_w, 4) || !aligned(dtopk_w, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  return hip_status(moe::launch_combine_bwd(dout, dout_dtype == MOE_OUT_F32, y_pairs, pair_pos,
+                                            topk_w, T, k, d, dy_pairs, dy_dtype == MOE_OUT_F32,
+                                            dtopk_w, (hipStream_t)stream),
+                    what);
+}

@@ -47,21 +47,6 @@ struct TokBlocks {
   static constexpr int value = N;
 };
 
-// One code word (elements 8j..8j+7, element 2i in nibble i, 2i+1 in
-// nibble 4+i) -> eight bf16 in element order: nibble c goes to mantissa
-// bits 3..6 and is XORed into D there.  D = 0x4340 (192.0): two's
-// complement codes q -> 192 + 8 q.  D = 0x4300 (128.0): unsigned nibbles
-// c -> 128 + 8 c; D = 0x4500 (2048.0): 16 (128 + 8 c).
-__device__ __forceinline__ bf16x8 w4_top(uint32_t w, uint32_t D) {
-  const uint32_t B = 0x00780078u;
-  u32x4 r;
-  r[0] = __builtin_amdgcn_bitop3_b32(w << 3, B, D, 0x6A);
-  r[1] = __builtin_amdgcn_bitop3_b32(w >> 1, B, D, 0x6A);
-  r[2] = __builtin_amdgcn_bitop3_b32(w >> 5, B, D, 0x6A);
-  r[3] = __builtin_amdgcn_bitop3_b32(w >> 9, B, D, 0x6A);
-  return __builtin_bit_cast(bf16x8, r);
-}
-
 // ---------------------------------------------------------------- pre-pass
 // For row r (token t of x, or grouped slot of h) and group g: s = fp32 sum
 // of the 128 bf16 elements, split exactly into three bf16 parts

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace moe {
 
 // Launch a kernel; when start/stop events are given they are attached to the
@@ -21,6 +23,14 @@ inline void launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t lds
     hipLaunchKernelGGL(kernel, grid, block, lds, s, args...);
 }
 
+// Calls f with two truth values as types (std::true_type / false_type).
+template <typename F>
+inline void with_bools(bool a, bool b, F&& f) {
+  if (a)
+    b ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+  else
+    b ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
+}
 
 size_t route_ws_bytes(int T, int E);
 hipError_t launch_route(const void* x, const void* wr, const float* bias,
@@ -127,6 +137,57 @@ hipError_t launch_cache_remap(const int32_t* topk_idx, int P, int E, const int32
 hipError_t launch_combine(const float* y, const int32_t* pair_pos,
                           const float* topk_w, int T, int k, int d, void* out,
                           int out_f32, hipStream_t s);
+
+// Norm in front of a block and its gradient (norm.hip).
+hipError_t launch_rmsnorm(const void* x, int x_f32, const float* gain, int T, int d, float eps,
+                          void* out, int out_f32, hipStream_t s);
+size_t rmsnorm_bwd_ws_bytes(int T, int d);
+hipError_t launch_rmsnorm_bwd(const void* dout, int do_f32, const void* x, int x_f32,
+                              const float* gain, const void* dres, int T, int d, float eps,
+                              void* dx, float* dgain, void* ws, hipStream_t s);
+// Column sums S of n rows of partial sums: out1 = S f1, out2 = S f2 (norm.hip).
+hipError_t launch_colsum(const float* rows, int n, int d, float* out1, const float* f1,
+                         float* out2, const float* f2, hipStream_t s);
+
+// End of a block: combine, post norm, gate, residual, next norm
+// (block_out.hip).
+struct BlockOutArgs {
+  const float* y;  // [T*k][d] (k > 0)
+  const int32_t* pair_pos;
+  const float* topk_w;
+  int k;
+  const void* add;  // [T][d] or null
+  const float* post_gain;
+  const float* gate;
+  int gate_mode;
+  float res_scale, eps;
+  int T, d, f32;  // f32: residual, add and their gradients are fp32
+};
+hipError_t launch_combine_residual(const BlockOutArgs& a, const void* residual,
+                                   const float* next_gain, void* out, void* next_out,
+                                   hipStream_t s);
+size_t combine_residual_bwd_ws_bytes(int T, int d);
+hipError_t launch_combine_residual_bwd(const BlockOutArgs& a, const void* dout, void* dy,
+                                       int dy_f32, float* dtopk_w, void* dadd, void* dresidual,
+                                       float* dpost_gain, float* dgate, void* ws,
+                                       hipStream_t s);
+
+// Tokens into expert order and the gradients of the sort and of the combine
+// (sort.hip).  topk_w null: weights 1.
+hipError_t launch_dispatch(const void* x, int f32, const int32_t* pair_pos, const float* topk_w,
+                           int T, int k, int d, void* xs, hipStream_t s);
+hipError_t launch_dispatch_bwd(const void* dxs, int f32, const void* x, const int32_t* pair_pos,
+                               const float* topk_w, int T, int k, int d, void* dx,
+                               float* dtopk_w, hipStream_t s);
+hipError_t launch_combine_bwd(const void* dout, int do_f32, const float* y,
+                              const int32_t* pair_pos, const float* topk_w, int T, int k, int d,
+                              void* dy, int dy_f32, float* dtopk_w, hipStream_t s);
+
+// Linear map with int4 weights (linear.hip).
+size_t linear_w4_ws_bytes(int T, int N, int K);
+hipError_t launch_linear_w4(const uint16_t* x, const uint8_t* codes, const uint16_t* scales,
+                            const float* bias, int T, int N, int K, void* out, int out_f32,
+                            void* ws, hipStream_t s);
 
 // Canonical -> streaming code layouts (retile.hip).
 hipError_t launch_retile_w4(const uint8_t* canon, long long R, int K, uint8_t* tiled,

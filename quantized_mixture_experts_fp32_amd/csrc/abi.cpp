@@ -543,13 +543,14 @@ int moe_linear_w4(const void* x_bf16, int T, int N, int K, int group_size, const
     return fail(MOE_ERR_UNSUPPORTED, "group_size=%d (only 128)", group_size);
   if (K % MOE_GROUP) return fail(MOE_ERR_UNSUPPORTED, "K=%d not a multiple of 128", K);
   if (N % 16) return fail(MOE_ERR_UNSUPPORTED, "N=%d not a multiple of 16", N);
+  if (K >= 1 << 20) return fail(MOE_ERR_UNSUPPORTED, "K=%d not below 2^20", K);
   if ((long long)T * K >= (1LL << 40) || (long long)T * N >= (1LL << 40))
     return fail(MOE_ERR_UNSUPPORTED, "moe_linear_w4: T*K and T*N must be below 2^40");
   if (T == 0) return ok();
   if (!x_bf16 || !codes || !scales_f16 || !out)
     return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: null pointer");
   if (!aligned(x_bf16, 16) || !aligned(codes, 16) || !aligned(scales_f16, 4) ||
-      !aligned(out, 16) || !aligned(bias, 4))
+      !aligned(out, 16) || !aligned(bias, 16))
     return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: misaligned pointer");
   const size_t need = moe::linear_w4_ws_bytes(T, N, K);
   if (need && (!ws || ws_bytes < need))

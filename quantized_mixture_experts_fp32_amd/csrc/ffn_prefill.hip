@@ -112,7 +112,9 @@ __device__ __forceinline__ void staged_barrier() {
 // Staged tile: row t (256 bytes) holds the token's 128 activations as
 // 16-byte chunks, chunk c at position c ^ (t & 15), so that the 32 rows a
 // fragment read touches fall on distinct banks.
-template <bool kGateUp>
+enum PfMode { kPfDown, kPfGateUp, kPfDenseF32, kPfDenseBf16 };
+
+template <PfMode kMode>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kPfWaves, kPfWaves)))
 void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K]
                   const int32_t* __restrict__ sorted_pair,  // gate/up: gather
@@ -124,7 +126,10 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
                   int nfb,                                  // feature blocks per tile
                   uint16_t* __restrict__ h_out,             // gate/up: [P][N]
                   float* __restrict__ y_out,                // down:    [P][N]
-                  uint2* __restrict__ hsum_out) {           // gate/up: [P][N/128]
+                  uint2* __restrict__ hsum_out,             // gate/up: [P][N/128]
+                  int T, const float* __restrict__ bias, void* __restrict__ dense_out) {
+  constexpr bool kGateUp = kMode == kPfGateUp;
+  constexpr bool kDense = kMode == kPfDenseF32 || kMode == kPfDenseBf16;
   // two staging buffers as distinct objects, so that reads of one are not
   // ordered behind the in-flight direct-to-LDS loads of the other
   __shared__ __attribute__((aligned(16))) uint8_t abuf0[kBufB];
@@ -136,10 +141,14 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
   // linear id, so XCD c runs tiles c, c + 8, ...; within an XCD all nfb
   // feature blocks of a tile are consecutive and run together, and the
   // tile's gathered activation rows are fetched into that XCD's L2 once.
+  // Dense: the (tile, feature block) pairs are cut into eight equal runs, one
+  // an XCD.
   const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
-  const int tile = (local / nfb) * 8 + xcd, fblk = local % nfb;
-  if (tile >= *num_tiles) return;
-  const PTile tl = tiles[tile];
+  const int pair = xcd * (gridDim.x >> 3) + local;
+  const int tile = kDense ? pair / nfb : (local / nfb) * 8 + xcd;
+  const int fblk = kDense ? pair % nfb : local % nfb;
+  if (kDense ? tile * kBT >= T : tile >= *num_tiles) return;
+  const PTile tl = kDense ? PTile{0, tile * kBT, min(kBT, T - tile * kBT), 8} : tiles[tile];
   const int G = K >> 7;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int c32 = lane & 31, hh = lane >> 5;
@@ -154,11 +163,13 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
     brow[1] = N + n;
     bstore[0] = bstore[1] = true;
   } else {
+    // down: N is a multiple of 128, so a B block is stored whole or not at
+    // all; dense: N may end inside one
     const int n0 = fblk * 256 + wave * 64;
-    bstore[0] = n0 < N;
-    bstore[1] = n0 + 32 < N;
-    brow[0] = bstore[0] ? n0 + c32 : c32;
-    brow[1] = bstore[1] ? n0 + 32 + c32 : c32;
+    bstore[0] = (kDense ? n0 + c32 : n0) < N;
+    bstore[1] = (kDense ? n0 + 32 + c32 : n0 + 32) < N;
+    brow[0] = bstore[0] ? n0 + c32 : kDense ? 0 : c32;
+    brow[1] = bstore[1] ? n0 + 32 + c32 : kDense ? 0 : c32;
   }
   const uint8_t* cb[2];
   const uint16_t* sb[2];
@@ -358,6 +369,18 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
           h_out[slot * N + brow[0]] = hb;
           hst[tok * 128 + 8 * ((lf >> 3) ^ (tok & 15)) + (lf & 7)] = hb;
         } else {
+          if (kDense) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              if (!bstore[m]) continue;
+              const float v = bias ? acc[t][m][i] + bias[brow[m]] : acc[t][m][i];
+              if (kMode == kPfDenseF32)
+                ((float*)dense_out)[slot * N + brow[m]] = v;
+              else
+                ((uint16_t*)dense_out)[slot * N + brow[m]] = (uint16_t)f32_to_bf16_rne(v);
+            }
+            continue;
+          }
           // y rows are read once, by the combine: streamed past the caches
           if (bstore[0]) __builtin_nontemporal_store(acc[t][0][i], y_out + slot * N + brow[0]);
           if (bstore[1]) __builtin_nontemporal_store(acc[t][1][i], y_out + slot * N + brow[1]);
@@ -1027,14 +1050,32 @@ hipError_t launch_ffn_prefill_w4(const FfnArgs& a, uint16_t* h, void* ws, hipStr
   }
   const unsigned mt8 = (unsigned)((mt + 7) & ~(size_t)7);
   // gate/up writes h and its group sums (the down pass's offset terms)
-  launch_k(pf_w4_kernel<true>, dim3(mt8 * (a.f / 128)), dim3(kThreads), 0, s, a.ev[0], a.ev[1],
+  launch_k(pf_w4_kernel<kPfGateUp>, dim3(mt8 * (a.f / 128)), dim3(kThreads), 0, s, a.ev[0], a.ev[1],
            a.x, a.sorted_pair, a.k, a.d, a.f, a.gu_codes, a.gu_scales, xsum,
-           (const PTile*)tiles, (const int*)num_tiles, a.f / 128, h, (float*)nullptr, hsum);
+           (const PTile*)tiles, (const int*)num_tiles, a.f / 128, h, (float*)nullptr, hsum, 0, (const float*)nullptr, (void*)nullptr);
   const int dn_fb = (a.d + 255) / 256;
-  launch_k(pf_w4_kernel<false>, dim3(mt8 * dn_fb), dim3(kThreads), 0, s, a.ev[2], a.ev[3],
+  launch_k(pf_w4_kernel<kPfDown>, dim3(mt8 * dn_fb), dim3(kThreads), 0, s, a.ev[2], a.ev[3],
            (const uint16_t*)h, a.sorted_pair, a.k, a.f, a.d, a.dn_codes, a.dn_scales,
            (const uint2*)hsum, (const PTile*)tiles, (const int*)num_tiles, dn_fb,
-           (uint16_t*)nullptr, a.y, (uint2*)nullptr);
+           (uint16_t*)nullptr, a.y, (uint2*)nullptr, 0, (const float*)nullptr, (void*)nullptr);
+  return hipGetLastError();
+}
+
+size_t linear_w4_gemm_ws_bytes(int T, int K) { return (size_t)T * (K / 128) * sizeof(uint2); }
+
+hipError_t launch_linear_w4_gemm(const uint16_t* x, const uint8_t* codes, const uint16_t* scales,
+                                 const float* bias, int T, int N, int K, void* out, int out_f32,
+                                 void* ws, hipStream_t s) {
+  uint2* xsum = (uint2*)ws;
+  const long long n = (long long)T * (K / 128);
+  hipLaunchKernelGGL(group_sums, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, x,
+                     (long long)T, K, xsum);
+  const int nfb = (N + 255) / 256, pairs = (T + kBT - 1) / kBT * nfb;
+  auto kern = out_f32 ? pf_w4_kernel<kPfDenseF32> : pf_w4_kernel<kPfDenseBf16>;
+  hipLaunchKernelGGL(kern, dim3((pairs + 7) & ~7), dim3(kThreads), 0, s, x,
+                     (const int32_t*)nullptr, 1, K, N, codes, scales, (const uint2*)xsum,
+                     (const PTile*)nullptr, (const int*)nullptr, nfb, (uint16_t*)nullptr,
+                     (float*)nullptr, (uint2*)nullptr, T, bias, out);
   return hipGetLastError();
 }
 

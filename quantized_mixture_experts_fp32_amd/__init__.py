@@ -517,18 +517,17 @@ def _addr(t):
 def _rows(fn, name, t, shape, dtypes, like=None):
     """Checks one tensor: its shape, that its dtype is one of `dtypes`, that it
     is dense, and that it is on like's device (its own, a GPU, without)."""
-    if tuple(t.shape) != shape:
+    if (t.shape == shape and t.dtype in dtypes and t.is_contiguous()
+            and (t.is_cuda if like is None else t.device == like.device)):
+        return t
+    if t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
     if t.dtype not in dtypes:
         raise ValueError(f"{fn}: {name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not contiguous")
-    if like is None:
-        if not t.is_cuda:
-            raise ValueError(f"{fn}: {name} is on {t.device}, expected a GPU")
-    elif t.device != like.device:
-        raise ValueError(f"{fn}: {name} is on {t.device}, expected {like.device}")
-    return t
+    raise ValueError(f"{fn}: {name} is on {t.device}, expected "
+                     f"{'a GPU' if like is None else like.device}")
 
 
 def _types():
@@ -552,8 +551,8 @@ def _code(t):
 def _out_rows(fn, name, t, shape, code, like):
     import torch
     if t is None:
-        return torch.empty(shape, dtype=torch.float32 if code == MOE_OUT_F32 else torch.bfloat16,
-                           device=like.device)
+        return like.new_empty(shape, dtype=torch.float32 if code == MOE_OUT_F32
+                              else torch.bfloat16)
     bf, _, f32, _ = _types()
     return _rows(fn, name, t, shape, f32 if code == MOE_OUT_F32 else bf, like)
 
@@ -603,7 +602,8 @@ def moe_linear_w4(x, codes, scales, bias=None, out=None, out_dtype=MOE_OUT_BF16,
         _rows(fn, "bias", bias, (N,), f32, x)
     out = _out_rows(fn, "out", out, (T, N), out_dtype, x)
     lib = _lib or load_library()
-    ws = _workspace(fn, ws, lib.moe_linear_w4_ws_bytes(T, N, K), x)
+    if T > 64 or ws is not None:  # the query is 0 up to 64 tokens
+        ws = _workspace(fn, ws, lib.moe_linear_w4_ws_bytes(T, N, K), x)
     rc = lib.moe_linear_w4(x.data_ptr(), T, N, K, MOE_GROUP, codes.data_ptr(), scales.data_ptr(),
                            _addr(bias), out.data_ptr(), out_dtype, *_ws_args(ws), _raw_stream(x))
     if rc:

@@ -27,42 +27,38 @@ namespace moe {
 namespace {
 using namespace row;
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+// Blocks of the backward pass: each takes every kBwdBlocks-th row and keeps
+// its share of the column sums in registers.
 constexpr int kBwdBlocks = 512;
 
-// The pairs of one token: KM >= k of them, dropped and missing ones with
-// weight 0 and slot -1.
-template <int KM>
-struct Pairs {
-  int slot[KM > 0 ? KM : 1];
-  float w[KM > 0 ? KM : 1];
-  __device__ __forceinline__ void load(const BlockOutArgs& a, int t) {
-    const int P = a.T * a.k;
-#pragma unroll
-    for (int j = 0; j < KM; ++j) {
-      slot[j] = -1;
-      w[j] = 0.0f;
-      if (j < a.k) {
-        const int s = a.pair_pos[(size_t)t * a.k + j];
-        if ((unsigned)s < (unsigned)P) {
-          slot[j] = s;
-          w[j] = a.topk_w[(size_t)t * a.k + j];
-        }
-      }
-    }
-  }
-};
-
-template <bool kF32, int KM, int NC>
+template <bool kF32, int KM, int NC, int kThreads>
 __global__ __launch_bounds__(kThreads) void combine_residual_kernel(
     BlockOutArgs a, const void* residual, const float* __restrict__ next_gain, void* out,
     void* __restrict__ next_out) {
+  constexpr int kWaves = kThreads / kWave;
+  // few rows (wide blocks): what does not depend on the routing is asked for
+  // before it, in registers that a full batch needs for occupancy
+  constexpr bool kAhead = kThreads == 512;
   __shared__ float red[2][kWaves];
   const int t = blockIdx.x, nch = a.d >> 3;
   const size_t base = (size_t)t * a.d;
+  f32x8 res[NC], fac[NC], nxt[NC];
+  auto ask = [&](int i) {
+    const int c = threadIdx.x + kThreads * i;
+    fac[i] = 1.0f;
+    nxt[i] = 1.0f;
+    if (c >= nch) return;
+    res[i] = load8<kF32>(residual, base + 8 * c);
+    if (a.post_gain) fac[i] = load8<true>(a.post_gain, 8 * c);
+    if (a.gate_mode == MOE_GATE_CHANNEL) fac[i] *= load8<true>(a.gate, 8 * c);
+    if (kAhead && next_gain) nxt[i] = load8<true>(next_gain, 8 * c);
+  };
   Pairs<KM> pr;
-  pr.load(a, t);
+  pr.load(a.pair_pos, a.topk_w, a.T * a.k, a.k, t);
+  if (kAhead) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) ask(i);
+  }
   f32x8 o[NC];
   float s[1] = {0.0f};
 #pragma unroll
@@ -70,9 +66,17 @@ __global__ __launch_bounds__(kThreads) void combine_residual_kernel(
     const int c = threadIdx.x + kThreads * i;
     o[i] = 0.0f;
     if (c < nch) {
+      constexpr int kBatch = KM < 8 ? (KM ? KM : 1) : 8;  // rows asked for together
+      Raw8<true> y[kBatch];
 #pragma unroll
-      for (int j = 0; j < KM; ++j)
-        if (pr.slot[j] >= 0) o[i] += pr.w[j] * load8<true>(a.y, (size_t)pr.slot[j] * a.d + 8 * c);
+      for (int j0 = 0; j0 < KM; j0 += kBatch) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (j0 + j < a.k) y[j].load(a.y, (size_t)pr.slot[j0 + j] * a.d + 8 * c);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (j0 + j < a.k) o[i] += pr.w[j0 + j] * y[j].get(pr.mask[j0 + j]);
+      }
       if (a.add) o[i] += load8<kF32>(a.add, base + 8 * c);
       s[0] += sum8(o[i], o[i]);
     }
@@ -87,11 +91,9 @@ __global__ __launch_bounds__(kThreads) void combine_residual_kernel(
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + kThreads * i;
+    if (!kAhead) ask(i);
     if (c < nch) {
-      f32x8 n = o[i] * tg;
-      if (a.post_gain) n *= load8<true>(a.post_gain, 8 * c);
-      if (a.gate_mode == MOE_GATE_CHANNEL) n *= load8<true>(a.gate, 8 * c);
-      o[i] = load8<kF32>(residual, base + 8 * c) * a.res_scale + n;
+      o[i] = res[i] * a.res_scale + o[i] * tg * fac[i];
       store8<kF32>(out, base + 8 * c, o[i]);
       s[0] += sum8(o[i], o[i]);
     }
@@ -103,19 +105,18 @@ __global__ __launch_bounds__(kThreads) void combine_residual_kernel(
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + kThreads * i;
     if (c < nch) {
-      f32x8 n = o[i] * rstd;
-      if (next_gain) n *= load8<true>(next_gain, 8 * c);
-      store8<false>(next_out, base + 8 * c, n);
+      if (!kAhead && next_gain) nxt[i] = load8<true>(next_gain, 8 * c);
+      store8<false>(next_out, base + 8 * c, o[i] * rstd * nxt[i]);
     }
   }
 }
 
-template <bool kF32, bool kDyF32, int KM, int NC>
+template <bool kF32, bool kDyF32, int KM, int NC, int kThreads>
 __global__ __launch_bounds__(kThreads) void combine_residual_bwd_kernel(
     BlockOutArgs a, const void* dout, void* __restrict__ dy, float* __restrict__ dtopk_w,
     void* __restrict__ dadd, void* dresidual, float* __restrict__ dgate_t,
     float* __restrict__ partial) {
-  constexpr int kSums = 2 + 2 * KM;
+  constexpr int kSums = 2 + 2 * KM, kWaves = kThreads / kWave;
   __shared__ float red[2][kSums * kWaves];
   const int nch = a.d >> 3;
   const bool post = a.post_gain != nullptr, gch = a.gate_mode == MOE_GATE_CHANNEL;
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void combine_residual_bwd_kernel(
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
     const size_t base = (size_t)t * a.d;
     Pairs<KM> pr;
-    pr.load(a, t);
+    pr.load(a.pair_pos, a.topk_w, a.T * a.k, a.k, t);
     f32x8 o[NC], u[NC], r[NC];
     float s[kSums];
 #pragma unroll
@@ -135,16 +136,30 @@ __global__ __launch_bounds__(kThreads) void combine_residual_bwd_kernel(
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + kThreads * i;
       if (c < nch) {
-        f32x8 y[KM > 0 ? KM : 1];
-        o[i] = 0.0f;
+        // the rows of up to 8 pairs stay in registers between o and the sums
+        // that need it; more are read four at a time, and again for the sums
+        constexpr int kBatch = KM > 8 ? 4 : KM ? KM : 1;
+        f32x8 y[kBatch];
+        auto rows = [&](int j0) {
 #pragma unroll
-        for (int j = 0; j < KM; ++j) {
-          y[j] = 0.0f;
-          if (pr.slot[j] >= 0) y[j] = load8<true>(a.y, (size_t)pr.slot[j] * a.d + 8 * c);
-          o[i] += pr.w[j] * y[j];
+          for (int j = 0; j < kBatch; ++j) {
+            y[j] = 0.0f;
+            if (j0 + j < a.k) y[j] = load8<true>(a.y, (size_t)pr.slot[j0 + j] * a.d + 8 * c);
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            if (!pr.mask[j0 + j]) y[j] = 0.0f;
+          if (KM > kBatch) __builtin_amdgcn_sched_barrier(0);
+        };
+        o[i] = 0.0f;
+        r[i] = load8<kF32>(dout, base + 8 * c);
+#pragma unroll
+        for (int j0 = 0; j0 < KM; j0 += kBatch) {
+          rows(j0);
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) o[i] += pr.w[j0 + j] * y[j];
         }
         if (a.add) o[i] += load8<kF32>(a.add, base + 8 * c);
-        r[i] = load8<kF32>(dout, base + 8 * c);
         if (dresidual) store8<kF32>(dresidual, base + 8 * c, r[i] * a.res_scale);
         u[i] = r[i];
         if (gch) u[i] *= load8<true>(a.gate, 8 * c);
@@ -152,11 +167,18 @@ __global__ __launch_bounds__(kThreads) void combine_residual_bwd_kernel(
         s[0] += sum8(o[i], o[i]);
         s[1] += sum8(u[i], o[i]);
 #pragma unroll
-        for (int j = 0; j < KM; ++j) {
-          s[2 + j] += sum8(u[i], y[j]);
-          s[2 + KM + j] += sum8(o[i], y[j]);
+        for (int j0 = 0; j0 < KM; j0 += kBatch) {
+          if (KM > kBatch) rows(j0);
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            s[2 + j0 + j] += sum8(u[i], y[j]);
+            s[2 + KM + j0 + j] += sum8(o[i], y[j]);
+          }
         }
       }
+      // one chunk's rows in registers at a time: occupancy hides more than
+      // asking for the next chunk's early would
+      __builtin_amdgcn_sched_barrier(0);
     }
     block_sum<kSums, kWaves>(s, red[turn]);
     const float tg = a.gate_mode == MOE_GATE_TOKEN ? a.gate[t] : 1.0f;
@@ -176,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void combine_residual_bwd_kernel(
         if (dy) {
 #pragma unroll
           for (int j = 0; j < KM; ++j)
-            if (pr.slot[j] >= 0)
+            if (pr.mask[j])
               store8<kDyF32>(dy, (size_t)pr.slot[j] * a.d + 8 * c, g * pr.w[j]);
         }
         acc[i] += r[i] * (o[i] * (tg * rstd));
@@ -191,37 +213,18 @@ __global__ __launch_bounds__(kThreads) void combine_residual_bwd_kernel(
   }
 }
 
-// Calls f with the number of pairs a token's kernel is built for (0, 8 or
-// 16) and the chunks a thread holds, as types.
-template <typename F>
-void by_shape(int k, int d, F&& f) {
-  auto nc = [&](auto km) {
-    switch ((d / 8 + kThreads - 1) / kThreads) {
-      case 1: return f(km, std::integral_constant<int, 1>{});
-      case 2: return f(km, std::integral_constant<int, 2>{});
-      case 3: return f(km, std::integral_constant<int, 3>{});
-      default: return f(km, std::integral_constant<int, 4>{});
-    }
-  };
-  if (k == 0)
-    nc(std::integral_constant<int, 0>{});
-  else if (k <= 8)
-    nc(std::integral_constant<int, 8>{});
-  else
-    nc(std::integral_constant<int, 16>{});
-}
-
 }  // namespace
 
 hipError_t launch_combine_residual(const BlockOutArgs& a, const void* residual,
                                    const float* next_gain, void* out, void* next_out,
                                    hipStream_t s) {
-  by_shape(a.k, a.d, [&](auto km, auto nc) {
-    constexpr int KM = decltype(km)::value, NC = decltype(nc)::value;
-    auto kern = a.f32 ? combine_residual_kernel<true, KM, NC>
-                      : combine_residual_kernel<false, KM, NC>;
-    hipLaunchKernelGGL(kern, dim3(a.T), dim3(kThreads), 0, s, a, residual, next_gain, out,
-                       next_out);
+  with_pairs(a.k, [&](auto km) {
+    with_shape(a.T, a.d, [&](auto th, auto nc) {
+      constexpr int KM = decltype(km)::value, TH = decltype(th)::value, NC = decltype(nc)::value;
+      auto kern = a.f32 ? combine_residual_kernel<true, KM, NC, TH>
+                        : combine_residual_kernel<false, KM, NC, TH>;
+      hipLaunchKernelGGL(kern, dim3(a.T), dim3(TH), 0, s, a, residual, next_gain, out, next_out);
+    });
   });
   return hipGetLastError();
 }
@@ -241,13 +244,15 @@ hipError_t launch_combine_residual_bwd(const BlockOutArgs& a, const void* dout, 
   const bool colsum = dpost_gain || dgate_c;
   float* partial = colsum ? (float*)ws : nullptr;
   if (nb) {
-    by_shape(a.k, a.d, [&](auto km, auto nc) {
-      constexpr int KM = decltype(km)::value, NC = decltype(nc)::value;
-      with_bools(a.f32, dy_f32, [&](auto f, auto yf) {
-        hipLaunchKernelGGL((combine_residual_bwd_kernel<decltype(f)::value, decltype(yf)::value,
-                                                        KM, NC>),
-                           dim3(nb), dim3(kThreads), 0, s, a, dout, dy, dtopk_w, dadd, dresidual,
-                           dgate_t, partial);
+    with_pairs(a.k, [&](auto km) {
+      with_shape(a.T, a.d, [&](auto th, auto nc) {
+        constexpr int KM = decltype(km)::value, TH = decltype(th)::value, NC = decltype(nc)::value;
+        with_bools(a.f32, dy_f32, [&](auto f, auto yf) {
+          hipLaunchKernelGGL((combine_residual_bwd_kernel<decltype(f)::value, decltype(yf)::value,
+                                                          KM, NC, TH>),
+                             dim3(nb), dim3(TH), 0, s, a, dout, dy, dtopk_w, dadd, dresidual,
+                             dgate_t, partial);
+        });
       });
     });
   }

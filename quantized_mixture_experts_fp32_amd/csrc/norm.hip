@@ -15,26 +15,27 @@ namespace moe {
 namespace {
 using namespace row;
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
 // Blocks of the backward pass: each takes every kBwdBlocks-th row and keeps
 // its share of the column sums in registers.
 constexpr int kBwdBlocks = 512;
 
-template <bool kXF32, bool kOutF32, int NC>
+template <bool kXF32, bool kOutF32, int NC, int kThreads>
 __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(const void* __restrict__ x,
                                                            const float* __restrict__ gain, int d,
                                                            float eps, void* __restrict__ out) {
+  constexpr int kWaves = kThreads / kWave;
   __shared__ float red[kWaves];
   const size_t base = (size_t)blockIdx.x * d;
   const int nch = d >> 3;
-  f32x8 v[NC];
+  f32x8 v[NC], g[NC];
   float s[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + kThreads * i;
+    g[i] = 1.0f;
     if (c < nch) {
       v[i] = load8<kXF32>(x, base + 8 * c);
+      if (gain) g[i] = load8<true>(gain, 8 * c);
       s[0] += sum8(v[i], v[i]);
     }
   }
@@ -43,39 +44,57 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(const void* __restric
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + kThreads * i;
-    if (c < nch) {
-      f32x8 r = v[i] * rstd;
-      if (gain) r *= load8<true>(gain, 8 * c);
-      store8<kOutF32>(out, base + 8 * c, r);
-    }
+    if (c < nch) store8<kOutF32>(out, base + 8 * c, v[i] * rstd * g[i]);
   }
 }
 
-template <bool kDoF32, bool kXF32, int NC>
+template <bool kDoF32, bool kXF32, int NC, int kThreads>
 __global__ __launch_bounds__(kThreads) void rmsnorm_bwd_kernel(
     const void* __restrict__ dout, const void* __restrict__ x, const float* __restrict__ gain,
     const void* dres, int T, int d, float eps, void* dx, float* __restrict__ partial) {
+  constexpr int kWaves = kThreads / kWave;
   __shared__ float red[2][2 * kWaves];
   const int nch = d >> 3;
   f32x8 g[NC], acc[NC];
+  int at[NC];  // the chunk's column; threads past the row read its first chunk
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
     const int c = threadIdx.x + kThreads * i;
+    at[i] = c < nch ? 8 * c : 0;
     acc[i] = 0.0f;
     g[i] = 1.0f;
     if (gain && c < nch) g[i] = load8<true>(gain, 8 * c);
   }
+  // the next row is asked for before this one's sums (past the last row: the
+  // last again, for nothing)
+  Raw8<kXF32> rx[NC], rr[NC];
+  Raw8<kDoF32> ru[NC];
+  auto ask = [&](int t) {
+    const size_t base = (size_t)min(t, T - 1) * d;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      rx[i].load(x, base + at[i]);
+      ru[i].load(dout, base + at[i]);
+      if (dres) rr[i].load(dres, base + at[i]);
+    }
+  };
+  ask(blockIdx.x);
   int turn = 0;
   for (int t = blockIdx.x; t < T; t += gridDim.x, turn ^= 1) {
     const size_t base = (size_t)t * d;
-    f32x8 v[NC], u[NC];
+    f32x8 v[NC], u[NC], r[NC];
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const int c = threadIdx.x + kThreads * i;
-      if (c < nch) {
-        v[i] = load8<kXF32>(x, base + 8 * c);
-        u[i] = load8<kDoF32>(dout, base + 8 * c);
+      v[i] = rx[i].get();
+      u[i] = ru[i].get();
+      r[i] = 0.0f;
+      if (dres) r[i] = rr[i].get();
+    }
+    ask(t + gridDim.x);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if ((int)threadIdx.x + kThreads * i < nch) {
         s[0] += sum8(v[i], v[i]);
         s[1] += sum8(u[i] * g[i], v[i]);
       }
@@ -87,9 +106,7 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_bwd_kernel(
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + kThreads * i;
       if (c < nch) {
-        f32x8 r = (u[i] * g[i] - v[i] * a) * rstd;
-        if (dres) r += load8<kXF32>(dres, base + 8 * c);
-        store8<kXF32>(dx, base + 8 * c, r);
+        store8<kXF32>(dx, base + 8 * c, (u[i] * g[i] - v[i] * a) * rstd + r[i]);
         acc[i] += u[i] * (v[i] * rstd);
       }
     }
@@ -115,7 +132,7 @@ __global__ __launch_bounds__(1024) void colsum_kernel(const float* __restrict__ 
   const int c = blockIdx.x * 64 + lane;
   float s = 0.0f;
   if (c < d) {
-#pragma unroll 4
+#pragma unroll 16
     for (int r = wave; r < n; r += 16) s += rows[(size_t)r * d + c];
   }
   red[wave][lane] = s;
@@ -139,19 +156,13 @@ hipError_t launch_colsum(const float* rows, int n, int d, float* out1, const flo
 
 hipError_t launch_rmsnorm(const void* x, int x_f32, const float* gain, int T, int d, float eps,
                           void* out, int out_f32, hipStream_t s) {
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3(T), dim3(kThreads), 0, s, x, gain, d, eps, out);
-  };
-  auto chunks = [&](auto xf, auto of) {
-    constexpr bool X = decltype(xf)::value, O = decltype(of)::value;
-    switch ((d / 8 + kThreads - 1) / kThreads) {
-      case 1: return go(rmsnorm_kernel<X, O, 1>);
-      case 2: return go(rmsnorm_kernel<X, O, 2>);
-      case 3: return go(rmsnorm_kernel<X, O, 3>);
-      default: return go(rmsnorm_kernel<X, O, 4>);
-    }
-  };
-  with_bools(x_f32, out_f32, chunks);
+  with_shape(T, d, [&](auto th, auto nc) {
+    with_bools(x_f32, out_f32, [&](auto xf, auto of) {
+      constexpr int TH = decltype(th)::value, NC = decltype(nc)::value;
+      hipLaunchKernelGGL((rmsnorm_kernel<decltype(xf)::value, decltype(of)::value, NC, TH>),
+                         dim3(T), dim3(TH), 0, s, x, gain, d, eps, out);
+    });
+  });
   return hipGetLastError();
 }
 
@@ -164,20 +175,15 @@ hipError_t launch_rmsnorm_bwd(const void* dout, int do_f32, const void* x, int x
                               void* dx, float* dgain, void* ws, hipStream_t s) {
   const int nb = T < kBwdBlocks ? T : kBwdBlocks;
   float* partial = dgain ? (float*)ws : nullptr;
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3(nb), dim3(kThreads), 0, s, dout, x, gain, dres, T, d, eps, dx,
-                       partial);
-  };
-  auto chunks = [&](auto df, auto xf) {
-    constexpr bool D = decltype(df)::value, X = decltype(xf)::value;
-    switch ((d / 8 + kThreads - 1) / kThreads) {
-      case 1: return go(rmsnorm_bwd_kernel<D, X, 1>);
-      case 2: return go(rmsnorm_bwd_kernel<D, X, 2>);
-      case 3: return go(rmsnorm_bwd_kernel<D, X, 3>);
-      default: return go(rmsnorm_bwd_kernel<D, X, 4>);
-    }
-  };
-  if (nb) with_bools(do_f32, x_f32, chunks);
+  if (nb) {
+    with_shape(kWideRows, d, [&](auto th, auto nc) {
+      with_bools(do_f32, x_f32, [&](auto df, auto xf) {
+        constexpr int TH = decltype(th)::value, NC = decltype(nc)::value;
+        hipLaunchKernelGGL((rmsnorm_bwd_kernel<decltype(df)::value, decltype(xf)::value, NC, TH>),
+                           dim3(nb), dim3(TH), 0, s, dout, x, gain, dres, T, d, eps, dx, partial);
+      });
+    });
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dgain) return e;
   return launch_colsum(partial, nb, d, dgain, nullptr, nullptr, nullptr, s);

@@ -127,7 +127,8 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
                   uint16_t* __restrict__ h_out,             // gate/up: [P][N]
                   float* __restrict__ y_out,                // down:    [P][N]
                   uint2* __restrict__ hsum_out,             // gate/up: [P][N/128]
-                  int T, const float* __restrict__ bias, void* __restrict__ dense_out) {
+                  int T, int tile_tokens,                   // dense
+                  const float* __restrict__ bias, void* __restrict__ dense_out) {
   constexpr bool kGateUp = kMode == kPfGateUp;
   constexpr bool kDense = kMode == kPfDenseF32 || kMode == kPfDenseBf16;
   // two staging buffers as distinct objects, so that reads of one are not
@@ -147,8 +148,10 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
   const int pair = xcd * (gridDim.x >> 3) + local;
   const int tile = kDense ? pair / nfb : (local / nfb) * 8 + xcd;
   const int fblk = kDense ? pair % nfb : local % nfb;
-  if (kDense ? tile * kBT >= T : tile >= *num_tiles) return;
-  const PTile tl = kDense ? PTile{0, tile * kBT, min(kBT, T - tile * kBT), 8} : tiles[tile];
+  if (kDense ? tile * tile_tokens >= T : tile >= *num_tiles) return;
+  const PTile tl =
+      kDense ? PTile{0, tile * tile_tokens, min(tile_tokens, T - tile * tile_tokens), 8}
+             : tiles[tile];
   const int G = K >> 7;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int c32 = lane & 31, hh = lane >> 5;
@@ -346,6 +349,15 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
       for (int t = 0; t < NTB; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[t][m][i] *= s_cur[m];
+    // (dense: scaled before the store's branches, not behind them, where a
+    // lane group without rows would leave too few steps after the last MFMA)
+    if (kDense) {
+#pragma unroll
+      for (int t = 0; t < NTB; ++t) {
+        asm volatile("" : "+v"(acc[t][0]));
+        asm volatile("" : "+v"(acc[t][1]));
+      }
+    }
 
     // ---- epilogue: lane owns feature brow (per B block) for 16 token rows
     // of each token block: rows 8*(i/4) + 4*hh + i%4 of the 32-row block.
@@ -1052,30 +1064,30 @@ hipError_t launch_ffn_prefill_w4(const FfnArgs& a, uint16_t* h, void* ws, hipStr
   // gate/up writes h and its group sums (the down pass's offset terms)
   launch_k(pf_w4_kernel<kPfGateUp>, dim3(mt8 * (a.f / 128)), dim3(kThreads), 0, s, a.ev[0], a.ev[1],
            a.x, a.sorted_pair, a.k, a.d, a.f, a.gu_codes, a.gu_scales, xsum,
-           (const PTile*)tiles, (const int*)num_tiles, a.f / 128, h, (float*)nullptr, hsum, 0, (const float*)nullptr, (void*)nullptr);
+           (const PTile*)tiles, (const int*)num_tiles, a.f / 128, h, (float*)nullptr, hsum, 0, 0, (const float*)nullptr, (void*)nullptr);
   const int dn_fb = (a.d + 255) / 256;
   launch_k(pf_w4_kernel<kPfDown>, dim3(mt8 * dn_fb), dim3(kThreads), 0, s, a.ev[2], a.ev[3],
            (const uint16_t*)h, a.sorted_pair, a.k, a.f, a.d, a.dn_codes, a.dn_scales,
            (const uint2*)hsum, (const PTile*)tiles, (const int*)num_tiles, dn_fb,
-           (uint16_t*)nullptr, a.y, (uint2*)nullptr, 0, (const float*)nullptr, (void*)nullptr);
+           (uint16_t*)nullptr, a.y, (uint2*)nullptr, 0, 0, (const float*)nullptr, (void*)nullptr);
   return hipGetLastError();
 }
 
 size_t linear_w4_gemm_ws_bytes(int T, int K) { return (size_t)T * (K / 128) * sizeof(uint2); }
 
 hipError_t launch_linear_w4_gemm(const uint16_t* x, const uint8_t* codes, const uint16_t* scales,
-                                 const float* bias, int T, int N, int K, void* out, int out_f32,
-                                 void* ws, hipStream_t s) {
+                                 const float* bias, int T, int N, int K, int tile_tokens,
+                                 void* out, int out_f32, void* ws, hipStream_t s) {
   uint2* xsum = (uint2*)ws;
   const long long n = (long long)T * (K / 128);
   hipLaunchKernelGGL(group_sums, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, x,
                      (long long)T, K, xsum);
-  const int nfb = (N + 255) / 256, pairs = (T + kBT - 1) / kBT * nfb;
+  const int nfb = (N + 255) / 256, pairs = (T + tile_tokens - 1) / tile_tokens * nfb;
   auto kern = out_f32 ? pf_w4_kernel<kPfDenseF32> : pf_w4_kernel<kPfDenseBf16>;
   hipLaunchKernelGGL(kern, dim3((pairs + 7) & ~7), dim3(kThreads), 0, s, x,
                      (const int32_t*)nullptr, 1, K, N, codes, scales, (const uint2*)xsum,
                      (const PTile*)nullptr, (const int*)nullptr, nfb, (uint16_t*)nullptr,
-                     (float*)nullptr, (uint2*)nullptr, T, bias, out);
+                     (float*)nullptr, (uint2*)nullptr, T, tile_tokens, bias, out);
   return hipGetLastError();
 }
 

@@ -9,6 +9,8 @@
 // Layout.  Lane (row r, quarter kq) of a wave reads bytes [16 kq, 16 kq + 16)
 // of row r of a 16-row tile's group: one 16-byte load per lane takes the
 // whole 1 KiB block.  The activations of token c sit in lanes (c, kq).
+#include <math.h>
+
 #include <algorithm>
 
 #include "kcommon.hpp"
@@ -186,6 +188,11 @@ __global__ __launch_bounds__(W * kWave) void linear_w4_stream(
           for (int r = 0; r < 4; ++r) acc[c][r] = fmaf(s[r], p[c][r] + seed[c][j], acc[c][r]);
         if (NT * NG > 2) __builtin_amdgcn_sched_barrier(0);
       }
+      // The totals are formed before the branch: read behind it, the last MFMA's
+      // result came too early (the compiler's wait states did not cover the
+      // path around the loads).
+#pragma unroll
+      for (int c = 0; c < NT; ++c) asm volatile("" : "+v"(acc[c]));
       if (decltype(ahead)::value || i + D < nmine) load(i + D, q, sc);
       f32x4* rd = red + (i & 1) * (W * NT * 64);
 #pragma unroll
@@ -387,47 +394,68 @@ hipError_t stream_as(const uint16_t* x, const uint8_t* codes, const uint16_t* sc
 
 }  // namespace
 
-// The GEMM kernel of the prefill path, when its blocks (128 tokens by 256
-// features) nearly fill the chip: at K = N = 4096 it takes 84 us for any batch
-// up to 2048 (too few blocks), 117 us for 2501 and 141 us for 4096 tokens; the
-// streaming kernel 53 us for 1024 and 151 us for 2501.
-static bool takes_gemm(int T, int N) {
-  return T >= 256 &&
-         (long long)((T + 127) / 128) * ((N + 255) / 256) >= 3 * kCUs / 4;
+// Tokens per tile of the GEMM kernel (blocks of 256 features, two a CU) where
+// it is the faster one, otherwise 0.  Its time goes by blocks a CU; measured
+// at K = 4096 (us, one block a CU and two): tiles of 64 tokens 50 and 81, of 96
+// 68 and 112, of 128 83 and 140, plus about 4 for the group sums.  The kernels
+// below take 2.9e-9 us per token, feature and input (3.2e-9 for K <= 2048,
+// 4.6e-9 for K <= 1024).  E.g. N = 4096: 1024 tokens 49 us streamed, 52 us in
+// tiles of 64; 2501 tokens 104 us in tiles of 96, 116 us in tiles of 128.
+static int gemm_tile(int T, int N, int K) {
+  if (T <= 64) return 0;
+  static const struct {
+    int tokens;
+    float one, two;
+  } kTiles[] = {{128, 83.0f, 140.0f}, {96, 68.0f, 112.0f}, {64, 50.0f, 81.0f}};
+  const float per = K <= 1024 ? 4.6e-9f : K <= 2048 ? 3.2e-9f : 2.9e-9f;
+  float best = per * (float)((T + 31) / 32 * 32) * N * K;
+  int tokens = 0;
+  for (const auto& t : kTiles) {
+    const float blocks = (float)((T + t.tokens - 1) / t.tokens) * ((N + 255) / 256);
+    const float per_cu = ceilf(blocks / kCUs);
+    const float us = (per_cu <= 1.0f ? t.one : 0.5f * per_cu * t.two) * (K / 4096.0f) + 4.0f;
+    if (us < best) {
+      best = us;
+      tokens = t.tokens;
+    }
+  }
+  return tokens;
 }
 
 size_t linear_w4_ws_bytes(int T, int N, int K) {
-  return takes_gemm(T, N) ? linear_w4_gemm_ws_bytes(T, K) : 0;
+  return gemm_tile(T, N, K) ? linear_w4_gemm_ws_bytes(T, K) : 0;
 }
 
 hipError_t launch_linear_w4(const uint16_t* x, const uint8_t* codes, const uint16_t* scales,
                             const float* bias, int T, int N, int K, void* out, int out_f32,
                             void* ws, hipStream_t s) {
-  if (takes_gemm(T, N))
-    return launch_linear_w4_gemm(x, codes, scales, bias, T, N, K, out, out_f32, ws, s);
+  if (const int tokens = gemm_tile(T, N, K))
+    return launch_linear_w4_gemm(x, codes, scales, bias, T, N, K, tokens, out, out_f32, ws, s);
   auto as = [&](auto f) { return f(x, codes, scales, bias, T, N, K, out, out_f32, s); };
   const int G = K >> 7, ntile = N >> 4;
   if (T <= 16) {
-    // tile kernel while a block a CU (two of four waves for a short K) takes
-    // every row tile at once; with more, the streaming kernel, which reads x
-    // once a block
+    // Tile kernel while every row tile is taken at once, by a block of one to
+    // three tiles a CU (K <= 1024: by two of four waves, 50304 features of 4
+    // tokens 8.7 us, streamed 12.6); with more, the streaming kernel, which
+    // reads x once a block (K = 4096, N = 50304: 22.5 us, tiled 26).
     if (ntile <= kCUs) return G >= 96 ? as(tile_as<16, 1, 1>) : as(tile_as<8, 1, 1>);
     if (G <= 8) return as(tile_as<4, 1, 2>);
     if (ntile <= 2 * kCUs) return as(tile_as<8, 1, 2>);
     if (ntile <= 5 * kCUs) return as(tile_as<8, 1, 3>);
-    return G <= 16 ? as(stream_as<16, 1, 1, 4>) : as(stream_as<16, 1, 2, 2>);
+    return G <= 16 ? as(stream_as<16, 1, 1, 2>) : as(stream_as<16, 1, 2, 2>);
   }
-  // Streaming kernel for many row tiles (its blocks read x once) and for many
-  // token passes; between them the tile kernel, 32 tokens a block, with as
-  // many row tiles a block as leave one or two blocks a CU.  At K = 4096: 64
-  // tokens, N = 50304: 45 us streamed, 54 us tiled; 1024 tokens, N = 4096: 53
-  // and 76 us; 256 tokens: 20 and 16 us.  64 tokens, N = 12288: 13 us with six
-  // tiles, 16 us with four.
-  if ((T <= 64 && ntile >= 8 * kCUs) || T > 512)
-    return G <= 16 ? as(stream_as<16, 2, 1, 3>) : as(stream_as<16, 2, 2, 2>);
-  const int units = (int)(((long long)ntile * ((T + 31) / 32) + kCUs - 1) / kCUs);
+  // 32 tokens a block or pass.  Tile kernel up to 8 row tiles a CU (and for a
+  // K that would leave streaming waves idle), with as many tiles a block as
+  // leave one or two blocks a CU; beyond, the streaming kernel.  At K = 4096:
+  // 64 tokens, N = 50304: 42 us streamed, 52 us tiled; 512 tokens, N = 4096: 27
+  // and 29 us; 128 tokens: 11.2 and 10.4 us; 64 tokens, N = 12288: 13.2 us with
+  // six tiles, 15.7 us with four.
+  const int units = (int)std::min<long long>(
+      ((long long)ntile * ((T + 31) / 32) + kCUs - 1) / kCUs, 1 << 30);
   if (units <= 2) return as(tile_as<8, 2, 2>);
-  return units == 5 || units == 6 ? as(tile_as<4, 2, 6>) : as(tile_as<4, 2, 4>);
+  if (units == 5 || units == 6) return as(tile_as<4, 2, 6>);
+  if (units <= 8 || G <= 8) return as(tile_as<4, 2, 4>);
+  return G <= 16 ? as(stream_as<16, 2, 1, 2>) : as(stream_as<16, 2, 2, 1>);
 }
 
 }  // namespace moe

@@ -62,7 +62,15 @@ def grouping(seed, T, k, E, drop=0.0, pad=0):
 LINEAR = [(1, 128, 16), (1, 2048, 2048), (2, 384, 48), (5, 4096, 272), (16, 1024, 1040),
           (17, 640, 528), (31, 1152, 64), (33, 2048, 272), (48, 4096, 512), (64, 2560, 4112),
           (65, 512, 272), (127, 1024, 48), (130, 384, 2064), (300, 1152, 528), (1000, 512, 784),
-          (515, 2048, 4096), (1, 14336, 400), (3, 16512, 64), (70, 16512, 32), (2050, 256, 16)]
+          (515, 2048, 4096), (1, 14336, 400), (3, 16512, 64), (70, 16512, 32), (2050, 256, 16),
+          # few tokens, more row tiles: two and three a block, streamed (one and
+          # several chunks of K)
+          (3, 1024, 4128), (2, 1152, 4112), (5, 1152, 8208), (4, 1152, 20496), (9, 2176, 20496),
+          (2, 8320, 20496),
+          # token passes: six tiles a block, streamed
+          (40, 640, 10256), (70, 1152, 12304), (70, 2176, 12304), (40, 4352, 24592),
+          # GEMM tiles of 64, 96 and 128 tokens, N ending inside a feature block
+          (1500, 640, 4112), (2501, 640, 2064), (1500, 256, 8208)]
 
 
 def linear_inputs(T, K, N, seed=0):
@@ -88,6 +96,22 @@ def test_linear(T, K, N, out_dtype):
     # sum of ~ 335 sigma give 2.5e-6; four times that, and the store
     rel = float((f64(out) - y).norm() / y.norm())
     assert rel <= 1e-5 + ref.HALF_STEP[out.dtype], rel
+
+
+def test_linear_many_row_tiles():
+    """More row tiles than a block's totals hold for a K of several chunks; the
+    rows of the first, some middle and the last tiles against the definition."""
+    T, K, N = 2, 4224, 131152
+    note(f"linear T={T} K={K} N={N}")
+    normal = gen(17)
+    x = normal(T, K, dtype=BF)
+    codes = torch.randint(0, 256, (N, K // 2), generator=normal.g, dtype=torch.uint8).to(DEV)
+    scales = (torch.rand(N, K // 128, generator=normal.g) * 0.01).to(torch.float16).to(DEV)
+    bias = normal(N)
+    out = moe.moe_linear_w4(x, codes, scales, bias=bias, out_dtype=moe.MOE_OUT_F32)
+    for a, b in ((0, 64), (4080, 4144), (65520, 65600), (N - 80, N)):
+        y, bound = ref.linear(x, codes[a:b], scales[a:b].contiguous(), bias[a:b])
+        assert_within(out[:, a:b], y, bound, f"rows {a}..{b}")
 
 
 def test_linear_accepts_bits_and_leading_axis():

@@ -505,9 +505,9 @@ int moe_retile_bitplane8(const uint8_t *planes_canonical, int E, int N, int K,
  * [N][K/128]; bias fp32 [N] or NULL; out [T][N] of out_dtype.  Products and
  * sums are fp32 (codes enter the matrix cores exactly, weights are never
  * rounded), rounded once on store.  A row of x that holds an infinity or NaN
- * gives a row of infinities and NaN; finite values must be below 2^119 (their
+ * gives a row of infinities and NaN; finite values must be below 2^110 (their
  * group sums are scaled by 192 in fp32).
- * Requires N % 16 == 0, K % 128 == 0, K below 2^20, T * K and T * N below 2^40.
+ * Requires N % 16 == 0, K % 128 == 0, K below 2^20, T * K and T * N below 2^38.
  * ws / ws_bytes: at least moe_linear_w4_ws_bytes(T, N, K) (0 for T <= 64),
  * 256-byte aligned, no contents carried between calls.
  * ------------------------------------------------------------------- */
@@ -528,7 +528,7 @@ int moe_linear_w4(const void *x_bf16, int T, int N, int K, int group_size,
  * dx may be dres.  rstd is computed again from x.
  * ws / ws_bytes: at least moe_rmsnorm_bwd_ws_bytes(T, d), 16-byte aligned
  * (NULL if dgain is NULL).  Sums are fp32 in a fixed order.
- * Both require d % 8 == 0, d <= 8192, eps > 0 and finite.
+ * Both require T below 2^23, d % 8 == 0, d <= 8192, eps > 0 and finite.
  * ------------------------------------------------------------------- */
 int moe_rmsnorm(const void *x, int x_dtype, const float *gain, int T, int d,
                 float eps, void *out, int out_dtype, void *stream);
@@ -567,7 +567,7 @@ int moe_rmsnorm_bwd(const void *dout, int dout_dtype, const void *x, int x_dtype
  * where do is the gradient of o.  ws / ws_bytes: at least
  * moe_combine_residual_bwd_ws_bytes(T, d), 16-byte aligned (NULL if neither
  * dpost_gain nor a channel gate's dgate is wanted).
- * Both require d % 8 == 0, d <= 8192, 0 <= k <= 16 (k + add not both absent),
+ * Both require T below 2^23, d % 8 == 0, d <= 8192, 0 <= k <= 16 (k = 0 needs add),
  * eps > 0, finite eps and res_scale.  Sums are fp32 in a fixed order.
  * ------------------------------------------------------------------- */
 int moe_combine_residual(const void *residual, int dtype, const float *y_pairs,
@@ -605,7 +605,7 @@ int moe_combine_residual_bwd(const void *dout, int dtype, const float *y_pairs,
  *   dy_dtype; either output may be NULL (y_pairs is read for dtopk_w alone,
  *   topk_w for dy_pairs alone).
  * dtopk_w of a dropped pair is 0.  Sums are fp32, ranks ascending.
- * All require d % 8 == 0, d <= 8192, 1 <= k <= 16.
+ * All require T below 2^23, d % 8 == 0, d <= 8192, 1 <= k <= 16.
  * ------------------------------------------------------------------- */
 int moe_dispatch(const void *x, int dtype, const int32_t *pair_pos,
                  const float *topk_w, int T, int k, int d, void *xs, void *stream);

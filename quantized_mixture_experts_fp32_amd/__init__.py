@@ -488,7 +488,7 @@ def _on_device(fn):
         if not isinstance(first, torch.Tensor):
             raise ValueError(f"{fn.__name__}: a tensor is needed, got {type(first).__name__}")
         if stream is None:
-            if not first.is_cuda or first.get_device() == torch.cuda.current_device():
+            if not first.is_cuda or first.get_device() == torch._C._cuda_getDevice():
                 return fn(first, *args, **kw)
             with torch.cuda.device(first.device):
                 return fn(first, *args, **kw)
@@ -530,17 +530,12 @@ def _rows(fn, name, t, shape, dtypes, like=None):
                      f"{'a GPU' if like is None else like.device}")
 
 
+@functools.lru_cache(None)
 def _types():
     """(bf16 as torch has it or as its bits, bf16 or fp32, fp32, int32)."""
-    global _type_sets
-    if _type_sets is None:
-        import torch
-        _type_sets = ((torch.bfloat16, torch.int16), (torch.bfloat16, torch.int16, torch.float32),
-                      (torch.float32,), (torch.int32,))
-    return _type_sets
-
-
-_type_sets = None
+    import torch
+    return ((torch.bfloat16, torch.int16), (torch.bfloat16, torch.int16, torch.float32),
+            (torch.float32,), (torch.int32,))
 
 
 def _code(t):
@@ -549,12 +544,10 @@ def _code(t):
 
 
 def _out_rows(fn, name, t, shape, code, like):
-    import torch
+    dtypes = _types()[2 if code == MOE_OUT_F32 else 0]
     if t is None:
-        return like.new_empty(shape, dtype=torch.float32 if code == MOE_OUT_F32
-                              else torch.bfloat16)
-    bf, _, f32, _ = _types()
-    return _rows(fn, name, t, shape, f32 if code == MOE_OUT_F32 else bf, like)
+        return like.new_empty(shape, dtype=dtypes[0])
+    return _rows(fn, name, t, shape, dtypes, like)
 
 
 def _out_f32(fn, name, t, shape, like):
@@ -564,7 +557,7 @@ def _out_f32(fn, name, t, shape, like):
 def _workspace(fn, ws, need, like):
     import torch
     if ws is None:
-        return torch.empty((need,), dtype=torch.uint8, device=like.device) if need else None
+        return like.new_empty((need,), dtype=torch.uint8) if need else None
     if not ws.is_contiguous() or ws.device != like.device:
         raise ValueError(f"{fn}: ws must be contiguous and on {like.device}")
     return ws
@@ -1029,6 +1022,27 @@ class MoeLayer:
                           self.y_pairs, self.ws_ffn, path, stream)
         return moe_combine(self.y_pairs, self.pair_pos, self.topk_w, out, out_dtype,
                            stream)
+
+    def forward_block(self, residual, gain=None, eps=1e-6, add=None, post_gain=None, gate=None,
+                      gate_mode=MOE_GATE_NONE, res_scale=1.0, next_gain=None, out=None,
+                      next_out=None, path=MOE_PATH_AUTO, stream=None):
+        """The layer as a residual block of a model: moe_rmsnorm of the
+        residual stream, routing, expert FFN, and moe_combine_residual in the
+        place of the combine -> (out, next_out or None), as that call."""
+        T = residual.shape[0]
+        x = moe_rmsnorm(residual, gain, eps=eps, stream=stream)
+        if self._T != T:
+            self._alloc(T, x)
+        moe_route_permute(x, self.wr, self.bias, self.k, self.ws_rp, self.topk_idx,
+                          self.topk_w, self.offsets, self.sorted_pair, self.pair_pos,
+                          stream)
+        moe_expert_ffn_wq(x, self.offsets, self.sorted_pair, self.k, self.f, self.gu, self.gus,
+                          self.dn, self.dns, self.fmt, self.bits, self.bits_mode,
+                          self.y_pairs, self.ws_ffn, path, stream)
+        return moe_combine_residual(residual, self.y_pairs, self.pair_pos, self.topk_w, add=add,
+                                    post_gain=post_gain, gate=gate, gate_mode=gate_mode,
+                                    res_scale=res_scale, eps=eps, next_gain=next_gain, out=out,
+                                    next_out=next_out, stream=stream)
 
     def bind(self, x, out, weights=None, path=MOE_PATH_AUTO, out_dtype=MOE_OUT_BF16,
              stream=None):

@@ -505,8 +505,8 @@ static int row_check(const char* what, int T, int d, int k, int kmin, int dtype1
   if (d > MOE_MAX_D) return fail(MOE_ERR_UNSUPPORTED, "%s: d=%d > %d", what, d, MOE_MAX_D);
   if (k > MOE_MAX_TOPK)
     return fail(MOE_ERR_UNSUPPORTED, "%s: k=%d > %d", what, k, MOE_MAX_TOPK);
-  if ((long long)T * k >= (1LL << 31))
-    return fail(MOE_ERR_UNSUPPORTED, "%s: T*k must be below 2^31", what);
+  // one block of up to 512 threads a token, fewer than 2^32 threads a launch
+  if (T >= 1 << 23) return fail(MOE_ERR_UNSUPPORTED, "%s: T=%d not below 2^23", what, T);
   return MOE_OK;
 }
 
@@ -544,8 +544,8 @@ int moe_linear_w4(const void* x_bf16, int T, int N, int K, int group_size, const
   if (K % MOE_GROUP) return fail(MOE_ERR_UNSUPPORTED, "K=%d not a multiple of 128", K);
   if (N % 16) return fail(MOE_ERR_UNSUPPORTED, "N=%d not a multiple of 16", N);
   if (K >= 1 << 20) return fail(MOE_ERR_UNSUPPORTED, "K=%d not below 2^20", K);
-  if ((long long)T * K >= (1LL << 40) || (long long)T * N >= (1LL << 40))
-    return fail(MOE_ERR_UNSUPPORTED, "moe_linear_w4: T*K and T*N must be below 2^40");
+  if ((long long)T * K >= (1LL << 38) || (long long)T * N >= (1LL << 38))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_linear_w4: T*K and T*N must be below 2^38");
   if (T == 0) return ok();
   if (!x_bf16 || !codes || !scales_f16 || !out)
     return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: null pointer");

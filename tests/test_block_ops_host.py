@@ -127,6 +127,7 @@ def test_norm_refusals(lib):
     def f(x=FAKE, xd=0, g=FAKE, T=4, d=64, eps=1e-6, out=FAKE, od=0):
         return lib.moe_rmsnorm(x, xd, g, T, d, eps, out, od, NULL)
     assert f(d=60) == UNS and f(d=8200) == UNS and f(d=0) == INV and f(T=-1) == INV
+    assert f(T=1 << 23) == UNS
     assert f(xd=2) == INV and f(od=-1) == INV
     for eps in (0.0, -1e-6, float("nan"), float("inf")):
         assert f(eps=eps) == INV

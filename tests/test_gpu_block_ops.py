@@ -157,7 +157,7 @@ def test_linear_nonfinite_row_stays_in_its_row(T):
 
 # ---------------------------------------------------------------------- norms
 NORM = [(1, 8), (3, 24), (5, 128), (2, 1000), (4, 2048), (3, 2056), (2, 4096), (1, 6152),
-        (1030, 264), (515, 2048), (7, 8192), (2100, 1024)]
+        (1030, 264), (515, 2048), (7, 8192), (2100, 1024), (300, 2600), (270, 5000)]
 
 
 @pytest.mark.parametrize("dtype,out_dtype", [(BF, 0), (BF, 1), (F32, 0), (F32, 1)])
@@ -212,7 +212,10 @@ BLOCK = [(1, 2048, 8, 64, BF, "token", True, True, False, 0.0, 0),
          (6, 6152, 0, 1, F32, "none", False, False, True, 0.0, 0),
          (700, 264, 6, 64, BF, "channel", True, True, False, 0.0, 77),
          (1100, 1024, 8, 64, F32, "token", False, True, True, 0.05, 5),
-         (530, 2048, 4, 8, BF, "channel", False, False, False, 0.0, 0)]
+         (530, 2048, 4, 8, BF, "channel", False, False, False, 0.0, 0),
+         (300, 2600, 8, 16, BF, "channel", True, True, False, 0.1, 7),
+         (270, 5000, 7, 16, F32, "none", True, True, True, 0.0, 0),
+         (260, 4360, 12, 16, BF, "token", True, False, False, 0.1, 0)]
 
 
 class BlockCase:
@@ -447,6 +450,35 @@ def test_sort_and_back_is_the_layer_grouping():
     assert_within(back, want, 20 * ref.U * f64(x).abs(), "back")
 
 
+def test_offsets_past_32_bits():
+    """Grouped rows past 4 GiB: the last token's rows of every call."""
+    note("offsets past 32 bits")
+    T, k, d = 20000, 8, 8192
+    normal = gen(31)
+    pos = torch.arange(T * k, dtype=torch.int32, device=DEV)
+    last = slice((T - 1) * k, T * k)
+    y = torch.zeros(T * k, d, device=DEV)           # 5.2 GB
+    x, w = torch.zeros(T, d, device=DEV), torch.softmax(normal(T, k), 1)
+    x[-1], y[last] = normal(d), normal(k, d)
+    y64, w64, x64 = f64(y[last]), f64(w[-1]), f64(x[-1])
+    out, _ = moe.moe_combine_residual(x, y, pos, w)
+    assert_within(out[-1:], (x64 + (w64[:, None] * y64).sum(0))[None],
+                  20 * ref.U * (x64.abs() + (w64[:, None] * y64.abs()).sum(0))[None], "combine")
+    dy, dw = moe.moe_combine_bwd(x, y, pos, w)
+    assert_within(dy[last], w64[:, None] * x64, 0.0, "dy")
+    assert_within(dw[-1], (y64 * x64).sum(1), ref.C * ref.U * (y64 * x64).abs().sum(1), "dw")
+    del dy
+    xs = moe.moe_dispatch(x, pos, k, topk_w=w)
+    assert_within(xs[last], w64[:, None] * x64, 0.0, "xs")
+    xs[last] = y[last]
+    dx, dw = moe.moe_dispatch_bwd(xs, pos, k, x=x, topk_w=w)
+    assert_within(dx[-1], (w64[:, None] * y64).sum(0),
+                  20 * ref.U * (w64[:, None] * y64.abs()).sum(0), "dx")
+    del xs
+    g = moe.moe_combine_residual_bwd(x, y, pos, w)
+    assert_within(g.dy_pairs[last], w64[:, None] * x64, 0.0, "block dy")
+
+
 # --------------------------------------------------- zero tokens, repeatability
 def test_zero_tokens():
     note("zero tokens")
@@ -590,6 +622,15 @@ def test_block_around_the_quantized_layer():
                                          f64(gains[2]))
     assert_within(out, v, ev, "out")
     assert_within(nxt, rn, en, "next")
+
+
+    # the layer's own method makes the same calls
+    got = layer.forward_block(res, gains[0], post_gain=gains[1], res_scale=0.5, eps=EPS,
+                              next_gain=gains[2])
+    assert torch.equal(got[0], out) and torch.equal(got[1], nxt)
+    plain, none = layer.forward_block(res, gains[0], eps=EPS)
+    assert none is None
+    assert_within(plain, f64(res) + f64(o), 8 * ref.U * o64.abs().max(), "plain block")
 
 
 def test_gpu_argument_checks():

@@ -544,8 +544,9 @@ int moe_linear_w4(const void* x_bf16, int T, int N, int K, int group_size, const
   if (K % MOE_GROUP) return fail(MOE_ERR_UNSUPPORTED, "K=%d not a multiple of 128", K);
   if (N % 16) return fail(MOE_ERR_UNSUPPORTED, "N=%d not a multiple of 16", N);
   if (K >= 1 << 20) return fail(MOE_ERR_UNSUPPORTED, "K=%d not below 2^20", K);
-  if ((long long)T * K >= (1LL << 38) || (long long)T * N >= (1LL << 38))
-    return fail(MOE_ERR_UNSUPPORTED, "moe_linear_w4: T*K and T*N must be below 2^38");
+  // fewer than 2^32 threads in every launch
+  if ((long long)T * K >= (1LL << 34) || (long long)T * N >= (1LL << 34))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_linear_w4: T*K and T*N must be below 2^34");
   if (T == 0) return ok();
   if (!x_bf16 || !codes || !scales_f16 || !out)
     return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: null pointer");

@@ -112,9 +112,10 @@ __device__ __forceinline__ void staged_barrier() {
 // Staged tile: row t (256 bytes) holds the token's 128 activations as
 // 16-byte chunks, chunk c at position c ^ (t & 15), so that the 32 rows a
 // fragment read touches fall on distinct banks.
-enum PfMode { kPfDown, kPfGateUp, kPfDenseF32, kPfDenseBf16 };
-
-template <PfMode kMode>
+//   dense (kDense): as down, for one matrix and plain rows: block (tile,
+//     feature block) of `tile_tokens` tokens, no lists; the bias is added and
+//     the result stored as fp32 or bf16 (kBf16).
+template <bool kGateUp, bool kDense = false, bool kBf16 = false>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(kPfWaves, kPfWaves)))
 void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K]
                   const int32_t* __restrict__ sorted_pair,  // gate/up: gather
@@ -129,8 +130,6 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
                   uint2* __restrict__ hsum_out,             // gate/up: [P][N/128]
                   int T, int tile_tokens,                   // dense
                   const float* __restrict__ bias, void* __restrict__ dense_out) {
-  constexpr bool kGateUp = kMode == kPfGateUp;
-  constexpr bool kDense = kMode == kPfDenseF32 || kMode == kPfDenseBf16;
   // two staging buffers as distinct objects, so that reads of one are not
   // ordered behind the in-flight direct-to-LDS loads of the other
   __shared__ __attribute__((aligned(16))) uint8_t abuf0[kBufB];
@@ -386,10 +385,10 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
             for (int m = 0; m < 2; ++m) {
               if (!bstore[m]) continue;
               const float v = bias ? acc[t][m][i] + bias[brow[m]] : acc[t][m][i];
-              if (kMode == kPfDenseF32)
-                ((float*)dense_out)[slot * N + brow[m]] = v;
-              else
+              if (kBf16)
                 ((uint16_t*)dense_out)[slot * N + brow[m]] = (uint16_t)f32_to_bf16_rne(v);
+              else
+                ((float*)dense_out)[slot * N + brow[m]] = v;
             }
             continue;
           }
@@ -1062,14 +1061,16 @@ hipError_t launch_ffn_prefill_w4(const FfnArgs& a, uint16_t* h, void* ws, hipStr
   }
   const unsigned mt8 = (unsigned)((mt + 7) & ~(size_t)7);
   // gate/up writes h and its group sums (the down pass's offset terms)
-  launch_k(pf_w4_kernel<kPfGateUp>, dim3(mt8 * (a.f / 128)), dim3(kThreads), 0, s, a.ev[0], a.ev[1],
+  launch_k(pf_w4_kernel<true>, dim3(mt8 * (a.f / 128)), dim3(kThreads), 0, s, a.ev[0], a.ev[1],
            a.x, a.sorted_pair, a.k, a.d, a.f, a.gu_codes, a.gu_scales, xsum,
-           (const PTile*)tiles, (const int*)num_tiles, a.f / 128, h, (float*)nullptr, hsum, 0, 0, (const float*)nullptr, (void*)nullptr);
+           (const PTile*)tiles, (const int*)num_tiles, a.f / 128, h, (float*)nullptr, hsum,
+           0, 0, (const float*)nullptr, (void*)nullptr);
   const int dn_fb = (a.d + 255) / 256;
-  launch_k(pf_w4_kernel<kPfDown>, dim3(mt8 * dn_fb), dim3(kThreads), 0, s, a.ev[2], a.ev[3],
+  launch_k(pf_w4_kernel<false>, dim3(mt8 * dn_fb), dim3(kThreads), 0, s, a.ev[2], a.ev[3],
            (const uint16_t*)h, a.sorted_pair, a.k, a.f, a.d, a.dn_codes, a.dn_scales,
            (const uint2*)hsum, (const PTile*)tiles, (const int*)num_tiles, dn_fb,
-           (uint16_t*)nullptr, a.y, (uint2*)nullptr, 0, 0, (const float*)nullptr, (void*)nullptr);
+           (uint16_t*)nullptr, a.y, (uint2*)nullptr, 0, 0, (const float*)nullptr,
+           (void*)nullptr);
   return hipGetLastError();
 }
 
@@ -1083,7 +1084,7 @@ hipError_t launch_linear_w4_gemm(const uint16_t* x, const uint8_t* codes, const 
   hipLaunchKernelGGL(group_sums, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, x,
                      (long long)T, K, xsum);
   const int nfb = (N + 255) / 256, pairs = (T + tile_tokens - 1) / tile_tokens * nfb;
-  auto kern = out_f32 ? pf_w4_kernel<kPfDenseF32> : pf_w4_kernel<kPfDenseBf16>;
+  auto kern = out_f32 ? pf_w4_kernel<false, true, false> : pf_w4_kernel<false, true, true>;
   hipLaunchKernelGGL(kern, dim3((pairs + 7) & ~7), dim3(kThreads), 0, s, x,
                      (const int32_t*)nullptr, 1, K, N, codes, scales, (const uint2*)xsum,
                      (const PTile*)nullptr, (const int*)nullptr, nfb, (uint16_t*)nullptr,

@@ -109,6 +109,7 @@ def test_linear_refusals(lib):
     assert f(K=200) == UNS and f(N=24) == UNS and f(group=64) == UNS
     assert f(T=-1) == INV and f(N=0) == INV and f(K=0) == INV and f(dt=2) == INV
     assert f(T=1 << 30, K=1 << 20) == UNS and f(T=1 << 30, N=1 << 20) == UNS
+    assert f(T=1 << 17, K=1 << 17) == UNS and f(T=1 << 17, N=1 << 17) == UNS  # 2^34
     for name in ("x", "c", "s", "out"):
         assert f(**{name: NULL}) == INV
     for name in ("x", "c", "out"):

@@ -1,14 +1,33 @@
 // Linear map with int4 weights: y = x W'^T (+ bias) for dense projections,
 // with the codes and group scales of the experts (W' = s q, group 128).
 //
-// Arithmetic.  A code word becomes eight bf16 values 192 + 8 q (w4_top); the
-// MFMA accumulator of every 128-group starts from -192 * sum(x over the
-// group), so the group's sum is 8 sum(q x) in fp32, and the fp16 scale / 8
-// (exact) weights it into the running fp32 total.  Weights are never rounded.
+// Arithmetic.  A code word becomes eight bf16 values 192 + 8 q (w4_top); every
+// 128-group's MFMA sum is corrected by -192 * sum(x over the group), which
+// leaves 8 sum(q x) in fp32, and the fp16 scale / 8 (exact) weights it into the
+// running fp32 total.  Weights are never rounded; the result is rounded once,
+// on store.
 //
 // Layout.  Lane (row r, quarter kq) of a wave reads bytes [16 kq, 16 kq + 16)
 // of row r of a 16-row tile's group: one 16-byte load per lane takes the
-// whole 1 KiB block.  The activations of token c sit in lanes (c, kq).
+// whole 1 KiB block.  The activations of token c sit in lanes (c, kq).  The
+// scale of row 4 q + i is loaded by lane i of each quad of lane row q and
+// reaches the quad by a lane permutation of the multiply's operand.
+//
+// Kernels.  Few tokens are bound by the codes' bytes, large batches by the
+// matrix cores; between them the conversion of codes (a VALU step per code and
+// token pass) and the activations, which every block reads whole, take as long
+// as either.  Measured (launches captured in a graph, weights rotated past the
+// Infinity Cache where they fit):
+//   tokens x K x N        us     bound
+//   1 x 2048 x 2048       3.2    launch
+//   1 x 4096 x 4096       4.4    launch and one round trip to HBM
+//   1 x 8192 x 8192       9.4    3.7 TB/s of codes
+//   4 x 4096 x 50304     22.6    4.7 TB/s (a large copy: 4.9)
+//   16 x 4096 x 12288     8.0    3.3 TB/s
+//   64 x 4096 x 12288    13.2    codes converted twice, activations 256 KB a CU
+//   512 x 4096 x 4096    27      638 TFLOP/s
+//   2501 x 4096 x 4096  104      806 TFLOP/s
+//   4096 x 4096 x 4096  141      977 TFLOP/s (a library bf16 product: 1225)
 #include <math.h>
 
 #include <algorithm>

@@ -192,12 +192,16 @@ __global__ __launch_bounds__(kThreads) void combine_residual_bwd_kernel(
 #pragma unroll
     for (int j = 0; j < KM; ++j)
       if (dtopk_w && j < a.k && (int)threadIdx.x == j)
-        dtopk_w[(size_t)t * a.k + j] = tg * rstd * (s[2 + j] - b * s[2 + KM + j]);
+        dtopk_w[(size_t)t * a.k + j] =
+            !pr.mask[j] ? 0.0f
+                        : tg * rstd * (post ? s[2 + j] - b * s[2 + KM + j] : s[2 + j]);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int c = threadIdx.x + kThreads * i;
       if (c < nch) {
-        const f32x8 g = (u[i] - o[i] * b) * (tg * rstd);
+        f32x8 g = u[i];
+        if (post) g -= o[i] * b;
+        g *= tg * rstd;
         if (dadd) store8<kF32>(dadd, base + 8 * c, g);
         if (dy) {
 #pragma unroll

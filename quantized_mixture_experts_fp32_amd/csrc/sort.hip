@@ -80,7 +80,8 @@ __global__ __launch_bounds__(kTh) void dispatch_bwd_kernel(
   block_sum<KM, kWaves>(dot, red);
 #pragma unroll
   for (int j = 0; j < KM; ++j)
-    if (j < k && (int)threadIdx.x == j) dtopk_w[(size_t)t * k + j] = dot[j];
+    if (j < k && (int)threadIdx.x == j)  // (an infinite x times a dropped row's zeros is NaN)
+      dtopk_w[(size_t)t * k + j] = pr.mask[j] ? dot[j] : 0.0f;
 }
 
 template <bool kDoF32, bool kDyF32, int KM>

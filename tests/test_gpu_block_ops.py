@@ -354,6 +354,38 @@ def test_block_gradient_against_differences():
         assert abs(num - float(ana.sum())) <= 1e-5 * float(ana.abs().sum()) + 1e-4, name
 
 
+@pytest.mark.parametrize("post", [False, True])
+def test_dropped_pairs_of_an_infinite_token(post):
+    """A dropped pair has the weight gradient 0 whatever its token's row holds."""
+    note(f"dropped pairs of an infinite token, post {post}")
+    normal = gen(5)
+    T, d, k = 3, 264, 3
+    pos = torch.tensor([0, -1, 1, 9, 2, 3, 4, 5, -1], dtype=torch.int32, device=DEV)
+    dropped = torch.tensor([[0, 1, 0], [1, 0, 0], [0, 0, 1]], dtype=torch.bool, device=DEV)
+    y, w = normal(T * k, d), torch.softmax(normal(T, k), 1)
+    x, dxs = normal(T, d), normal(T * k, d)
+    x[:, 17] = float("inf")
+    gain = 1 + 0.3 * normal(d) if post else None
+    dw = moe.moe_combine_residual_bwd(x, y, pos, w, post_gain=gain, eps=EPS).dtopk_w
+    assert (dw[dropped] == 0).all() and not torch.isfinite(dw[~dropped]).any()
+    for dw in (moe.moe_dispatch_bwd(dxs, pos, k, x=x, topk_w=w)[1],
+               moe.moe_combine_bwd(x, y, pos, w)[1]):
+        assert (dw[dropped] == 0).all() and torch.isinf(dw[~dropped]).all()
+
+
+def test_block_gradient_without_norm_does_not_square_the_output():
+    """Without a norm the gradient of o is gate * dout and no <o, y_j> enters:
+    rows of 1e25, whose squares have no fp32, leave it finite."""
+    note("block gradient without norm, large rows")
+    c = BlockCase(5, 264, 3, 8, F32, "token", False, False, True, 0.2, 0)
+    c.y *= 1e25
+    g = moe.moe_combine_residual_bwd(c.dout, c.y, c.pos, c.w, **c.kw())
+    r = ref.combine_residual_bwd(f64(c.dout), *c.refs(), EPS)
+    assert_within(g.dadd, *r["do"], "dadd")
+    assert_within(g.dtopk_w, *r["dw"], "dtopk_w")
+    assert_within(g.dgate, *r["dgate_t"], "dgate")
+
+
 # ------------------------------------------------------------------ token sort
 # (T, d, k, E, dtype, share of dropped pairs, padding)
 SORT = [(1, 8, 1, 1, BF, 0.0, 0), (1, 2048, 8, 64, F32, 0.0, 0), (3, 24, 2, 4, F32, 0.4, 1),

@@ -110,6 +110,7 @@ def test_linear_refusals(lib):
     assert f(T=-1) == INV and f(N=0) == INV and f(K=0) == INV and f(dt=2) == INV
     assert f(T=1 << 30, K=1 << 20) == UNS and f(T=1 << 30, N=1 << 20) == UNS
     assert f(T=1 << 17, K=1 << 17) == UNS and f(T=1 << 17, N=1 << 17) == UNS  # 2^34
+    assert f(T=1 << 23, K=128, N=16) == UNS and f(T=1, K=128, N=1 << 28) == UNS
     for name in ("x", "c", "s", "out"):
         assert f(**{name: NULL}) == INV
     for name in ("x", "c", "out"):

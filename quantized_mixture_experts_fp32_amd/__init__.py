@@ -516,8 +516,10 @@ def _addr(t):
 
 def _rows(fn, name, t, shape, dtypes, like=None):
     """Checks one tensor: its shape, that its dtype is one of `dtypes`, that it
-    is dense, and that it is on like's device (its own, a GPU, without)."""
+    is dense, that the ABI's 32-bit ints hold its sizes, and that it is on
+    like's device (its own, a GPU, without)."""
     if (t.shape == shape and t.dtype in dtypes and t.is_contiguous()
+            and max(shape, default=0) < 1 << 31
             and (t.is_cuda if like is None else t.device == like.device)):
         return t
     if t.shape != shape:
@@ -526,6 +528,8 @@ def _rows(fn, name, t, shape, dtypes, like=None):
         raise ValueError(f"{fn}: {name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not contiguous")
+    if max(shape, default=0) >= 1 << 31:
+        raise ValueError(f"{fn}: {name} has shape {tuple(shape)}, sizes must be below 2^31")
     raise ValueError(f"{fn}: {name} is on {t.device}, expected "
                      f"{'a GPU' if like is None else like.device}")
 

@@ -225,6 +225,8 @@ def test_binding_refusals():
     refused("expected a GPU", moe.moe_rmsnorm, x, gain)
     refused("float64", moe.moe_rmsnorm, x.double())
     refused("contiguous", moe.moe_rmsnorm, z(64, 4).t())
+    for shape in ((2 ** 32 + 5, 8), (1, 2 ** 32 + 8)):  # an int of 32 bits would wrap
+        refused("below 2", moe.moe_rmsnorm, torch.empty(shape, device="meta"))
     refused("dout must be", moe.moe_rmsnorm_bwd, gain, x)
     refused("expected a GPU", moe.moe_rmsnorm_bwd, x, x, gain)
     refused("x must be", moe.moe_linear_w4, gain, z(16, 32, dtype=torch.uint8), z(16, 1))

@@ -488,7 +488,7 @@ def _on_device(fn):
         if not isinstance(first, torch.Tensor):
             raise ValueError(f"{fn.__name__}: a tensor is needed, got {type(first).__name__}")
         if stream is None:
-            if not first.is_cuda or first.get_device() == torch._C._cuda_getDevice():
+            if not first.is_cuda or first.get_device() == _current_device():
                 return fn(first, *args, **kw)
             with torch.cuda.device(first.device):
                 return fn(first, *args, **kw)
@@ -503,6 +503,11 @@ def _on_device(fn):
             return fn(first, *args, **kw)
 
     return call
+
+
+def _current_device():
+    import torch
+    return torch._C._cuda_getDevice()
 
 
 def _raw_stream(t):
@@ -1035,7 +1040,19 @@ class MoeLayer:
                       next_out=None, path=MOE_PATH_AUTO, stream=None):
         """The layer as a residual block of a model: moe_rmsnorm of the
         residual stream, routing, expert FFN, and moe_combine_residual in the
-        place of the combine -> (out, next_out or None), as that call."""
+        place of the combine -> (out, next_out or None), as that call.
+        residual [T][d] (bf16 or fp32) on the layer's device."""
+        if residual.dim() != 2 or residual.shape[1] != self.d:
+            raise ValueError(f"forward_block: residual has shape {tuple(residual.shape)}, "
+                             f"expected [T][{self.d}]")
+        if residual.device != self.wr.device:
+            raise ValueError(f"forward_block: residual is on {residual.device}, the layer on "
+                             f"{self.wr.device}")
+        if residual.is_cuda and residual.get_device() != _current_device():
+            import torch
+            with torch.cuda.device(residual.device):
+                return self.forward_block(residual, gain, eps, add, post_gain, gate, gate_mode,
+                                          res_scale, next_gain, out, next_out, path, stream)
         T = residual.shape[0]
         x = moe_rmsnorm(residual, gain, eps=eps, stream=stream)
         if self._T != T:

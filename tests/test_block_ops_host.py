@@ -240,3 +240,17 @@ def test_binding_refusals():
     refused("must be", moe.moe_dispatch_bwd, z(7, 64), pos, 2)
     refused("must be", moe.moe_dispatch_bwd, y, pos, 0)
     refused("must be", moe.moe_combine_bwd, x, y, pos, gain)
+
+
+def test_block_layer_refusals():
+    """forward_block checks the residual before it allocates or launches: the
+    router reads its weights by the residual's width."""
+    wr = torch.zeros(8, 128)
+    layer = moe.MoeLayer(wr, None, 2, 128, None, None, None, None)
+    for bad in (torch.zeros(4, 256), torch.zeros(4, 64), torch.zeros(128)):
+        with pytest.raises(ValueError, match="expected .T..128."):
+            layer.forward_block(bad)
+    with pytest.raises(ValueError, match="residual is on meta"):
+        layer.forward_block(torch.empty(4, 128, device="meta"))
+    with pytest.raises(ValueError, match="expected a GPU"):
+        layer.forward_block(torch.zeros(4, 128))

@@ -655,7 +655,6 @@ def test_block_around_the_quantized_layer():
     assert_within(out, v, ev, "out")
     assert_within(nxt, rn, en, "next")
 
-
     # the layer's own method makes the same calls
     got = layer.forward_block(res, gains[0], post_gain=gains[1], res_scale=0.5, eps=EPS,
                               next_gain=gains[2])
@@ -663,6 +662,42 @@ def test_block_around_the_quantized_layer():
     plain, none = layer.forward_block(res, gains[0], eps=EPS)
     assert none is None
     assert_within(plain, f64(res) + f64(o), 8 * ref.U * o64.abs().max(), "plain block")
+
+
+@pytest.mark.parametrize("T", [1, 37])
+def test_block_layer_on_a_stream_and_captured(T):
+    """forward_block with bf16 and fp32 residuals, in place, on a side stream
+    and replayed from a graph, equals the eager call."""
+    note(f"forward_block T={T}: stream, graph")
+    d, E, k, f = 512, 8, 2, 256
+    normal = gen(60 + T)
+    wr = (normal(E, d) / d ** 0.5).to(BF)
+    gu = moe.moe_quantize_w4((normal(E, 2 * f, d) / d ** 0.5).contiguous())
+    dn = moe.moe_quantize_w4((normal(E, d, f) / f ** 0.5).contiguous())
+    layer = moe.MoeLayer(wr, None, k, f, *gu, *dn)
+    gain, nxt, gate = 1 + 0.2 * normal(d), 1 + 0.2 * normal(d), normal(d)
+    kw = dict(gate=gate, gate_mode=moe.MOE_GATE_CHANNEL, post_gain=gain, next_gain=nxt, eps=EPS)
+    for dtype in (BF, F32):
+        res = normal(T, d, dtype=dtype)
+        want = layer.forward_block(res, gain, **kw)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = layer.forward_block(res, gain, stream=side, **kw)
+        side.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        graph, buf = torch.cuda.CUDAGraph(), res.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            out, nout = layer.forward_block(buf, gain, out=buf, **kw)
+        assert out is buf
+        for _ in range(3):
+            buf.copy_(res)
+            graph.replay()
+            torch.cuda.synchronize()
+            again = layer.forward_block(res, gain, **kw)
+            torch.cuda.synchronize()
+            assert torch.equal(buf, want[0]) and torch.equal(nout, want[1])
+            assert torch.equal(again[0], want[0])
 
 
 def test_gpu_argument_checks():

@@ -495,8 +495,10 @@ int moe_retile_bitplane8(const uint8_t *planes_canonical, int E, int N, int K,
  * next to them; these calls take and return what the calls above do.
  * Dtype arguments are MOE_OUT_BF16 or MOE_OUT_F32.  Arrays are dense and
  * row-major; arrays of rows, gains and channel gates are 16-byte aligned, all
- * others (and the gradients of gains and gates) 4-byte.  Unless said otherwise outputs must not overlap inputs.  T == 0 writes only the
- * gradients of gains and channel gates (zeros).
+ * others (and the gradients of gains and gates) 4-byte.  Unless said otherwise
+ * outputs must not overlap inputs.  T == 0 writes only the gradients of gains
+ * and channel gates (zeros).  A row's sums (of squares, of products with a
+ * gradient) are fp32 and must stay below 2^128.
  *
  * moe_linear_w4 -- y = x W'^T + bias with symmetric group-128 int4 weights.
  *   out[t][n] = sum_g s[n][g] sum_{i in group g} q[n][i] x[t][i] + bias[n]
@@ -548,7 +550,7 @@ int moe_rmsnorm_bwd(const void *dout, int dout_dtype, const void *x, int x_dtype
  *   out  = v;   next_out = v * rstd(v) * next_gain
  * y_pairs fp32 [T*k][d], pair_pos int32 [T*k], topk_w fp32 [T][k] as for
  * moe_combine.  A pair whose pair_pos is outside [0, T*k) (e.g. -1, a padding
- * token's) is dropped: its weight and row are not read.  k = 0: no routed
+ * token's) is dropped: its weight and what any row holds do not enter.  k = 0: no routed
  * pairs (y_pairs, pair_pos, topk_w NULL), the block's output is add alone.
  * add [T][d] (a shared expert's or dense block's output) or NULL; residual,
  * add and out are of `dtype`; gate fp32 [T] or [d] by gate_mode, NULL for

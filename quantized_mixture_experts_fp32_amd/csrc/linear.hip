@@ -14,20 +14,22 @@
 // reaches the quad by a lane permutation of the multiply's operand.
 //
 // Kernels.  Few tokens are bound by the codes' bytes, large batches by the
-// matrix cores; between them the conversion of codes (a VALU step per code and
-// token pass) and the activations, which every block reads whole, take as long
-// as either.  Measured (launches captured in a graph, weights rotated past the
-// Infinity Cache where they fit):
+// matrix cores; between them the issue of instructions counts: the conversion
+// of codes (a VALU step per code and token block), the activations, which every
+// block reads whole, and the MFMAs run one after the other in a wave.  Measured
+// (launches captured in a graph, weights rotated past the Infinity Cache where
+// they fit):
 //   tokens x K x N        us     bound
-//   1 x 2048 x 2048       3.2    launch
-//   1 x 4096 x 4096       4.4    launch and one round trip to HBM
-//   1 x 8192 x 8192       9.4    3.7 TB/s of codes
-//   4 x 4096 x 50304     22.6    4.7 TB/s (a large copy: 4.9)
-//   16 x 4096 x 12288     8.0    3.3 TB/s
-//   64 x 4096 x 12288    13.2    codes converted twice, activations 256 KB a CU
-//   512 x 4096 x 4096    27      638 TFLOP/s
+//   1 x 2048 x 2048       3.0    launch
+//   1 x 4096 x 4096       4.3    launch and one round trip to HBM
+//   1 x 8192 x 8192       8.8    3.9 TB/s of codes
+//   4 x 4096 x 50304     22.5    4.7 TB/s (a large copy: 4.9)
+//   16 x 4096 x 12288     7.2    3.7 TB/s
+//   64 x 4096 x 12288    11.5    issue: without any memory traffic 0.8 us less
+//   64 x 4096 x 50304    41      issue: without any memory traffic 35
+//   512 x 4096 x 4096    23.7    725 TFLOP/s
 //   2501 x 4096 x 4096  104      806 TFLOP/s
-//   4096 x 4096 x 4096  141      977 TFLOP/s (a library bf16 product: 1225)
+//   4096 x 4096 x 4096  141      970 TFLOP/s (a library bf16 product: 1225)
 #include <math.h>
 
 #include <algorithm>
@@ -84,15 +86,13 @@ struct XPiece {
     }
   };
   // rows t0 + 4 i + lane / 16 of the 16 from t0 on, chunk lane % 16
-  // (mask 0: one word of the first chunk instead, a load for nothing)
-  __device__ __forceinline__ void load(const uint16_t* x, int t0, int T, int K, int g, Lane& l,
-                                       uint32_t mask = ~0u) {
+  __device__ __forceinline__ void load(const uint16_t* x, int t0, int T, int K, int g, Lane& l) {
     asm volatile("" : "+v"(l.full), "+v"(l.last));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = min(t0 + 4 * i, (T - 1) & ~3);
       const char* b = (const char*)(x + (size_t)t * K + 128 * g);
-      v[i] = *(const u32x4*)(b + ((t + 4 <= T ? l.full : l.last) & mask));
+      v[i] = *(const u32x4*)(b + (t + 4 <= T ? l.full : l.last));
     }
   }
   __device__ __forceinline__ void turn(u32x4* buf, int lane, bf16x8 (&f)[4]) const {
@@ -248,85 +248,152 @@ __global__ __launch_bounds__(W * kWave) void linear_w4_stream(
   }
 }
 
+// Calls f with the integral constants 0 .. N - 1.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
+// Lane n of every row of 16 lanes to all lanes of the row.
+template <int n>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + n, 0xF, 0xF, true);
+}
+
 // Tile kernel.  A block computes 16 RT features of 16 NT tokens; its W waves
-// take the 128-groups of K in turn (wave w those of w, w + W, ..) and stream
-// codes and activations into registers, one group ahead; the waves' totals
-// are joined once, through LDS in wave order.  (The loop is kept small: with
-// more groups in flight its code grows, and at 3 to 10 us a call fetching it
-// costs more than the deeper queue gives.)
+// take the 128-groups of K in turn (wave w those of w, w + W, ..), and the
+// waves' totals are joined once, through LDS in wave order.  Of its group a
+// wave holds the codes in registers and the activations in 4 NT KiB of LDS of
+// its own, both asked for one group ahead.  The activations go to LDS directly
+// (no registers, and no stores to issue: 64 tokens x 4096 x 12288 11.6 us,
+// through registers 13.2), in whole 256-byte row pieces, chunk c of token t at
+// position c ^ t: no bank conflicts.  One scale load serves four row tiles,
+// lane 4 r + i of a row of 16 lanes holding row 4 kq + i of tile r.
+//
+// The compiler does not follow direct loads into LDS, so the waits are written
+// out: all of a group's loads are waited for before its pieces are read, and
+// the reads before the next group's loads may overwrite them.  Only this wave
+// touches its pieces.
 template <int W, int NT, int RT, bool kOutF32>
 __global__ __launch_bounds__(W * kWave) void linear_w4_tile(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ codes,
     const uint16_t* __restrict__ scales, const float* __restrict__ bias, int T, int N, int K,
     int ntb, void* __restrict__ out) {
-  extern __shared__ f32x4 lds[];  // x pieces [W][256], then totals [W][RT * NT][64]
+  extern __shared__ f32x4 lds[];  // x pieces [W][NT][256], then totals [W][RT * NT][64]
+  constexpr int RS = (RT + 3) / 4;  // scale loads, of four row tiles each
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, kq = lane >> 4, G = K >> 7, ntile = N >> 4;
-  // the token blocks of one row block run next to each other on one XCD
-  const int id = blockIdx.x;
-  const int rb = ((id >> 3) / ntb) * 8 + (id & 7), t0 = ((id >> 3) % ntb) * 16 * NT;
-  if (rb * RT >= ntile) return;
-  uint32_t lane_code = 64 * col + 16 * kq, lane_scale = (4 * kq + (col & 3)) * G * 2;
+  // The token blocks of one row block run next to each other on one XCD, which
+  // then reads the codes once; the row blocks past a multiple of the eight XCDs
+  // are dealt over all of them (700 tokens x 4096 x 1024: 12.4 us, on the first
+  // XCDs 19.6).
+  const int id = blockIdx.x, nrb = (ntile + RT - 1) / RT, rest = nrb & 7;
+  const int first = (nrb - rest) * ntb;  // blocks of the row blocks that come in eights
+  const bool even = id < first;
+  const int rb = even ? ((id >> 3) / ntb) * 8 + (id & 7) : nrb - rest + (id - first) % rest;
+  const int t0 = (even ? (id >> 3) % ntb : (id - first) / rest) * 16 * NT;
+  uint32_t lane_code = 64 * col + 16 * kq, lane_scale[RS];
   const uint8_t* cb[RT];
-  const uint16_t* sb[RT];
+  const uint16_t* sb = scales + (size_t)(rb * RT) * 16 * G;
 #pragma unroll
   for (int r = 0; r < RT; ++r) {  // tiles past the last one repeat it, unstored
     const int n0 = min(rb * RT + r, ntile - 1) << 4;
     cb[r] = codes + (size_t)n0 * (K >> 1);
-    sb[r] = scales + (size_t)n0 * G;
   }
-  XPiece px[NT];
-  XPiece::Lane xlane(T, K, lane);
+#pragma unroll
+  for (int r = 0; r < RS; ++r) {
+    const int tile = min(min(4 * r + (col >> 2), RT - 1), ntile - 1 - rb * RT);
+    lane_scale[r] = (16 * tile + 4 * kq + (col & 3)) * G * 2;
+  }
+  u32x4* xl = (u32x4*)lds + wave * (NT * 256);
+  const char* xb = (const char*)(x + (size_t)t0 * K);
+  uint32_t xoff[NT][4];
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 4 * i + (lane >> 4);
+      xoff[c][i] = (uint32_t)min(16 * c + t, T - 1 - t0) * K * 2 + 16 * ((lane & 15) ^ t);
+    }
   struct Codes {
     u32x4 q[RT];
-    _Float16 sc[RT];
+    _Float16 sc[RS];
   };
   // Loads past the wave's last group read one word for nothing: a load under
   // a branch would make the compiler wait for all loads in flight.
   auto load_codes = [&](int g, Codes& f) {
     const uint32_t mask = g < G ? ~0u : 0u;
     const int gc = min(g, G - 1);
-    asm volatile("" : "+v"(lane_code), "+v"(lane_scale));
+    asm volatile("" : "+v"(lane_code));
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
+    for (int r = 0; r < RT; ++r)
       f.q[r] = *(const u32x4*)(cb[r] + (size_t)1024 * gc + (lane_code & mask));
-      f.sc[r] = *(const _Float16*)((const char*)(sb[r] + gc) + (lane_scale & mask));
+#pragma unroll
+    for (int r = 0; r < RS; ++r) {
+      asm volatile("" : "+v"(lane_scale[r]));
+      f.sc[r] = *(const _Float16*)((const char*)(sb + gc) + (lane_scale[r] & mask));
     }
   };
   auto load_x = [&](int g) {
+    const uint32_t mask = g < G ? ~0u : 0u;
+    const char* b = xb + (size_t)256 * min(g, G - 1);
 #pragma unroll
     for (int c = 0; c < NT; ++c)
-      px[c].load(x, t0 + 16 * c, T, K, min(g, G - 1), xlane, g < G ? ~0u : 0u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o = xoff[c][i] & mask;
+        asm volatile("" : "+v"(o));
+        __builtin_amdgcn_global_load_lds(
+            b + o, (__attribute__((address_space(3))) void*)(xl + c * 256 + i * 64), 16, 0, 0);
+      }
   };
   f32x4 acc[RT][NT];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int c = 0; c < NT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // Group g from f and px.  Loads return in order, so the activations of the
-  // next group are asked for before the codes of the one after it: waiting
-  // for the former leaves the latter, which come from HBM, in flight.
-  auto step = [&](int g, Codes& f) {
+  auto step = [&](int g, Codes& f, Codes& next) {
     bf16x8 xf[NT][4];
+    // group g's pieces and codes, issued one group ago, have landed ..
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int c = 0; c < NT; ++c) px[c].turn((u32x4*)lds + 256 * wave, lane, xf[c]);
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        xf[c][m] = as_bf16x8(xl[c * 256 + col * 16 + ((4 * kq + m) ^ col)]);
+    // .. and are in registers before the next group's overwrite them
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
     load_x(g + W);
+    load_codes(g + W, next);
     __builtin_amdgcn_sched_barrier(0);
     f32x4 seed[NT];  // -192 * sum of token col's group, in every row
     u32x4 neg;
     neg = kNegOffset;
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      seed[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < NT; ++c) seed[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int m = 0; m < 4; ++m) seed[c] = mfma16(as_bf16x8(neg), xf[c][m], seed[c]);
-    }
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const uint32_t sv = __float_as_uint(0.125f * (float)f.sc[r]);
-      const float s[4] = {__uint_as_float(quad_lane<0>(sv)), __uint_as_float(quad_lane<1>(sv)),
-                          __uint_as_float(quad_lane<2>(sv)), __uint_as_float(quad_lane<3>(sv))};
+      for (int c = 0; c < NT; ++c) seed[c] = mfma16(as_bf16x8(neg), xf[c][m], seed[c]);
+    uint32_t sv[RS];
+#pragma unroll
+    for (int r = 0; r < RS; ++r) sv[r] = __float_as_uint(0.125f * (float)f.sc[r]);
+    static_for<RT>([&](auto rc) {
+      constexpr int r = decltype(rc)::value, b = 4 * (r & 3);
+      const float s[4] = {__uint_as_float(row_lane<b>(sv[r >> 2])),
+                          __uint_as_float(row_lane<b + 1>(sv[r >> 2])),
+                          __uint_as_float(row_lane<b + 2>(sv[r >> 2])),
+                          __uint_as_float(row_lane<b + 3>(sv[r >> 2]))};
       f32x4 p[NT];
 #pragma unroll
       for (int c = 0; c < NT; ++c) p[c] = seed[c];
@@ -340,25 +407,23 @@ __global__ __launch_bounds__(W * kWave) void linear_w4_tile(
       for (int c = 0; c < NT; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[r][c][i] = fmaf(s[i], p[c][i], acc[r][c][i]);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    load_codes(g + 2 * W, f);
+    });
     __builtin_amdgcn_sched_barrier(0);
   };
   if (wave < G) {
     Codes a, b;
-    load_codes(wave, a);
-    __builtin_amdgcn_sched_barrier(0);
     load_x(wave);
-    __builtin_amdgcn_sched_barrier(0);
-    load_codes(wave + W, b);
-    __builtin_amdgcn_sched_barrier(0);
+    load_codes(wave, a);
     int g = wave;
     for (; g + W < G; g += 2 * W) {
-      step(g, a);
-      step(g + W, b);
+      step(g, a, b);
+      step(g + W, b, a);
     }
-    if (g < G) step(g, a);
+    if (g < G) step(g, a, b);
+    // the loads for nothing past the last group still write this wave's pieces
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    asm volatile("" ::: "memory");
   }
   __syncthreads();
 #pragma unroll
@@ -381,10 +446,18 @@ hipError_t tile_as(const uint16_t* x, const uint8_t* codes, const uint16_t* scal
                    hipStream_t s) {
   const int ntb = (T + 16 * NT - 1) / (16 * NT), nrb = ((N >> 4) + RT - 1) / RT;
   auto kern = out_f32 ? linear_w4_tile<W, NT, RT, true> : linear_w4_tile<W, NT, RT, false>;
-  hipLaunchKernelGGL(kern, dim3(((nrb + 7) & ~7) * ntb), dim3(W * kWave),
-                     sizeof(f32x4) * 64 * W * std::max(RT * NT, 4), s, x, codes, scales, bias, T,
-                     N, K, ntb, out);
+  hipLaunchKernelGGL(kern, dim3(nrb * ntb), dim3(W * kWave),
+                     sizeof(f32x4) * 64 * W * std::max(RT * NT, 4 * NT), s, x, codes, scales,
+                     bias, T, N, K, ntb, out);
   return hipGetLastError();
+}
+
+// Blocks of the streaming kernel per token pass: one a CU over all passes, more
+// where LDS would not hold a block's tiles; a multiple of 8 for the XCDs.
+int stream_slots(int ntile, int npass, int nchunk) {
+  const int most = nchunk > 1 ? kMaxTotals : kMaxTiles;
+  const int n = std::max(std::max(kCUs / npass & ~7, 8), (ntile + most - 1) / most);
+  return (std::min(n, ntile) + 7) & ~7;
 }
 
 template <int W, int NT, int NG, int D>
@@ -393,88 +466,121 @@ hipError_t stream_as(const uint16_t* x, const uint8_t* codes, const uint16_t* sc
                      hipStream_t s) {
   const int G = K >> 7, ntile = N >> 4, npass = (T + 16 * NT - 1) / (16 * NT);
   const int nchunk = (G + W * NG - 1) / (W * NG), gpc = (G + nchunk - 1) / nchunk;
-  // one block a CU over all passes, more where LDS would not hold its tiles
-  const int most = nchunk > 1 ? kMaxTotals : kMaxTiles;
-  int nslot = std::max((kCUs + npass - 1) / npass, (ntile + most - 1) / most);
-  nslot = (std::min(nslot, ntile) + 7) & ~7;
+  const int nslot = stream_slots(ntile, npass, nchunk);
   const size_t lds = sizeof(f32x4) * (W * 64 * (NT > 2 ? 2 * NT : 4) + 4 * kMaxTiles +
                                       (nchunk > 1 ? 64 * NT * kMaxTotals : 0));
-  // a block with one tile has nothing to load ahead
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3(nslot * npass), dim3((W * kWave)), lds, s, x, codes, scales, bias,
-                       T, N, K, npass, nchunk, gpc, out);
-  };
-  if (ntile <= nslot)
-    out_f32 ? go(linear_w4_stream<W, NT, NG, 1, true>) : go(linear_w4_stream<W, NT, NG, 1, false>);
-  else
-    out_f32 ? go(linear_w4_stream<W, NT, NG, D, true>) : go(linear_w4_stream<W, NT, NG, D, false>);
+  auto kern =
+      out_f32 ? linear_w4_stream<W, NT, NG, D, true> : linear_w4_stream<W, NT, NG, D, false>;
+  hipLaunchKernelGGL(kern, dim3(nslot * npass), dim3(W * kWave), lds, s, x, codes, scales, bias, T,
+                     N, K, npass, nchunk, gpc, out);
   return hipGetLastError();
+}
+
+typedef hipError_t (*RunFn)(const uint16_t*, const uint8_t*, const uint16_t*, const float*, int,
+                            int, int, void*, int, hipStream_t);
+
+// A tile kernel and its time, which goes by blocks a CU: at K = 4096 (32
+// groups) `fixed` + `per` for each block a CU, and 0.065 us per MB of codes.
+// Fitted to 480 shapes of 1 to 512 tokens, K 512 to 14336, N 512 to 50304 (a
+// tenth off on most); the choices by it take 2 % longer than the best kernel
+// of each shape on average.  For up to 1024 inputs (8 groups) four waves do.
+struct Tile {
+  int tokens, rows, min_groups, max_groups;
+  float fixed, per;
+  RunFn run;
+};
+const Tile kTiles[] = {
+    {16, 1, 1, 1 << 30, 2.3f, 1.85f, tile_as<8, 1, 1>},
+    {16, 2, 1, 8, 2.4f, 2.6f, tile_as<4, 1, 2>},
+    {16, 2, 9, 1 << 30, 2.4f, 2.5f, tile_as<8, 1, 2>},
+    {16, 3, 9, 1 << 30, 2.7f, 3.15f, tile_as<8, 1, 3>},
+    {32, 2, 1, 1 << 30, 2.8f, 3.75f, tile_as<4, 2, 2>},
+    {32, 3, 1, 1 << 30, 3.1f, 4.55f, tile_as<4, 2, 3>},
+    {32, 4, 1, 1 << 30, 3.0f, 5.9f, tile_as<4, 2, 4>},
+    {32, 6, 1, 1 << 30, 3.4f, 7.65f, tile_as<4, 2, 6>},
+    {48, 4, 1, 1 << 30, 3.6f, 7.5f, tile_as<4, 3, 4>},
+    {64, 4, 1, 1 << 30, 4.4f, 9.3f, tile_as<4, 4, 4>},
+};
+
+struct Choice {
+  const Tile* tile;  // a tile kernel, or
+  int gemm_tokens;   // the GEMM in tiles of so many tokens, or (0) streaming
+};
+
+Choice choose(int T, int N, int K) {
+  const int G = K >> 7, ntile = N >> 4;
+  auto up = [](long long a, long long b) { return (a + b - 1) / b; };
+  Choice c = {nullptr, 0};
+  float best = 1e30f;
+  // The token blocks of a row block run next to each other, and past some 640
+  // tokens their activations do not stay in an XCD's L2: 1.17 times the time
+  // at 1024 tokens, 1.41 at 1536, 1.85 at 2501.
+  const float crowd = 1.0f + std::max(T - 640, 0) / 2200.0f;
+  for (const Tile& t : kTiles) {
+    if (G < t.min_groups || G > t.max_groups) continue;
+    const float per_cu = (float)up(up(T, t.tokens) * up(ntile, t.rows), kCUs);
+    const float us = t.fixed + t.per * crowd * per_cu * G / 32 + 0.0325e-6f * N * K;
+    if (us < best) {
+      best = us;
+      c.tile = &t;
+    }
+  }
+  // Streaming: the prologue, which goes by K, and a block's row tiles.  It
+  // reads the activations once a block: 4 tokens x 4096 x 50304 22.5 us
+  // (tiled 23.1), 16 tokens 23.2 (27.9), 64 tokens 41 (48.9).
+  // (For few tokens and up to 2048 inputs the tile kernel is the faster one.)
+  if (G > (T <= 16 ? 16 : 8)) {
+    const int npass = (int)up(T, T <= 16 ? 16 : 32);
+    const int nslot = stream_slots(ntile, npass, (int)up(G, G <= 16 ? 16 : 32));
+    const float tiles = crowd * up(ntile, nslot) * up((long long)nslot * npass, kCUs);
+    const float us = T <= 16 ? 1.2f + 0.165f * G + tiles * (0.45f + 0.025f * G)
+                             : 5.0f + 0.165f * G + tiles * (0.18f + 0.033f * G);
+    if (us < best) {
+      best = us;
+      c.tile = nullptr;
+    }
+  }
+  // GEMM (blocks of 256 features, two a CU): at K = 4096, one block a CU and
+  // two, tiles of 64 tokens 50 and 81 us, of 96 68 and 112, of 128 83 and 140,
+  // plus about 4 for the group sums.  E.g. N = 4096: 1024 tokens 49 us as
+  // 64-token tiles of the tile kernel, 52 us here; 2501 tokens 104 us in tiles
+  // of 96, 116 us in tiles of 128.
+  if (T > 64) {
+    static const struct {
+      int tokens;
+      float one, two;
+    } kGemm[] = {{128, 83.0f, 140.0f}, {96, 68.0f, 112.0f}, {64, 50.0f, 81.0f}};
+    for (const auto& t : kGemm) {
+      const float per_cu = (float)up(up(T, t.tokens) * up(N, 256), kCUs);
+      const float us = (per_cu <= 1.0f ? t.one : 0.5f * per_cu * t.two) * (K / 4096.0f) + 4.0f;
+      if (us < best) {
+        best = us;
+        c.tile = nullptr;
+        c.gemm_tokens = t.tokens;
+      }
+    }
+  }
+  return c;
 }
 
 }  // namespace
 
-// Tokens per tile of the GEMM kernel (blocks of 256 features, two a CU) where
-// it is the faster one, otherwise 0.  Its time goes by blocks a CU; measured
-// at K = 4096 (us, one block a CU and two): tiles of 64 tokens 50 and 81, of 96
-// 68 and 112, of 128 83 and 140, plus about 4 for the group sums.  The kernels
-// below take 2.9e-9 us per token, feature and input (3.2e-9 for K <= 2048,
-// 4.6e-9 for K <= 1024).  E.g. N = 4096: 1024 tokens 49 us streamed, 52 us in
-// tiles of 64; 2501 tokens 104 us in tiles of 96, 116 us in tiles of 128.
-static int gemm_tile(int T, int N, int K) {
-  if (T <= 64) return 0;
-  static const struct {
-    int tokens;
-    float one, two;
-  } kTiles[] = {{128, 83.0f, 140.0f}, {96, 68.0f, 112.0f}, {64, 50.0f, 81.0f}};
-  const float per = K <= 1024 ? 4.6e-9f : K <= 2048 ? 3.2e-9f : 2.9e-9f;
-  float best = per * (float)((T + 31) / 32 * 32) * N * K;
-  int tokens = 0;
-  for (const auto& t : kTiles) {
-    const float blocks = (float)((T + t.tokens - 1) / t.tokens) * ((N + 255) / 256);
-    const float per_cu = ceilf(blocks / kCUs);
-    const float us = (per_cu <= 1.0f ? t.one : 0.5f * per_cu * t.two) * (K / 4096.0f) + 4.0f;
-    if (us < best) {
-      best = us;
-      tokens = t.tokens;
-    }
-  }
-  return tokens;
-}
-
 size_t linear_w4_ws_bytes(int T, int N, int K) {
-  return gemm_tile(T, N, K) ? linear_w4_gemm_ws_bytes(T, K) : 0;
+  return choose(T, N, K).gemm_tokens ? linear_w4_gemm_ws_bytes(T, K) : 0;
 }
 
 hipError_t launch_linear_w4(const uint16_t* x, const uint8_t* codes, const uint16_t* scales,
                             const float* bias, int T, int N, int K, void* out, int out_f32,
                             void* ws, hipStream_t s) {
-  if (const int tokens = gemm_tile(T, N, K))
-    return launch_linear_w4_gemm(x, codes, scales, bias, T, N, K, tokens, out, out_f32, ws, s);
-  auto as = [&](auto f) { return f(x, codes, scales, bias, T, N, K, out, out_f32, s); };
-  const int G = K >> 7, ntile = N >> 4;
-  if (T <= 16) {
-    // Tile kernel while every row tile is taken at once, by a block of one to
-    // three tiles a CU (K <= 1024: by two of four waves, 50304 features of 4
-    // tokens 8.7 us, streamed 12.6); with more, the streaming kernel, which
-    // reads x once a block (K = 4096, N = 50304: 22.5 us, tiled 26).
-    if (ntile <= kCUs) return G >= 96 ? as(tile_as<16, 1, 1>) : as(tile_as<8, 1, 1>);
-    if (G <= 8) return as(tile_as<4, 1, 2>);
-    if (ntile <= 2 * kCUs) return as(tile_as<8, 1, 2>);
-    if (ntile <= 5 * kCUs) return as(tile_as<8, 1, 3>);
-    return G <= 16 ? as(stream_as<16, 1, 1, 2>) : as(stream_as<16, 1, 2, 2>);
-  }
-  // 32 tokens a block or pass.  Tile kernel up to 8 row tiles a CU (and for a
-  // K that would leave streaming waves idle), with as many tiles a block as
-  // leave one or two blocks a CU; beyond, the streaming kernel.  At K = 4096:
-  // 64 tokens, N = 50304: 42 us streamed, 52 us tiled; 512 tokens, N = 4096: 27
-  // and 29 us; 128 tokens: 11.2 and 10.4 us; 64 tokens, N = 12288: 13.2 us with
-  // six tiles, 15.7 us with four.
-  const int units = (int)std::min<long long>(
-      ((long long)ntile * ((T + 31) / 32) + kCUs - 1) / kCUs, 1 << 30);
-  if (units <= 2) return as(tile_as<8, 2, 2>);
-  if (units == 5 || units == 6) return as(tile_as<4, 2, 6>);
-  if (units <= 8 || G <= 8) return as(tile_as<4, 2, 4>);
-  return G <= 16 ? as(stream_as<16, 2, 1, 2>) : as(stream_as<16, 2, 2, 1>);
+  const Choice c = choose(T, N, K);
+  if (c.gemm_tokens)
+    return launch_linear_w4_gemm(x, codes, scales, bias, T, N, K, c.gemm_tokens, out, out_f32, ws,
+                                 s);
+  const RunFn run = c.tile          ? c.tile->run
+                    : T <= 16        ? stream_as<16, 1, 2, 2>
+                    : K <= 16 * 128 ? stream_as<16, 2, 1, 2>
+                                    : stream_as<16, 2, 2, 1>;
+  return run(x, codes, scales, bias, T, N, K, out, out_f32, s);
 }
 
 }  // namespace moe

@@ -70,7 +70,15 @@ LINEAR = [(1, 128, 16), (1, 2048, 2048), (2, 384, 48), (5, 4096, 272), (16, 1024
           # token passes: six tiles a block, streamed
           (40, 640, 10256), (70, 1152, 12304), (70, 2176, 12304), (40, 4352, 24592),
           # GEMM tiles of 64, 96 and 128 tokens, N ending inside a feature block
-          (1500, 640, 4112), (2501, 640, 2064), (1500, 256, 8208)]
+          (1500, 640, 4112), (2501, 640, 2064), (1500, 256, 8208),
+          # tiles of 32, 48 and 64 tokens by two to six row tiles
+          (2501, 1408, 64), (64, 640, 976), (387, 640, 976), (33, 640, 13696), (97, 2304, 6224),
+          (191, 4224, 4112),
+          # few tokens streamed over one and several chunks of K, token passes
+          (3, 3200, 26608), (16, 4224, 24912), (17, 1664, 50480), (17, 2176, 49216),
+          (45, 2176, 49232), (19, 5248, 25712),
+          # the GEMM for short K
+          (2501, 128, 6160), (97, 256, 61664), (3001, 256, 3856)]
 
 
 def linear_inputs(T, K, N, seed=0):

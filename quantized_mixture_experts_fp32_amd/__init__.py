@@ -521,11 +521,12 @@ def _addr(t):
 
 def _rows(fn, name, t, shape, dtypes, like=None):
     """Checks one tensor: its shape, that its dtype is one of `dtypes`, that it
-    is dense, that the ABI's 32-bit ints hold its sizes, and that it is on
-    like's device (its own, a GPU, without)."""
-    if (t.shape == shape and t.dtype in dtypes and t.is_contiguous()
-            and max(shape, default=0) < 1 << 31
-            and (t.is_cuda if like is None else t.device == like.device)):
+    is dense, and that it is on like's device.  Without like it is the call's
+    first tensor, which must be on a GPU and whose sizes (the other tensors
+    have them too) the ABI's 32-bit ints must hold."""
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous() and (
+            t.is_cuda and max(shape) < 1 << 31 if like is None
+            else t.get_device() == like.get_device()):
         return t
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
@@ -533,7 +534,7 @@ def _rows(fn, name, t, shape, dtypes, like=None):
         raise ValueError(f"{fn}: {name} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not contiguous")
-    if max(shape, default=0) >= 1 << 31:
+    if like is None and max(shape) >= 1 << 31:
         raise ValueError(f"{fn}: {name} has shape {tuple(shape)}, sizes must be below 2^31")
     raise ValueError(f"{fn}: {name} is on {t.device}, expected "
                      f"{'a GPU' if like is None else like.device}")
@@ -598,6 +599,8 @@ def moe_linear_w4(x, codes, scales, bias=None, out=None, out_dtype=MOE_OUT_BF16,
         raise ValueError(f"{fn}: x must be [T][K] and codes [N][K/2]")
     T, K = x.shape
     N = codes.shape[-2]
+    if N >= 1 << 31:
+        raise ValueError(f"{fn}: codes have {N} rows, sizes must be below 2^31")
     lead = (1,) * (codes.dim() - 2)
     _rows(fn, "x", x, (T, K), bf)
     _rows(fn, "codes", codes, lead + (N, K // 2), (torch.uint8,), x)
@@ -677,6 +680,8 @@ def _block_inputs(fn, rows, y_pairs, pair_pos, topk_w, add, post_gain, gate, gat
         if pair_pos is None or topk_w is None or topk_w.dim() != 2:
             raise ValueError(f"{fn}: y_pairs needs pair_pos [T*k] and topk_w [T][k]")
         k = topk_w.shape[1]
+        if k >= 1 << 31:
+            raise ValueError(f"{fn}: k = {k}, sizes must be below 2^31")
         _rows(fn, "topk_w", topk_w, (T, k), f32, rows)
         _rows(fn, "y_pairs", y_pairs, (T * k, d), f32, rows)
         if pair_pos.numel() != T * k:
@@ -777,6 +782,8 @@ def moe_combine_residual_bwd(dout, y_pairs=None, pair_pos=None, topk_w=None, add
 
 def _sort_inputs(fn, T, k, pair_pos, topk_w, like):
     _, _, f32, i32 = _types()
+    if not -1 << 31 <= k < 1 << 31:
+        raise ValueError(f"{fn}: k = {k}, sizes must be below 2^31")
     if pair_pos.numel() != T * k:
         raise ValueError(f"{fn}: pair_pos has {pair_pos.numel()} entries, expected {T * k}")
     _rows(fn, "pair_pos", pair_pos, tuple(pair_pos.shape), i32, like)

@@ -717,6 +717,8 @@ def test_gpu_argument_checks():
         moe.moe_rmsnorm(x, torch.ones(64))
     with pytest.raises(ValueError, match="not contiguous"):
         moe.moe_rmsnorm(torch.zeros(64, 4, device=DEV).t())
+    with pytest.raises(ValueError, match="below 2"):   # an int of 32 bits would wrap
+        moe.moe_dispatch(x, torch.zeros(8, dtype=torch.int32, device=DEV), 2 ** 32 + 2)
     with pytest.raises(moe.MoeError, match="misaligned"):
         moe.moe_rmsnorm(torch.zeros(4 * 64 + 1, device=DEV)[1:].view(4, 64))
     with pytest.raises(moe.MoeError, match="multiple of 8"):

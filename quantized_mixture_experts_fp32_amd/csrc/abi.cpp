@@ -528,7 +528,7 @@ static int colsum_ws_check(const char* what, bool wanted, size_t need, const voi
 }
 
 size_t moe_linear_w4_ws_bytes(int T, int N, int K) {
-  if (T < 0 || N <= 0 || K <= 0) return 0;
+  if (T <= 0 || N <= 0 || K <= 0) return 0;
   return moe::linear_w4_ws_bytes(T, N, K);
 }
 
@@ -544,8 +544,8 @@ int moe_linear_w4(const void* x_bf16, int T, int N, int K, int group_size, const
   if (K % MOE_GROUP) return fail(MOE_ERR_UNSUPPORTED, "K=%d not a multiple of 128", K);
   if (N % 16) return fail(MOE_ERR_UNSUPPORTED, "N=%d not a multiple of 16", N);
   if (K >= 1 << 20) return fail(MOE_ERR_UNSUPPORTED, "K=%d not below 2^20", K);
-  // fewer than 2^32 threads in every launch (a tile kernel takes up to 8 N for
-  // few tokens, and at least 256 T, as its grid is dealt to the eight XCDs)
+  // fewer than 2^32 threads in every launch (up to 11 N for few tokens, and at
+  // least 256 T streaming, whose blocks come in eights)
   if (T >= 1 << 23 || N >= 1 << 28)
     return fail(MOE_ERR_UNSUPPORTED, "moe_linear_w4: T=%d not below 2^23 or N=%d not below 2^28",
                 T, N);

@@ -123,6 +123,11 @@ def test_linear_refusals(lib):
             assert f(T=T, N=N, K=K, wsb=need - 1) == WSP and f(T=T, N=N, K=K, ws=NULL) == WSP
             assert f(T=T, N=N, K=K, ws=ctypes.c_void_p(0x10010)) == INV
     assert lib.moe_linear_w4_ws_bytes(-1, 16, 128) == 0
+    for N, K in ((16, 128), (50304, 4096), (4096, 14336)):
+        assert lib.moe_linear_w4_ws_bytes(0, N, K) == 0
+        assert all(lib.moe_linear_w4_ws_bytes(T, N, K) == 0 for T in range(65))
+    for T, N, K in ((1, 1, 1), (100, 8, 100), ((1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1)):
+        lib.moe_linear_w4_ws_bytes(T, N, K)     # refused sizes are priced all the same
 
 
 def test_norm_refusals(lib):

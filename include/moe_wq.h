@@ -511,8 +511,9 @@ int moe_retile_bitplane8(const uint8_t *planes_canonical, int E, int N, int K,
  * group sums are scaled by 192 in fp32).
  * Requires N % 16 == 0, K % 128 == 0, T below 2^23, N below 2^28, K below 2^20,
  * T * K and T * N below 2^34.
- * ws / ws_bytes: at least moe_linear_w4_ws_bytes(T, N, K) (0 for T <= 64),
- * 256-byte aligned, no contents carried between calls.
+ * ws / ws_bytes: at least moe_linear_w4_ws_bytes(T, N, K) (0 for T <= 64 and
+ * for sizes that the call refuses), 256-byte aligned, no contents carried
+ * between calls.
  * ------------------------------------------------------------------- */
 size_t moe_linear_w4_ws_bytes(int T, int N, int K);
 int moe_linear_w4(const void *x_bf16, int T, int N, int K, int group_size,

@@ -527,30 +527,39 @@ static int colsum_ws_check(const char* what, bool wanted, size_t need, const voi
   return MOE_OK;
 }
 
+// Why moe_linear_w4 refuses these sizes, or null; the kernel choice takes only
+// sizes that pass (it divides by counts of row tiles).
+static const char* linear_refusal(int T, int N, int K, int* status) {
+  *status = MOE_ERR_INVALID_ARG;
+  if (T < 0 || N <= 0 || K <= 0) return "bad size";
+  *status = MOE_ERR_UNSUPPORTED;
+  if (K % MOE_GROUP) return "K not a multiple of 128";
+  if (N % 16) return "N not a multiple of 16";
+  if (K >= 1 << 20) return "K not below 2^20";
+  // fewer than 2^32 threads in every launch (up to 11 N for few tokens, and at
+  // least 256 T streaming, whose blocks come in eights)
+  if (T >= 1 << 23 || N >= 1 << 28) return "T not below 2^23 or N not below 2^28";
+  if ((long long)T * K >= (1LL << 34) || (long long)T * N >= (1LL << 34))
+    return "T*K and T*N must be below 2^34";
+  return nullptr;
+}
+
 size_t moe_linear_w4_ws_bytes(int T, int N, int K) {
-  if (T <= 0 || N <= 0 || K <= 0) return 0;
+  int status;
+  if (T == 0 || linear_refusal(T, N, K, &status)) return 0;
   return moe::linear_w4_ws_bytes(T, N, K);
 }
 
 int moe_linear_w4(const void* x_bf16, int T, int N, int K, int group_size, const uint8_t* codes,
                   const uint16_t* scales_f16, const float* bias, void* out, int out_dtype,
                   void* ws, size_t ws_bytes, void* stream) {
-  if (T < 0 || N <= 0 || K <= 0)
-    return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: bad size (T=%d N=%d K=%d)", T, N, K);
+  int status;
+  if (const char* why = linear_refusal(T, N, K, &status))
+    return fail(status, "moe_linear_w4: %s (T=%d N=%d K=%d)", why, T, N, K);
   if (!known_dtype(out_dtype))
     return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: unknown out_dtype %d", out_dtype);
   if (group_size != MOE_GROUP)
     return fail(MOE_ERR_UNSUPPORTED, "group_size=%d (only 128)", group_size);
-  if (K % MOE_GROUP) return fail(MOE_ERR_UNSUPPORTED, "K=%d not a multiple of 128", K);
-  if (N % 16) return fail(MOE_ERR_UNSUPPORTED, "N=%d not a multiple of 16", N);
-  if (K >= 1 << 20) return fail(MOE_ERR_UNSUPPORTED, "K=%d not below 2^20", K);
-  // fewer than 2^32 threads in every launch (up to 11 N for few tokens, and at
-  // least 256 T streaming, whose blocks come in eights)
-  if (T >= 1 << 23 || N >= 1 << 28)
-    return fail(MOE_ERR_UNSUPPORTED, "moe_linear_w4: T=%d not below 2^23 or N=%d not below 2^28",
-                T, N);
-  if ((long long)T * K >= (1LL << 34) || (long long)T * N >= (1LL << 34))
-    return fail(MOE_ERR_UNSUPPORTED, "moe_linear_w4: T*K and T*N must be below 2^34");
   if (T == 0) return ok();
   if (!x_bf16 || !codes || !scales_f16 || !out)
     return fail(MOE_ERR_INVALID_ARG, "moe_linear_w4: null pointer");

@@ -12,6 +12,7 @@ first two also as one call, moe_route_permute).
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
 import functools
 import os
@@ -162,6 +163,52 @@ def _stream(stream):
 def _empty(shape, dtype, like):
     import torch
     return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+@contextlib.contextmanager
+def _launch_on(stream, values):
+    """Makes `stream` current, so that what the call allocates comes from that
+    stream's memory, and records the tensors among `values` on it, so that
+    memory the caller frees meanwhile is not handed out before the call is
+    through."""
+    import torch
+    with torch.cuda.stream(stream):
+        if not torch.cuda.is_current_stream_capturing():
+            for t in values:
+                if isinstance(t, torch.Tensor) and t.device == stream.device:
+                    t.record_stream(stream)
+        yield
+
+
+def _current_device():
+    import torch
+    return torch._C._cuda_getDevice()
+
+
+def _launch_stream():
+    """The current stream's handle, and whether it is recording a graph."""
+    import torch
+    return (torch._C._cuda_getCurrentRawStream(_current_device()),
+            torch.cuda.is_current_stream_capturing())
+
+
+class _StepBuffers:
+    """Keeps a layer's buffers from step to step (_alloc makes them).
+
+    A set serves one batch size on one stream and comes from that stream's
+    memory, so that dropping it needs no wait.  A step that is recorded into a
+    graph takes a set of its own from the graph's memory, which lasts as long
+    as the graph does, and leaves it to no later step."""
+
+    _held = None
+
+    def _buffers(self, T, like):
+        stream, recording = _launch_stream()
+        if recording or self._held != (T, stream):
+            self._held = None
+            self._alloc(T, like)
+            if not recording:
+                self._held = (T, stream)
 
 
 # ----------------------------------------------------------------- the ABI
@@ -495,19 +542,10 @@ def _on_device(fn):
         if first.is_cuda and stream.device != first.device:
             raise ValueError(f"{fn.__name__}: stream of {stream.device}, tensors on "
                              f"{first.device}")
-        with torch.cuda.stream(stream):
-            if not torch.cuda.is_current_stream_capturing():
-                for t in (first, *args, *kw.values()):
-                    if isinstance(t, torch.Tensor) and t.is_cuda:
-                        t.record_stream(stream)
+        with _launch_on(stream, (first, *args, *kw.values())):
             return fn(first, *args, **kw)
 
     return call
-
-
-def _current_device():
-    import torch
-    return torch._C._cuda_getDevice()
 
 
 def _raw_stream(t):
@@ -890,7 +928,7 @@ def moe_cache_plan(E, slots, fmt, slot_expert, slot_bits, slot_last, step, need)
                 V=V.value)
 
 
-class ExpertCache:
+class ExpertCache(_StepBuffers):
     """Expert bank in pinned host memory behind `slots` device slots
     (moe_cache_*): forward(x) runs one layer step, copying the experts (or
     bitplanes) it is missing into the slots first."""
@@ -911,7 +949,6 @@ class ExpertCache:
             self.E, self.d, f, fmt, slots, *[_ptr(t) for t in self.host],
             *[_ptr(t) for t in self.dev], ctypes.cast(ctypes.pointer(h), ctypes.c_void_p)))
         self.handle = h
-        self._T = None
 
     def _alloc(self, T, like):
         import torch
@@ -923,14 +960,15 @@ class ExpertCache:
         self.y_pairs = torch.empty((T * k, d), dtype=torch.float32, device=dev)
         nb = int(load_library().moe_cache_ws_bytes(self.handle, T, k))
         self.ws = torch.empty((max(nb, 256),), dtype=torch.uint8, device=dev)
-        self._T = T
 
     def forward(self, x, out=None, out_dtype=MOE_OUT_BF16, bits=None,
                 bits_mode=MOE_BITS_NONE, stream=None):
         import torch
+        if stream is not None:
+            with _launch_on(stream, (x, out, bits)):
+                return self.forward(x, out, out_dtype, bits, bits_mode)
         T = x.shape[0]
-        if self._T != T:
-            self._alloc(T, x)
+        self._buffers(T, x)
         if out is None:
             out = _empty((T, self.d), torch.bfloat16 if out_dtype == MOE_OUT_BF16
                          else torch.float32, x)
@@ -973,10 +1011,11 @@ class ExpertCache:
 
 
 # --------------------------------------------------------- one whole layer
-class MoeLayer:
-    """Resident quantized expert weights plus preallocated buffers for one
-    batch size; `forward(x)` enqueues route+permute, the expert FFN and the
-    combine on one stream."""
+class MoeLayer(_StepBuffers):
+    """Resident quantized expert weights plus the buffers of a step;
+    `forward(x)` enqueues route+permute, the expert FFN and the combine on one
+    stream.  The buffers (topk_idx, .., y_pairs) are those of the last step and
+    stay in place while its batch size and stream do."""
 
     def __init__(self, wr, bias, k, f, gate_up_codes, gate_up_scales,
                  down_codes, down_scales, fmt=MOE_FMT_W4_SYM,
@@ -986,7 +1025,6 @@ class MoeLayer:
         self.gu, self.gus, self.dn, self.dns = (gate_up_codes, gate_up_scales,
                                                 down_codes, down_scales)
         self.fmt, self.bits_mode, self.bits = fmt, bits_mode, bits
-        self._T = None
 
     def _alloc(self, T, like):
         import torch
@@ -1005,15 +1043,16 @@ class MoeLayer:
         self.ws_layer = torch.empty((max(moe_layer_ws_bytes(T, k, E, d, f, self.fmt), 256),),
                                     dtype=torch.uint8, device=dev)
         self.y_pairs = torch.empty((P, d), dtype=torch.float32, device=dev)
-        self._T = T
 
     def forward(self, x, out=None, out_dtype=MOE_OUT_BF16, path=MOE_PATH_AUTO,
                 stream=None, weights=None):
         """One layer step through moe_layer_forward_wq."""
         import torch
+        if stream is not None:
+            with _launch_on(stream, (x, out, *(weights or ()))):
+                return self.forward(x, out, out_dtype, path, None, weights)
         T = x.shape[0]
-        if self._T != T:
-            self._alloc(T, x)
+        self._buffers(T, x)
         gu, gus, dn, dns = weights if weights is not None else (
             self.gu, self.gus, self.dn, self.dns)
         if out is None:
@@ -1028,9 +1067,11 @@ class MoeLayer:
                       stream=None, weights=None):
         """The same step as moe_route_permute, moe_expert_ffn_wq and
         moe_combine calls (the composition the layer entry point equals)."""
+        if stream is not None:
+            with _launch_on(stream, (x, out, *(weights or ()))):
+                return self.forward_steps(x, out, out_dtype, path, None, weights)
         T = x.shape[0]
-        if self._T != T:
-            self._alloc(T, x)
+        self._buffers(T, x)
         gu, gus, dn, dns = weights if weights is not None else (
             self.gu, self.gus, self.dn, self.dns)
         moe_route_permute(x, self.wr, self.bias, self.k, self.ws_rp, self.topk_idx,
@@ -1055,36 +1096,45 @@ class MoeLayer:
         if residual.device != self.wr.device:
             raise ValueError(f"forward_block: residual is on {residual.device}, the layer on "
                              f"{self.wr.device}")
+        if stream is not None:
+            if residual.is_cuda and stream.device != residual.device:
+                raise ValueError(f"forward_block: stream of {stream.device}, residual on "
+                                 f"{residual.device}")
+            with _launch_on(stream, (residual, gain, add, post_gain, gate, next_gain, out,
+                                     next_out)):
+                return self.forward_block(residual, gain, eps, add, post_gain, gate, gate_mode,
+                                          res_scale, next_gain, out, next_out, path)
         if residual.is_cuda and residual.get_device() != _current_device():
             import torch
             with torch.cuda.device(residual.device):
                 return self.forward_block(residual, gain, eps, add, post_gain, gate, gate_mode,
-                                          res_scale, next_gain, out, next_out, path, stream)
-        T = residual.shape[0]
-        x = moe_rmsnorm(residual, gain, eps=eps, stream=stream)
-        if self._T != T:
-            self._alloc(T, x)
+                                          res_scale, next_gain, out, next_out, path)
+        x = moe_rmsnorm(residual, gain, eps=eps)
+        self._buffers(residual.shape[0], x)
         moe_route_permute(x, self.wr, self.bias, self.k, self.ws_rp, self.topk_idx,
-                          self.topk_w, self.offsets, self.sorted_pair, self.pair_pos,
-                          stream)
+                          self.topk_w, self.offsets, self.sorted_pair, self.pair_pos)
         moe_expert_ffn_wq(x, self.offsets, self.sorted_pair, self.k, self.f, self.gu, self.gus,
                           self.dn, self.dns, self.fmt, self.bits, self.bits_mode,
-                          self.y_pairs, self.ws_ffn, path, stream)
+                          self.y_pairs, self.ws_ffn, path)
         return moe_combine_residual(residual, self.y_pairs, self.pair_pos, self.topk_w, add=add,
                                     post_gain=post_gain, gate=gate, gate_mode=gate_mode,
                                     res_scale=res_scale, eps=eps, next_gain=next_gain, out=out,
-                                    next_out=next_out, stream=stream)
+                                    next_out=next_out)
 
     def bind(self, x, out, weights=None, path=MOE_PATH_AUTO, out_dtype=MOE_OUT_BF16,
              stream=None):
         """A step with every argument marshalled once: returns a callable that
         enqueues the same ABI call as forward(x, out, ...) for these fixed
-        buffers (x, out and the weights must stay alive and in place).
+        buffers (x, out and the weights must stay alive and in place; the
+        step's own buffers are kept with the callable) on the stream that was
+        current here, or `stream`.
         For decode loops, where converting arguments on every call would cost
         as much host time as the kernels take on the GPU."""
+        if stream is not None:
+            with _launch_on(stream, (x, out, *(weights or ()))):
+                return self.bind(x, out, weights, path, out_dtype)
         T = x.shape[0]
-        if self._T != T:
-            self._alloc(T, x)
+        self._buffers(T, x)
         gu, gus, dn, dns = weights if weights is not None else (
             self.gu, self.gus, self.dn, self.dns)
         E, k, d, f = self.E, self.k, self.d, self.f
@@ -1102,17 +1152,18 @@ class MoeLayer:
                 _check("moe_layer_forward_wq", rc)
             return out
 
+        # (a later step with another batch size or stream takes other buffers)
+        step.buffers = (self.topk_idx, self.topk_w, self.offsets, self.sorted_pair,
+                        self.pair_pos, self.y_pairs, self.ws_layer)
         return step
 
     def capture(self, x, out, weights=None, path=MOE_PATH_AUTO, out_dtype=MOE_OUT_BF16):
         """One step for these fixed buffers recorded as a HIP graph (torch's
         CUDAGraph object; replay() re-runs the five kernels with one host
-        call).  The library records only kernel launches (no memset or
-        copy nodes) and allocates nothing, so replays are self-contained."""
+        call).  The library records only kernel launches (no memset or copy
+        nodes), and the step's own buffers are the graph's: replays do not
+        meet other steps' of this layer, eager or recorded."""
         import torch
-        T = x.shape[0]
-        if self._T != T:
-            self._alloc(T, x)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):  # binds to the capture stream
             self.bind(x, out, weights, path, out_dtype)()

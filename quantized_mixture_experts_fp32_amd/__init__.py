@@ -15,6 +15,7 @@ import collections
 import contextlib
 import ctypes
 import functools
+import inspect
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -180,6 +181,22 @@ def _launch_on(stream, values):
         yield
 
 
+def _on_stream(fn):
+    """For calls with an argument `stream` that create what they are not given:
+    runs fn with that stream current."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with _launch_on(stream, (*args, *kw.values())):
+            return fn(*args, **kw)
+
+    return call
+
+
 def _current_device():
     import torch
     return torch._C._cuda_getDevice()
@@ -216,6 +233,7 @@ def moe_route_ws_bytes(T, E):
     return int(load_library().moe_route_ws_bytes(T, E))
 
 
+@_on_stream
 def moe_route(x, wr, bias, k, topk_idx=None, topk_w=None, ws=None, stream=None):
     """x bf16 [T][d], wr bf16 [E][d], bias fp32 [E] or None -> (idx, w)."""
     import torch
@@ -237,6 +255,7 @@ def moe_permute_ws_bytes(T, k, E):
     return int(load_library().moe_permute_ws_bytes(T, k, E))
 
 
+@_on_stream
 def moe_permute(topk_idx, E, ws=None, offsets=None, sorted_pair=None,
                 pair_pos=None, stream=None):
     """topk_idx int32 [T][k] -> (expert_offsets [E+1], sorted_pair, pair_pos)."""
@@ -262,6 +281,7 @@ def moe_route_permute_ws_bytes(T, k, E):
     return int(load_library().moe_route_permute_ws_bytes(T, k, E))
 
 
+@_on_stream
 def moe_route_permute(x, wr, bias, k, ws=None, topk_idx=None, topk_w=None, offsets=None,
                       sorted_pair=None, pair_pos=None, stream=None):
     """moe_route then moe_permute in one call -> (idx, w, offsets, sorted_pair,
@@ -293,6 +313,7 @@ def moe_ffn_ws_bytes(T, k, E, d, f, fmt=MOE_FMT_W4_SYM):
     return int(load_library().moe_ffn_ws_bytes(T, k, E, d, f, fmt))
 
 
+@_on_stream
 def moe_expert_ffn_wq(x, expert_offsets, sorted_pair, k, f, gate_up_codes,
                       gate_up_scales, down_codes, down_scales,
                       fmt=MOE_FMT_W4_SYM, bits=None, bits_mode=MOE_BITS_NONE,
@@ -399,6 +420,7 @@ def moe_layer_forward_noalloc(x, wr, bias, k, f, gate_up_codes, gate_up_scales, 
     return out
 
 
+@_on_stream
 def moe_bp_distortion(gate_up_planes, gate_up_scales, down_planes, down_scales, d, f,
                       dist=None, ws=None, stream=None):
     """Weight-space distortion [E][8] (fp64) of bitplane experts at prefix
@@ -416,6 +438,7 @@ def moe_bp_distortion(gate_up_planes, gate_up_scales, down_planes, down_scales, 
     return dist
 
 
+@_on_stream
 def moe_allocate_bits(dist, counts, d, f, b_min, b_max, budget_bytes, bits=None,
                       lam=None, read=None, stream=None):
     """Per-expert prefix widths [E] (u8) under a routing-weighted read
@@ -435,6 +458,7 @@ def moe_allocate_bits(dist, counts, d, f, b_min, b_max, budget_bytes, bits=None,
     return bits, lam, read
 
 
+@_on_stream
 def moe_combine(y_pairs, pair_pos, topk_w, out=None, out_dtype=MOE_OUT_BF16,
                 stream=None):
     """Layer output [T][d] (bf16 bits in an int16 tensor, or fp32)."""
@@ -450,6 +474,7 @@ def moe_combine(y_pairs, pair_pos, topk_w, out=None, out_dtype=MOE_OUT_BF16,
     return out
 
 
+@_on_stream
 def moe_quantize_w4(w, codes=None, scales=None, stream=None):
     """fp32 [E][N][K] -> (codes, scales fp16-bits [E][N][K/128]).
 
@@ -467,6 +492,7 @@ def moe_quantize_w4(w, codes=None, scales=None, stream=None):
     return codes, scales
 
 
+@_on_stream
 def moe_retile_w4(codes_canonical, N, K, codes=None, stream=None):
     """Canonical row-major int4 codes u8 [E][N][K/2] -> the tiled layout
     (a u8 tensor [E][N][K/2] as moe_quantize_w4 returns)."""
@@ -479,6 +505,7 @@ def moe_retile_w4(codes_canonical, N, K, codes=None, stream=None):
     return codes
 
 
+@_on_stream
 def moe_retile_bitplane8(planes_canonical, N, K, planes=None, stream=None):
     """Canonical plane slabs u8 [E][8][N][K/8] -> the bitplane streaming
     layout (a u8 tensor [E][8][N][K/8] as moe_quantize_bitplane8 returns)."""
@@ -491,6 +518,7 @@ def moe_retile_bitplane8(planes_canonical, N, K, planes=None, stream=None):
     return planes
 
 
+@_on_stream
 def moe_quantize_bitplane8(w, planes=None, scales=None, stream=None):
     """fp32 [E][N][K] -> (planes, scales fp16-bits [E][N][K/128]).
 

@@ -1,7 +1,11 @@
 """The buffers that a layer keeps between steps: one set per batch size and
 stream, from that stream's memory, and a set of its own for every recorded
 step.  On the CPU the rule is checked with the stream stood in for; on the GPU
-steps change batch size and stream, and graphs replay beside eager steps."""
+steps change batch size and stream, and graphs replay beside eager steps.  The
+calls that create results and workspaces take them from their stream too."""
+import contextlib
+import inspect
+
 import pytest
 import torch
 
@@ -69,6 +73,63 @@ def test_buffers_are_made_again_after_a_failed_allocation(stream, monkeypatch):
             layer._buffers(5, layer.wr)
     held(layer, 5)
     held(layer, 4)
+
+
+class AnyCall:
+    """Stands in for the library: every call succeeds, sizes are 64 bytes."""
+
+    def __getattr__(self, name):
+        return lambda *args: 64 if name.endswith("_bytes") else 0
+
+
+Z = torch.zeros
+CALLS = {
+    "moe_route": (Z(4, 128), Z(8, 128), None, 2),
+    "moe_permute": (Z(4, 2, dtype=torch.int32), 8),
+    "moe_route_permute": (Z(4, 128), Z(8, 128), None, 2),
+    "moe_expert_ffn_wq": (Z(4, 128), Z(9), Z(8), 2, 128, None, None, None, None),
+    "moe_combine": (Z(8, 128), Z(8), Z(4, 2)),
+    "moe_bp_distortion": (Z(8, 8), None, None, None, 128, 128),
+    "moe_allocate_bits": (Z(8, 8), Z(8), 128, 128, 2, 8, 1000),
+    "moe_quantize_w4": (Z(1, 16, 128),),
+    "moe_quantize_bitplane8": (Z(1, 16, 128),),
+    "moe_retile_w4": (Z(1, 16, 64), 16, 128),
+    "moe_retile_bitplane8": (Z(1, 8, 16, 16), 16, 128),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_what_a_call_creates_is_the_given_streams(name, monkeypatch):
+    """Results and workspaces are allocated while the given stream is current,
+    whether it is given by name or by position."""
+    class Stream:
+        cuda_stream, device = 1234, torch.device("cuda:0")
+
+    side, now, made = Stream(), [], []
+
+    @contextlib.contextmanager
+    def launch_on(stream, values):
+        now.append(stream)
+        yield
+        now.pop()
+
+    empty = torch.empty
+
+    def watched(*args, **kw):
+        made.append(list(now))
+        return empty(*args, **kw)
+
+    monkeypatch.setattr(moe, "load_library", AnyCall)
+    monkeypatch.setattr(moe, "_launch_on", launch_on)
+    monkeypatch.setattr(torch, "empty", watched)
+    call = getattr(moe, name)
+    call(*CALLS[name], stream=side)
+    assert made and all(m == [side] for m in made), made
+    made.clear()
+    names = list(inspect.signature(call).parameters)
+    rest = [inspect.signature(call).parameters[n].default for n in names[len(CALLS[name]):-1]]
+    call(*CALLS[name], *rest, side)
+    assert made and all(m == [side] for m in made), made
 
 
 # ------------------------------------------------------------------ on the GPU
@@ -241,4 +302,33 @@ def test_block_on_two_streams_in_turn():
     torch.cuda.synchronize()
     for i, o in enumerate(got):
         for a, b in zip(want[i % 2], o):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_calls_on_a_side_stream_keep_their_own_memory():
+    """Grouping and combine on a side stream with workspaces of their own,
+    while the default stream takes and writes memory."""
+    note("calls on a side stream")
+    T, d, k, E = 150, 512, 4, 8
+    g = torch.Generator().manual_seed(6)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)])
+    ids = ids.to(torch.int32).to(DEV)
+    y = torch.randn(T * k, d, generator=g).to(DEV)
+    w = torch.softmax(torch.randn(T, k, generator=g), 1).to(DEV)
+
+    def step(stream=None):
+        off, sp, pos = moe.moe_permute(ids, E, stream=stream)
+        churn(1)
+        return off, sp, pos, moe.moe_combine(y, pos, w, stream=stream)
+
+    want = step()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        churn()
+        got = step(side)
+        churn()
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
             assert torch.equal(a, b)

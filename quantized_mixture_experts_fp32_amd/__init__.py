@@ -553,26 +553,34 @@ def moe_set_ffn_events(gateup_begin=None, gateup_end=None, down_begin=None,
 # launch on.
 
 def _on_device(fn):
-    """Runs fn with the first tensor's device current and, when the keyword
+    """Runs fn with its first parameter's device current and, when the keyword
     `stream` is given, with that stream current; fn launches on the current
     stream."""
+    sig = inspect.signature(fn)
+    lead = next(iter(sig.parameters))
 
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         import torch
+        if not args and lead not in kw:
+            return fn(**kw)  # (a TypeError that names the parameter)
+        first = args[0] if args else kw[lead]
         if not isinstance(first, torch.Tensor):
             raise ValueError(f"{fn.__name__}: a tensor is needed, got {type(first).__name__}")
         if stream is None:
             if not first.is_cuda or first.get_device() == _current_device():
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
             with torch.cuda.device(first.device):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
         if first.is_cuda and stream.device != first.device:
             raise ValueError(f"{fn.__name__}: stream of {stream.device}, tensors on "
                              f"{first.device}")
-        with _launch_on(stream, (first, *args, *kw.values())):
-            return fn(first, *args, **kw)
+        with _launch_on(stream, (*args, *kw.values())):
+            return fn(*args, **kw)
 
+    call.__signature__ = sig.replace(parameters=[
+        *sig.parameters.values(),
+        inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
 
 

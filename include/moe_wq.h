@@ -508,7 +508,9 @@ int moe_retile_bitplane8(const uint8_t *planes_canonical, int E, int N, int K,
  * sums are fp32 (codes enter the matrix cores exactly, weights are never
  * rounded), rounded once on store.  A row of x that holds an infinity or NaN
  * gives a row of infinities and NaN; finite values must be below 2^110 (their
- * group sums are scaled by 192 in fp32).
+ * group sums are scaled by 192 in fp32) and 2^120 / K (large batches add up in
+ * units of the row's largest scale so far), and terms below 2^-126 of a row's
+ * largest scale may be lost.  A group whose scale is 0 contributes nothing.
  * Requires N % 16 == 0, K % 128 == 0, T below 2^23, N below 2^28, K below 2^20,
  * T * K and T * N below 2^34.
  * ws / ws_bytes: at least moe_linear_w4_ws_bytes(T, N, K) (0 for T <= 64 and

@@ -255,13 +255,16 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
         for (int i = 0; i < 16; ++i) acc[t][m][i] = 0.0f;
     float s_cur[2] = {0.0f, 0.0f};
 
-    // B column of the offset MFMA: -192 in K rows 0..2 (lanes of half 0)
-    u32x4 negv = {0u, 0u, 0u, 0u};
-    if (hh == 0) {
-      negv[0] = 0xC340C340u;  // -192, -192
-      negv[1] = 0x0000C340u;  // -192, 0
-    }
-    const bf16x8 negB = __builtin_bit_cast(bf16x8, negv);
+    // B column of the offset MFMA: minus the conversion's offset D (192.0
+    // twice) in K rows 0..2 (lanes of half 0)
+    const uint32_t half0 = hh == 0 ? ~0u : 0u;
+    auto neg_col = [&](uint32_t D) {
+      u32x4 v = {0u, 0u, 0u, 0u};
+      v[0] = (D ^ 0x80008000u) & half0;
+      v[1] = v[0] & 0xFFFFu;
+      return __builtin_bit_cast(bf16x8, v);
+    };
+    const bf16x8 negB = neg_col(0x43404340u);
 
     // fragment address of (token block 0, K step 0) in a staged buffer, and
     // the chunk swizzle of K steps 1..7
@@ -281,14 +284,31 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
       // scale and its codes are masked to 0 (which convert to the offset 192
       // that the offset MFMA cancels), whatever codes it holds
       float r[2];
-      uint32_t qmask[2];
+      uint32_t qmask[2], D[2];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const float sg = 0.125f * f16_bits_to_f32(sc[m]);
         const bool upd = sg != 0.0f;
-        r[m] = upd ? ((s_cur[m] == 0.0f) ? 0.0f : s_cur[m] / sg) : 1.0f;
-        s_cur[m] = upd ? sg : s_cur[m];
         qmask[m] = upd ? 0xFFFFFFFFu : 0u;
+        if (kDense) {
+          // A unit stays in or above the last one's binade (it is the scale
+          // times 2^e, e up to fp16's 39 binades), or the total of groups with
+          // large scales would overflow in units of a small one; the group's
+          // codes are converted to 2^-e times their values for it, all exact.
+          // A group without weight is converted to zeros, offset included: the
+          // offset's rounding goes by its activations, whatever their size.
+          // (Selected by masks: the compiler makes branches of conditions.)
+          const uint32_t cur = __float_as_uint(s_cur[m]), own = __float_as_uint(sg);
+          const int up = (int)(cur & 0x7F800000u) - (int)(own & 0x7F800000u);
+          const uint32_t e = (uint32_t)min(max(up, 0), 40 << 23);  // in exponent position
+          const float q = ldexpf(s_cur[m] / sg, -(int)(e >> 23));
+          r[m] = __uint_as_float((__float_as_uint(q) & qmask[m]) | (0x3F800000u & ~qmask[m]));
+          s_cur[m] = __uint_as_float(((own + e) & qmask[m]) | (cur & ~qmask[m]));
+          D[m] = (0x43404340u - (e | e >> 16)) & qmask[m];
+        } else {
+          r[m] = upd ? ((s_cur[m] == 0.0f) ? 0.0f : s_cur[m] / sg) : 1.0f;
+          s_cur[m] = upd ? sg : s_cur[m];
+        }
       }
       // offset term and rescale, token block by token block
 #pragma unroll
@@ -304,7 +324,7 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
         for (int m = 0; m < 2; ++m) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[t][m][i] *= r[m];
-          acc[t][m] = mfma32(sumA, negB, acc[t][m]);
+          acc[t][m] = mfma32(sumA, kDense ? neg_col(D[m]) : negB, acc[t][m]);
         }
       }
       const uint8_t* rd = ab + rd_base;
@@ -325,7 +345,8 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
         bf16x8 bfr[2];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-          bfr[m] = w4_top(q[m][s2 >> 2][s2 & 3] & qmask[m], 0x43404340u);
+          bfr[m] = kDense ? w4_top(q[m][s2 >> 2][s2 & 3], D[m], 0x00780078u & qmask[m])
+                          : w4_top(q[m][s2 >> 2][s2 & 3] & qmask[m], 0x43404340u);
 #pragma unroll
         for (int t = 0; t < NTB; ++t)
 #pragma unroll

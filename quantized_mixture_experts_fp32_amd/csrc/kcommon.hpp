@@ -90,8 +90,8 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
 // bits 3..6 and is XORed into D there.  D = 0x4340 (192.0): two's
 // complement codes q -> 192 + 8 q.  D = 0x4300 (128.0): unsigned nibbles
 // c -> 128 + 8 c; D = 0x4500 (2048.0): 16 (128 + 8 c).
-__device__ __forceinline__ bf16x8 w4_top(uint32_t w, uint32_t D) {
-  const uint32_t B = 0x00780078u;
+// B: the nibbles' bits; 0 drops the code and leaves D.
+__device__ __forceinline__ bf16x8 w4_top(uint32_t w, uint32_t D, uint32_t B = 0x00780078u) {
   u32x4 r;
   r[0] = __builtin_amdgcn_bitop3_b32(w << 3, B, D, 0x6A);
   r[1] = __builtin_amdgcn_bitop3_b32(w >> 1, B, D, 0x6A);

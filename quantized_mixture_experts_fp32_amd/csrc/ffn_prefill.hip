@@ -369,14 +369,13 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
       for (int t = 0; t < NTB; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[t][m][i] *= s_cur[m];
-    // (dense: scaled before the store's branches, not behind them, where a
-    // lane group without rows would leave too few steps after the last MFMA)
-    if (kDense) {
+    // (scaled before the store's branches: moved behind them, the products
+    // could reach the last MFMA's result too early on the path around a lane
+    // group without rows, where the compiler has been seen not to count)
 #pragma unroll
-      for (int t = 0; t < NTB; ++t) {
-        asm volatile("" : "+v"(acc[t][0]));
-        asm volatile("" : "+v"(acc[t][1]));
-      }
+    for (int t = 0; t < NTB; ++t) {
+      asm volatile("" : "+v"(acc[t][0]));
+      asm volatile("" : "+v"(acc[t][1]));
     }
 
     // ---- epilogue: lane owns feature brow (per B block) for 16 token rows

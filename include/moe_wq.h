@@ -516,8 +516,12 @@ int moe_retile_bitplane8(const uint8_t *planes_canonical, int E, int N, int K,
  * ws / ws_bytes: at least moe_linear_w4_ws_bytes(T, N, K) (0 for T <= 64 and
  * for sizes that the call refuses), 256-byte aligned, no contents carried
  * between calls.
+ * moe_linear_w4_kernel: the kernel that these sizes run, for tests and
+ * profiles: "tile 16x32 w8" (tokens x features, waves), "stream 16" (tokens a
+ * pass), "gemm 96" (tokens a tile); "" where nothing runs.
  * ------------------------------------------------------------------- */
 size_t moe_linear_w4_ws_bytes(int T, int N, int K);
+const char *moe_linear_w4_kernel(int T, int N, int K);
 int moe_linear_w4(const void *x_bf16, int T, int N, int K, int group_size,
                   const uint8_t *codes, const uint16_t *scales_f16,
                   const float *bias, void *out, int out_dtype, void *ws,

@@ -40,7 +40,7 @@ EXPORTS = ("moe_status_str", "moe_last_error", "moe_route_ws_bytes", "moe_route"
            "moe_bp_distortion", "moe_allocate_bits", "moe_cache_create", "moe_cache_destroy",
            "moe_cache_ws_bytes", "moe_cache_forward", "moe_cache_stats", "moe_cache_slots",
            "moe_cache_reset", "moe_cache_plan", "moe_retile_w4", "moe_retile_bitplane8",
-           "moe_linear_w4_ws_bytes", "moe_linear_w4", "moe_rmsnorm",
+           "moe_linear_w4_ws_bytes", "moe_linear_w4_kernel", "moe_linear_w4", "moe_rmsnorm",
            "moe_rmsnorm_bwd_ws_bytes", "moe_rmsnorm_bwd", "moe_combine_residual",
            "moe_combine_residual_bwd_ws_bytes", "moe_combine_residual_bwd", "moe_dispatch",
            "moe_dispatch_bwd", "moe_combine_bwd")
@@ -111,6 +111,8 @@ def load_library():
                                    vp, vp, i32, vp, vp]
     f32 = ctypes.c_float
     lib.moe_linear_w4_ws_bytes.argtypes, lib.moe_linear_w4_ws_bytes.restype = [i32] * 3, sz
+    lib.moe_linear_w4_kernel.argtypes = [i32] * 3
+    lib.moe_linear_w4_kernel.restype = ctypes.c_char_p
     lib.moe_linear_w4.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, sz, vp]
     lib.moe_rmsnorm.argtypes = [vp, i32, vp, i32, i32, f32, vp, i32, vp]
     lib.moe_rmsnorm_bwd_ws_bytes.argtypes = [i32, i32]
@@ -656,6 +658,11 @@ def _ws_args(ws):
 
 def moe_linear_w4_ws_bytes(T, N, K):
     return int(load_library().moe_linear_w4_ws_bytes(T, N, K))
+
+
+def moe_linear_w4_kernel(T, N, K):
+    """The kernel that these sizes run ("" where nothing runs)."""
+    return load_library().moe_linear_w4_kernel(T, N, K).decode()
 
 
 @_on_device

@@ -550,6 +550,12 @@ size_t moe_linear_w4_ws_bytes(int T, int N, int K) {
   return moe::linear_w4_ws_bytes(T, N, K);
 }
 
+const char* moe_linear_w4_kernel(int T, int N, int K) {
+  int status;
+  if (T == 0 || linear_refusal(T, N, K, &status)) return "";
+  return moe::linear_w4_kernel(T, N, K);
+}
+
 int moe_linear_w4(const void* x_bf16, int T, int N, int K, int group_size, const uint8_t* codes,
                   const uint16_t* scales_f16, const float* bias, void* out, int out_dtype,
                   void* ws, size_t ws_bytes, void* stream) {

@@ -184,12 +184,13 @@ hipError_t launch_combine_bwd(const void* dout, int do_f32, const float* y,
                               void* dy, int dy_f32, float* dtopk_w, hipStream_t s);
 
 // Linear map with int4 weights (linear.hip; large batches: the GEMM kernel of
-// ffn_prefill.hip with tiles of 32 to 128 tokens).
+// ffn_prefill.hip with tiles of 64, 96 or 128 tokens).
 size_t linear_w4_gemm_ws_bytes(int T, int K);
 hipError_t launch_linear_w4_gemm(const uint16_t* x, const uint8_t* codes, const uint16_t* scales,
                                  const float* bias, int T, int N, int K, int tile_tokens,
                                  void* out, int out_f32, void* ws, hipStream_t s);
 size_t linear_w4_ws_bytes(int T, int N, int K);
+const char* linear_w4_kernel(int T, int N, int K);  // the chosen kernel's name
 hipError_t launch_linear_w4(const uint16_t* x, const uint8_t* codes, const uint16_t* scales,
                             const float* bias, int T, int N, int K, void* out, int out_f32,
                             void* ws, hipStream_t s);

@@ -488,19 +488,31 @@ struct Tile {
   int tokens, rows, min_groups, max_groups;
   float fixed, per;
   RunFn run;
+  const char* name;
 };
 const Tile kTiles[] = {
-    {16, 1, 1, 1 << 30, 2.3f, 1.85f, tile_as<8, 1, 1>},
-    {16, 2, 1, 8, 2.4f, 2.6f, tile_as<4, 1, 2>},
-    {16, 2, 9, 1 << 30, 2.4f, 2.5f, tile_as<8, 1, 2>},
-    {16, 3, 9, 1 << 30, 2.7f, 3.15f, tile_as<8, 1, 3>},
-    {32, 2, 1, 1 << 30, 2.8f, 3.75f, tile_as<4, 2, 2>},
-    {32, 3, 1, 1 << 30, 3.1f, 4.55f, tile_as<4, 2, 3>},
-    {32, 4, 1, 1 << 30, 3.0f, 5.9f, tile_as<4, 2, 4>},
-    {32, 6, 1, 1 << 30, 3.4f, 7.65f, tile_as<4, 2, 6>},
-    {48, 4, 1, 1 << 30, 3.6f, 7.5f, tile_as<4, 3, 4>},
-    {64, 4, 1, 1 << 30, 4.4f, 9.3f, tile_as<4, 4, 4>},
+    {16, 1, 1, 1 << 30, 2.3f, 1.85f, tile_as<8, 1, 1>, "tile 16x16 w8"},
+    {16, 2, 1, 8, 2.4f, 2.6f, tile_as<4, 1, 2>, "tile 16x32 w4"},
+    {16, 2, 9, 1 << 30, 2.4f, 2.5f, tile_as<8, 1, 2>, "tile 16x32 w8"},
+    {16, 3, 9, 1 << 30, 2.7f, 3.15f, tile_as<8, 1, 3>, "tile 16x48 w8"},
+    {32, 2, 1, 1 << 30, 2.8f, 3.75f, tile_as<4, 2, 2>, "tile 32x32 w4"},
+    {32, 3, 1, 1 << 30, 3.1f, 4.55f, tile_as<4, 2, 3>, "tile 32x48 w4"},
+    {32, 4, 1, 1 << 30, 3.0f, 5.9f, tile_as<4, 2, 4>, "tile 32x64 w4"},
+    {32, 6, 1, 1 << 30, 3.4f, 7.65f, tile_as<4, 2, 6>, "tile 32x96 w4"},
+    {48, 4, 1, 1 << 30, 3.6f, 7.5f, tile_as<4, 3, 4>, "tile 48x64 w4"},
+    {64, 4, 1, 1 << 30, 4.4f, 9.3f, tile_as<4, 4, 4>, "tile 64x64 w4"},
 };
+
+// The streaming kernel for T tokens and K inputs.
+struct Stream {
+  RunFn run;
+  const char* name;
+};
+Stream stream_for(int T, int K) {
+  if (T <= 16) return {stream_as<16, 1, 2, 2>, "stream 16"};
+  if (K <= 16 * 128) return {stream_as<16, 2, 1, 2>, "stream 32 short"};
+  return {stream_as<16, 2, 2, 1>, "stream 32"};
+}
 
 struct Choice {
   const Tile* tile;  // a tile kernel, or
@@ -565,6 +577,13 @@ Choice choose(int T, int N, int K) {
 
 }  // namespace
 
+const char* linear_w4_kernel(int T, int N, int K) {
+  const Choice c = choose(T, N, K);
+  if (c.gemm_tokens)
+    return c.gemm_tokens == 64 ? "gemm 64" : c.gemm_tokens == 96 ? "gemm 96" : "gemm 128";
+  return c.tile ? c.tile->name : stream_for(T, K).name;
+}
+
 size_t linear_w4_ws_bytes(int T, int N, int K) {
   return choose(T, N, K).gemm_tokens ? linear_w4_gemm_ws_bytes(T, K) : 0;
 }
@@ -576,10 +595,7 @@ hipError_t launch_linear_w4(const uint16_t* x, const uint8_t* codes, const uint1
   if (c.gemm_tokens)
     return launch_linear_w4_gemm(x, codes, scales, bias, T, N, K, c.gemm_tokens, out, out_f32, ws,
                                  s);
-  const RunFn run = c.tile          ? c.tile->run
-                    : T <= 16        ? stream_as<16, 1, 2, 2>
-                    : K <= 16 * 128 ? stream_as<16, 2, 1, 2>
-                                    : stream_as<16, 2, 2, 1>;
+  const RunFn run = c.tile ? c.tile->run : stream_for(T, K).run;
   return run(x, codes, scales, bias, T, N, K, out, out_f32, s);
 }
 

@@ -6,6 +6,7 @@ import sys
 import pytest
 
 import quantized_mixture_experts_fp32_amd as moe
+from linear_shapes import LISTED, SHAPES
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -36,3 +37,25 @@ def test_workspace_query_of_accepted_sizes():
     for T, N, K in ((2501, 4096, 4096), (1500, 8208, 256), (4096, 2048, 2048)):
         assert moe.moe_linear_w4_ws_bytes(T, N, K) == T * (K // 128) * 8
     assert moe.moe_linear_w4_ws_bytes(1, 16, 128) == 0
+
+
+@pytest.mark.parametrize("name,T,K,N", LISTED)
+def test_shapes_run_the_kernel_that_they_are_listed_for(name, T, K, N):
+    """What the GPU tests of a kernel's shapes reach: a change of the kernel
+    choice has to come with shapes for what it moved."""
+    assert moe.moe_linear_w4_kernel(T, N, K) == name
+
+
+def test_kernels_in_use():
+    """Only listed kernels run, over the range of sizes; refused and empty
+    sizes run none; the GEMM alone has a workspace."""
+    seen = set()
+    for T in (1, 2, 5, 16, 17, 33, 48, 64, 65, 97, 200, 333, 515, 1024, 1500, 2501, 4096):
+        for K in (128, 256, 640, 1024, 1664, 2048, 2176, 4096, 5248, 8192, 14336):
+            for N in (16, 272, 784, 2064, 4112, 8208, 12304, 25712, 50304):
+                name = moe.moe_linear_w4_kernel(T, N, K)
+                seen.add(name)
+                assert (moe.moe_linear_w4_ws_bytes(T, N, K) > 0) == name.startswith("gemm")
+    assert seen <= set(SHAPES) and len(seen) >= 14, seen ^ set(SHAPES)
+    for T, N, K in (*REFUSED, (0, 16, 128)):
+        assert moe.moe_linear_w4_kernel(T, N, K) == ""

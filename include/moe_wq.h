@@ -567,7 +567,9 @@ int moe_rmsnorm_bwd(const void *dout, int dout_dtype, const void *x, int x_dtype
  *
  * moe_combine_residual_bwd -- the gradient for dout [T][d] of `dtype`, the
  * gradient of out (that of next_out is moe_rmsnorm_bwd's, with out as its x
- * and dout joined through dres).  Outputs, each NULL if not wanted:
+ * and dout joined through dres; for bf16 that takes the gradient at v rounded,
+ * where the forward's next norm takes v before).  Outputs, each NULL if not
+ * wanted:
  *   dy_pairs [T*k][d] of dy_dtype: w_j do in the rows that pairs own; rows
  *     that no pair owns keep what they held.  Rows must be owned once.
  *   dtopk_w fp32 [T][k]: <do, y_j>, 0 for a dropped pair.

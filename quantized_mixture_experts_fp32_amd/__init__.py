@@ -553,6 +553,8 @@ def moe_set_ffn_events(gateup_begin=None, gateup_end=None, down_begin=None,
 # pointer (ValueError), launch on the device their tensors are on, and take
 # outputs and workspaces that they create from the memory of the stream they
 # launch on.
+# Results carry no autograd history, whatever their inputs require: the *_bwd
+# calls give the gradients.
 
 def _on_device(fn):
     """Runs fn with its first parameter's device current and, when the keyword

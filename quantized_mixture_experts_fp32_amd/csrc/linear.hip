@@ -20,16 +20,20 @@
 // (launches captured in a graph, weights rotated past the Infinity Cache where
 // they fit):
 //   tokens x K x N        us     bound
-//   1 x 2048 x 2048       3.0    launch
-//   1 x 4096 x 4096       4.3    launch and one round trip to HBM
-//   1 x 8192 x 8192       8.8    3.9 TB/s of codes
+//   1 x 2048 x 2048       3.2    launch
+//   1 x 4096 x 4096       4.4    launch and one round trip to HBM
+//   1 x 8192 x 8192       8.9    3.9 TB/s of codes
 //   4 x 4096 x 50304     22.5    4.7 TB/s (a large copy: 4.9)
-//   16 x 4096 x 12288     7.2    3.7 TB/s
-//   64 x 4096 x 12288    11.5    issue: without any memory traffic 0.8 us less
-//   64 x 4096 x 50304    41      issue: without any memory traffic 35
-//   512 x 4096 x 4096    23.7    725 TFLOP/s
-//   2501 x 4096 x 4096  104      806 TFLOP/s
-//   4096 x 4096 x 4096  141      970 TFLOP/s (a library bf16 product: 1225)
+//   16 x 4096 x 12288     7.4    3.6 TB/s
+//   64 x 4096 x 12288    11.7    issue: one wave a SIMD, which issues in 57 % of
+//                                its cycles, waits for the slot in 15 % and for
+//                                memory, LDS and results in 29 %
+//                                (profiles/counters_linear_w4_batch.txt);
+//                                without any memory traffic 0.8 us less
+//   64 x 4096 x 50304    40      issue: without any memory traffic 35
+//   512 x 4096 x 4096    23.8    721 TFLOP/s
+//   2501 x 4096 x 4096  105      798 TFLOP/s
+//   4096 x 4096 x 4096  143      959 TFLOP/s (a library bf16 product: 1225)
 #include <math.h>
 
 #include <algorithm>
@@ -482,8 +486,9 @@ typedef hipError_t (*RunFn)(const uint16_t*, const uint8_t*, const uint16_t*, co
 // A tile kernel and its time, which goes by blocks a CU: at K = 4096 (32
 // groups) `fixed` + `per` for each block a CU, and 0.065 us per MB of codes.
 // Fitted to 480 shapes of 1 to 512 tokens, K 512 to 14336, N 512 to 50304 (a
-// tenth off on most); the choices by it take 2 % longer than the best kernel
-// of each shape on average.  For up to 1024 inputs (8 groups) four waves do.
+// tenth off on most).  On 120 random shapes of 1 to 4096 tokens the choice took
+// 1.3 % longer than the fastest kernel on average, 29 % at most
+// (profiles/linear_choice.txt).  For up to 1024 inputs (8 groups) four waves do.
 struct Tile {
   int tokens, rows, min_groups, max_groups;
   float fixed, per;
@@ -525,8 +530,10 @@ Choice choose(int T, int N, int K) {
   Choice c = {nullptr, 0};
   float best = 1e30f;
   // The token blocks of a row block run next to each other, and past some 640
-  // tokens their activations do not stay in an XCD's L2: 1.17 times the time
-  // at 1024 tokens, 1.41 at 1536, 1.85 at 2501.
+  // tokens their activations do not stay in an XCD's L2: at K = 4096 1.17 times
+  // the time at 1024 tokens, 1.41 at 1536, 1.85 at 2501.  (By T alone; for the
+  // six of the 120 shapes with more than 640 tokens and K up to 1024 the choice
+  // took 0.5 % longer than the fastest.)
   const float crowd = 1.0f + std::max(T - 640, 0) / 2200.0f;
   for (const Tile& t : kTiles) {
     if (G < t.min_groups || G > t.max_groups) continue;
@@ -555,8 +562,8 @@ Choice choose(int T, int N, int K) {
   // GEMM (blocks of 256 features, two a CU): at K = 4096, one block a CU and
   // two, tiles of 64 tokens 50 and 81 us, of 96 68 and 112, of 128 83 and 140,
   // plus about 4 for the group sums.  E.g. N = 4096: 1024 tokens 49 us as
-  // 64-token tiles of the tile kernel, 52 us here; 2501 tokens 104 us in tiles
-  // of 96, 116 us in tiles of 128.
+  // 64-token tiles of the tile kernel, 52 us here; 2501 tokens 105 us in tiles
+  // of 96, 117 us in tiles of 128.
   if (T > 64) {
     static const struct {
       int tokens;

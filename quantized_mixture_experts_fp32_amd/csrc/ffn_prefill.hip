@@ -20,8 +20,9 @@
 // total is kept in units of the current group's fp16 scale / 8: before a
 // group is accumulated, the total is multiplied by s_prev / s_g, and after
 // the last group by the final scale, so every group's sum is weighted by its
-// own scale without a separate partial accumulator.  A pre-pass kernel computes the group sums
-// (and their splits) of x per token and of h per grouped pair.
+// own scale without a separate partial accumulator (the dense form bounds the
+// ratio, see there).  A pre-pass kernel computes the group sums (and their
+// splits) of x per token and of h per grouped pair.
 //
 // Tiling and pipeline: see the GEMM core below.
 #include "kcommon.hpp"
@@ -281,8 +282,9 @@ void pf_w4_kernel(const uint16_t* __restrict__ act,       // x [T][K] or h [P][K
         codes_load(g + 1, qn, scn);
       }
       // a zero-scale group contributes nothing: the row keeps its running
-      // scale and its codes are masked to 0 (which convert to the offset 192
-      // that the offset MFMA cancels), whatever codes it holds
+      // scale and its codes are masked to 0, whatever codes it holds (in the
+      // experts' forms they convert to the offset 192, which the offset MFMA
+      // takes off again up to its fp32 rounding)
       float r[2];
       uint32_t qmask[2], D[2];
 #pragma unroll

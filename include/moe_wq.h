@@ -629,6 +629,98 @@ int moe_combine_bwd(const void *dout, int dout_dtype, const float *y_pairs,
                     int d, void *dy_pairs, int dy_dtype, float *dtopk_w,
                     void *stream);
 
+/* ---------------------------------------------------------------------
+ * Beside the routed experts: rows in 8-bit integers (activation checkpoints
+ * and the operands of an 8-bit linear map), the passes that read such
+ * checkpoints, and a gated feed-forward block with bf16 weights (a shared
+ * expert; its output is the `add` of moe_combine_residual) with its gradient.
+ * [ExactMoE] Abstract: only the routed experts are quantized to 4 bits, what
+ * runs next to them keeps more.  Dtypes, layout, alignment and overlap as in
+ * the section above; all matrices, 8-bit codes, scales and bias of
+ * moe_linear_i8 are 16-byte aligned, scales of rows 4-byte.
+ *
+ * moe_quantize_i8 -- rows x [T][K] of x_dtype as int8 codes [T][K] and fp32
+ *   scales, one for each group_size = 128 values of a row (the last group may
+ *   be shorter): [T][ceil(K/128)]; group_size = 0: one for the whole row, [T].
+ *     m = max |x| in the group,  scale = m / 127,  code = rne(x * (127 / m))
+ *   in fp32, every step correctly rounded: the same codes and scales on every
+ *   run and machine.  Restored as code * scale, at most about scale / 2 away
+ *   (fp32 roundings of the three steps beside it).  A group with m < 2^-119 is
+ *   stored as zeros; one that holds an infinity or NaN as zeros with scale NaN.
+ * moe_dequantize_i8 -- out = code * scale, [T][K] of out_dtype.
+ * Both require K % 8 == 0, K below 2^20, T below 2^23, T * K below 2^34.
+ *
+ * moe_rmsnorm_i8, moe_rmsnorm_bwd_i8 -- moe_rmsnorm and moe_rmsnorm_bwd with x
+ *   restored from codes and scales of group_size 128; dres and dx are of
+ *   dx_dtype.  Workspace as moe_rmsnorm_bwd.
+ * ------------------------------------------------------------------- */
+int moe_quantize_i8(const void *x, int x_dtype, int T, int K, int group_size,
+                    int8_t *codes, float *scales, void *stream);
+int moe_dequantize_i8(const int8_t *codes, const float *scales, int T, int K,
+                      int group_size, void *out, int out_dtype, void *stream);
+int moe_rmsnorm_i8(const int8_t *codes, const float *scales, const float *gain,
+                   int T, int d, float eps, void *out, int out_dtype,
+                   void *stream);
+int moe_rmsnorm_bwd_i8(const void *dout, int dout_dtype, const int8_t *codes,
+                       const float *scales, const float *gain, const void *dres,
+                       int T, int d, float eps, void *dx, int dx_dtype,
+                       float *dgain, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------
+ * moe_linear_i8 -- y = x W^T + bias with both operands in 8-bit integers, a
+ * scale for each token and each feature.
+ *   out[t][n] = sx[t] * sw[n] * sum_k qx[t][k] * qw[n][k] + bias[n]
+ * codes int8 [N][K] and scales fp32 [N] as moe_quantize_i8 returns them for the
+ * rows of W with group_size 0; bias fp32 [N] or NULL; out [T][N] of out_dtype.
+ * x: int8 codes [T][K] with x_scales fp32 [T], or (x_scales NULL) bf16 [T][K],
+ * which the call quantizes by token first, as moe_quantize_i8 does.  The sum is
+ * exact (int32); the scaling and the bias are fp32, rounded once on store.  A
+ * token whose row holds an infinity or NaN gives a row of NaN.
+ * Requires K % 16 == 0, N % 8 == 0, K below 2^17, T below 2^23, N below 2^28,
+ * T * K and T * N below 2^34.
+ * ws / ws_bytes: at least moe_linear_i8_ws_bytes(T, N, K, x_scales != NULL),
+ * 256-byte aligned, no contents carried between calls.
+ * ------------------------------------------------------------------- */
+size_t moe_linear_i8_ws_bytes(int T, int N, int K, int x_quantized);
+int moe_linear_i8(const void *x, const float *x_scales, int T, int N, int K,
+                  const int8_t *codes, const float *scales, const float *bias,
+                  void *out, int out_dtype, void *ws, size_t ws_bytes,
+                  void *stream);
+
+/* ---------------------------------------------------------------------
+ * moe_gated_ffn -- a gated feed-forward block with bf16 weights.
+ *   [g u] = x Wgu^T,  h = silu(g) * u,  out = h Wd^T
+ * x bf16 [T][d]; w_gate_up bf16 [2f][d] (gate rows, then up rows); w_down bf16
+ * [d][f]; out [T][d] of out_dtype; gate_up bf16 [T][2f], the pre-activations
+ * for the gradient, or NULL.  Sums are fp32; h is rounded to bf16 between the
+ * products, as the experts' is.
+ * moe_gated_ffn_bwd -- its gradient for dout [T][d] of dout_dtype (fp32 is
+ * rounded to bf16 first).  Outputs, each NULL if not wanted: dx bf16 [T][d];
+ * dw_gate_up [2f][d] and dw_down [d][f] of dw_dtype (overwritten, zeros for
+ * T == 0).
+ *   x: bf16 [T][d], or (x_scales not NULL) codes of moe_quantize_i8 with
+ *     group_size 128, restored and rounded to bf16.
+ *   gate_up: as the forward call left it, or NULL: computed again from x.
+ * dg, du and h are rounded to bf16 between the products.
+ * Both require d % 8 == 0, f % 8 == 0, d and f at most 65536, T below 2^23,
+ * T * d below 2^34, T * f below 2^33.  ws / ws_bytes: at least the query's
+ * bytes (dout_dtype, x_scales != NULL, gate_up != NULL), 256-byte aligned, no
+ * contents carried between calls.
+ * ------------------------------------------------------------------- */
+size_t moe_gated_ffn_ws_bytes(int T, int d, int f);
+int moe_gated_ffn(const void *x_bf16, const void *w_gate_up_bf16,
+                  const void *w_down_bf16, int T, int d, int f, void *out,
+                  int out_dtype, void *gate_up_bf16, void *ws, size_t ws_bytes,
+                  void *stream);
+size_t moe_gated_ffn_bwd_ws_bytes(int T, int d, int f, int dout_dtype,
+                                  int x_quantized, int gate_up_kept);
+int moe_gated_ffn_bwd(const void *dout, int dout_dtype, const void *x,
+                      const float *x_scales, const void *gate_up_bf16,
+                      const void *w_gate_up_bf16, const void *w_down_bf16, int T,
+                      int d, int f, void *dx_bf16, void *dw_gate_up,
+                      void *dw_down, int dw_dtype, void *ws, size_t ws_bytes,
+                      void *stream);
+
 #ifdef __cplusplus
 }
 #endif

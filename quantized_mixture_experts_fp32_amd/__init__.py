@@ -43,7 +43,10 @@ EXPORTS = ("moe_status_str", "moe_last_error", "moe_route_ws_bytes", "moe_route"
            "moe_linear_w4_ws_bytes", "moe_linear_w4_kernel", "moe_linear_w4", "moe_rmsnorm",
            "moe_rmsnorm_bwd_ws_bytes", "moe_rmsnorm_bwd", "moe_combine_residual",
            "moe_combine_residual_bwd_ws_bytes", "moe_combine_residual_bwd", "moe_dispatch",
-           "moe_dispatch_bwd", "moe_combine_bwd")
+           "moe_dispatch_bwd", "moe_combine_bwd", "moe_quantize_i8", "moe_dequantize_i8",
+           "moe_rmsnorm_i8", "moe_rmsnorm_bwd_i8", "moe_linear_i8_ws_bytes", "moe_linear_i8",
+           "moe_gated_ffn_ws_bytes", "moe_gated_ffn", "moe_gated_ffn_bwd_ws_bytes",
+           "moe_gated_ffn_bwd")
 
 
 class MoeError(RuntimeError):
@@ -127,9 +130,23 @@ def load_library():
     lib.moe_dispatch.argtypes = [vp, i32, vp, vp, i32, i32, i32, vp, vp]
     lib.moe_dispatch_bwd.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp]
     lib.moe_combine_bwd.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp]
+    lib.moe_quantize_i8.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp]
+    lib.moe_dequantize_i8.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp]
+    lib.moe_rmsnorm_i8.argtypes = [vp, vp, vp, i32, i32, f32, vp, i32, vp]
+    lib.moe_rmsnorm_bwd_i8.argtypes = [vp, i32, vp, vp, vp, vp, i32, i32, f32, vp, i32, vp, vp,
+                                       sz, vp]
+    lib.moe_linear_i8_ws_bytes.argtypes, lib.moe_linear_i8_ws_bytes.restype = [i32] * 4, sz
+    lib.moe_linear_i8.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp, i32, vp, sz, vp]
+    lib.moe_gated_ffn_ws_bytes.argtypes, lib.moe_gated_ffn_ws_bytes.restype = [i32] * 3, sz
+    lib.moe_gated_ffn.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, sz, vp]
+    lib.moe_gated_ffn_bwd_ws_bytes.argtypes = [i32] * 6
+    lib.moe_gated_ffn_bwd_ws_bytes.restype = sz
+    lib.moe_gated_ffn_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, i32,
+                                      vp, sz, vp]
     for name in ("moe_linear_w4", "moe_rmsnorm", "moe_rmsnorm_bwd", "moe_combine_residual",
                  "moe_combine_residual_bwd", "moe_dispatch", "moe_dispatch_bwd",
-                 "moe_combine_bwd"):
+                 "moe_combine_bwd", "moe_quantize_i8", "moe_dequantize_i8", "moe_rmsnorm_i8",
+                 "moe_rmsnorm_bwd_i8", "moe_linear_i8", "moe_gated_ffn", "moe_gated_ffn_bwd"):
         getattr(lib, name).restype = i32
     for name in ("moe_route", "moe_permute", "moe_route_permute", "moe_expert_ffn_wq",
                  "moe_combine", "moe_layer_forward_wq", "moe_layer_forward_wq_noalloc",
@@ -626,6 +643,17 @@ def _types():
             (torch.float32,), (torch.int32,))
 
 
+@functools.lru_cache(None)
+def _i8():
+    import torch
+    return (torch.int8,)
+
+
+def _groups(n):
+    """Groups of 128 in a row of n values, the last may be shorter."""
+    return -(-n // MOE_GROUP)
+
+
 def _code(t):
     """The ABI's dtype code of a row tensor."""
     return MOE_OUT_F32 if t.element_size() == 4 else MOE_OUT_BF16
@@ -703,38 +731,60 @@ def moe_linear_w4(x, codes, scales, bias=None, out=None, out_dtype=MOE_OUT_BF16,
 
 
 @_on_device
-def moe_rmsnorm(x, gain=None, eps=1e-6, out=None, out_dtype=MOE_OUT_BF16):
-    """The norm in front of a block: x [T][d] (bf16 or fp32), gain fp32 [d]."""
+def moe_rmsnorm(x, gain=None, eps=1e-6, out=None, out_dtype=MOE_OUT_BF16, x_scales=None):
+    """The norm in front of a block: x [T][d] (bf16 or fp32), gain fp32 [d].
+    With x_scales [T][ceil(d/128)], x is an 8-bit checkpoint: the int8 codes
+    that moe_quantize_i8 returned beside those scales."""
     fn = "moe_rmsnorm"
     _, row, f32, _ = _types()
     if x.dim() != 2:
         raise ValueError(f"{fn}: x must be [T][d]")
     T, d = x.shape
-    _rows(fn, "x", x, (T, d), row)
+    _rows(fn, "x", x, (T, d), row if x_scales is None else _i8())
+    if x_scales is not None:
+        _rows(fn, "x_scales", x_scales, (T, _groups(d)), f32, x)
     if gain is not None:
         _rows(fn, "gain", gain, (d,), f32, x)
     out = _out_rows(fn, "out", out, (T, d), out_dtype, x)
-    rc = (_lib or load_library()).moe_rmsnorm(x.data_ptr(), _code(x), _addr(gain), T, d, eps,
-                                              out.data_ptr(), out_dtype, _raw_stream(x))
+    lib = _lib or load_library()
+    if x_scales is None:
+        rc = lib.moe_rmsnorm(x.data_ptr(), _code(x), _addr(gain), T, d, eps, out.data_ptr(),
+                             out_dtype, _raw_stream(x))
+    else:
+        rc = lib.moe_rmsnorm_i8(x.data_ptr(), x_scales.data_ptr(), _addr(gain), T, d, eps,
+                                out.data_ptr(), out_dtype, _raw_stream(x))
     if rc:
         _check(fn, rc)
     return out
 
 
 @_on_device
-def moe_rmsnorm_bwd(dout, x, gain=None, eps=1e-6, dres=None, dx=None, dgain=None, ws=None):
+def moe_rmsnorm_bwd(dout, x, gain=None, eps=1e-6, dres=None, dx=None, dgain=None, ws=None,
+                    x_scales=None, dx_dtype=None):
     """Gradient of moe_rmsnorm, plus dres (the gradient of x past the norm)
-    -> (dx in x's type, dgain fp32 [d]; None when there is no gain)."""
+    -> (dx in x's type, dgain fp32 [d]; None when there is no gain).
+    With x_scales, x is an 8-bit checkpoint (as in moe_rmsnorm); dx and dres
+    then have the type dx_dtype (bf16 unless given)."""
     fn = "moe_rmsnorm_bwd"
     _, row, f32, _ = _types()
     if dout.dim() != 2:
         raise ValueError(f"{fn}: dout must be [T][d]")
     T, d = dout.shape
     _rows(fn, "dout", dout, (T, d), row)
-    _rows(fn, "x", x, (T, d), row, dout)
+    if x_scales is None:
+        _rows(fn, "x", x, (T, d), row, dout)
+        if dx_dtype not in (None, _code(x)):
+            raise ValueError(f"{fn}: dx_dtype is for 8-bit checkpoints, dx has x's type")
+        dx_dtype = _code(x)
+        like_x = (x.dtype,)
+    else:
+        _rows(fn, "x", x, (T, d), _i8(), dout)
+        _rows(fn, "x_scales", x_scales, (T, _groups(d)), f32, dout)
+        dx_dtype = MOE_OUT_BF16 if dx_dtype is None else dx_dtype
+        like_x = _types()[2 if dx_dtype == MOE_OUT_F32 else 0]
     if dres is not None:
-        _rows(fn, "dres", dres, (T, d), (x.dtype,), dout)
-    dx = _out_rows(fn, "dx", dx, (T, d), _code(x), dout)
+        _rows(fn, "dres", dres, (T, d), like_x, dout)
+    dx = _out_rows(fn, "dx", dx, (T, d), dx_dtype, dout)
     if gain is not None:
         _rows(fn, "gain", gain, (d,), f32, dout)
         dgain = _out_f32(fn, "dgain", dgain, (d,), dout)
@@ -742,9 +792,15 @@ def moe_rmsnorm_bwd(dout, x, gain=None, eps=1e-6, dres=None, dx=None, dgain=None
         raise ValueError(f"{fn}: dgain without gain")
     lib = _lib or load_library()
     ws = _workspace(fn, ws, lib.moe_rmsnorm_bwd_ws_bytes(T, d) if dgain is not None else 0, dout)
-    rc = lib.moe_rmsnorm_bwd(dout.data_ptr(), _code(dout), x.data_ptr(), _code(x), _addr(gain),
-                             _addr(dres), T, d, eps, dx.data_ptr(), _addr(dgain), *_ws_args(ws),
-                             _raw_stream(dout))
+    if x_scales is None:
+        rc = lib.moe_rmsnorm_bwd(dout.data_ptr(), _code(dout), x.data_ptr(), _code(x),
+                                 _addr(gain), _addr(dres), T, d, eps, dx.data_ptr(), _addr(dgain),
+                                 *_ws_args(ws), _raw_stream(dout))
+    else:
+        rc = lib.moe_rmsnorm_bwd_i8(dout.data_ptr(), _code(dout), x.data_ptr(),
+                                    x_scales.data_ptr(), _addr(gain), _addr(dres), T, d, eps,
+                                    dx.data_ptr(), dx_dtype, _addr(dgain), *_ws_args(ws),
+                                    _raw_stream(dout))
     if rc:
         _check(fn, rc)
     return dx, dgain
@@ -945,6 +1001,200 @@ def moe_combine_bwd(dout, y_pairs, pair_pos, topk_w, dy_dtype=MOE_OUT_F32, dy_pa
     return dy_pairs, dtopk_w
 
 
+# ------------------------------------- beside the routed experts: 8-bit rows
+def _i8_inputs(fn, codes, scales, like=None):
+    """Checks 8-bit rows: codes int8 [T][K] with scales fp32 [T][ceil(K/128)]
+    or [T].  Returns (T, K, group size)."""
+    if codes.dim() != 2 or scales.dim() not in (1, 2):
+        raise ValueError(f"{fn}: codes must be [T][K], scales [T][ceil(K/128)] or [T]")
+    T, K = codes.shape
+    _rows(fn, "codes", codes, (T, K), _i8(), like)
+    by_row = scales.dim() == 1
+    _rows(fn, "scales", scales, (T,) if by_row else (T, _groups(K)), _types()[2], codes)
+    return T, K, 0 if by_row else MOE_GROUP
+
+
+@_on_device
+def moe_quantize_i8(x, group=MOE_GROUP, codes=None, scales=None):
+    """Rows x [T][K] (bf16 or fp32) in 8-bit integers -> (codes int8 [T][K],
+    scales fp32).  group 128: a scale for each 128 values of a row,
+    [T][ceil(K/128)], the form of activation checkpoints; group 0: one scale a
+    row, [T], the form of moe_linear_i8's operands."""
+    import torch
+    fn = "moe_quantize_i8"
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: x must be [T][K]")
+    T, K = x.shape
+    _rows(fn, "x", x, (T, K), _types()[1])
+    if group not in (0, MOE_GROUP):
+        raise ValueError(f"{fn}: group is {group}, expected 128 or 0 (a whole row)")
+    codes = (torch.empty_like(x, dtype=torch.int8) if codes is None
+             else _rows(fn, "codes", codes, (T, K), _i8(), x))
+    scales = _out_f32(fn, "scales", scales, (T, _groups(K)) if group else (T,), x)
+    rc = (_lib or load_library()).moe_quantize_i8(x.data_ptr(), _code(x), T, K, group,
+                                                  codes.data_ptr(), scales.data_ptr(),
+                                                  _raw_stream(x))
+    if rc:
+        _check(fn, rc)
+    return codes, scales
+
+
+@_on_device
+def moe_dequantize_i8(codes, scales, out=None, out_dtype=MOE_OUT_BF16):
+    """What moe_quantize_i8 stored: codes times scales, [T][K] bf16 or fp32."""
+    fn = "moe_dequantize_i8"
+    T, K, group = _i8_inputs(fn, codes, scales)
+    out = _out_rows(fn, "out", out, (T, K), out_dtype, codes)
+    rc = (_lib or load_library()).moe_dequantize_i8(codes.data_ptr(), scales.data_ptr(), T, K,
+                                                    group, out.data_ptr(), out_dtype,
+                                                    _raw_stream(codes))
+    if rc:
+        _check(fn, rc)
+    return out
+
+
+def moe_linear_i8_ws_bytes(T, N, K, x_quantized=False):
+    return int(load_library().moe_linear_i8_ws_bytes(T, N, K, x_quantized))
+
+
+@_on_device
+def moe_linear_i8(x, codes, scales, bias=None, out=None, out_dtype=MOE_OUT_BF16, ws=None,
+                  x_scales=None):
+    """x [T][K] times a matrix in 8-bit integers -> [T][N] (bf16 or fp32).
+
+    codes int8 [N][K] and scales fp32 [N] as moe_quantize_i8(w, group=0)
+    returns them; bias fp32 [N] or None.  x is bf16, quantized by token inside
+    the call, or int8 codes with x_scales fp32 [T].
+    """
+    fn = "moe_linear_i8"
+    bf, _, f32, _ = _types()
+    if x.dim() != 2 or codes.dim() != 2:
+        raise ValueError(f"{fn}: x must be [T][K] and codes [N][K]")
+    T, K = x.shape
+    N = codes.shape[0]
+    if N >= 1 << 31:
+        raise ValueError(f"{fn}: codes have {N} rows, sizes must be below 2^31")
+    _rows(fn, "x", x, (T, K), bf if x_scales is None else _i8())
+    if x_scales is not None:
+        _rows(fn, "x_scales", x_scales, (T,), f32, x)
+    _rows(fn, "codes", codes, (N, K), _i8(), x)
+    _rows(fn, "scales", scales, (N,), f32, x)
+    if bias is not None:
+        _rows(fn, "bias", bias, (N,), f32, x)
+    out = _out_rows(fn, "out", out, (T, N), out_dtype, x)
+    lib = _lib or load_library()
+    ws = _workspace(fn, ws, lib.moe_linear_i8_ws_bytes(T, N, K, x_scales is not None), x)
+    rc = lib.moe_linear_i8(x.data_ptr(), _addr(x_scales), T, N, K, codes.data_ptr(),
+                           scales.data_ptr(), _addr(bias), out.data_ptr(), out_dtype,
+                           *_ws_args(ws), _raw_stream(x))
+    if rc:
+        _check(fn, rc)
+    return out
+
+
+# --------------------------------- beside the routed experts: a shared expert
+def _gated_weights(fn, w_gate_up, w_down, d, like):
+    """Checks the block's weights; returns f."""
+    bf = _types()[0]
+    if w_gate_up.dim() != 2 or w_down.dim() != 2:
+        raise ValueError(f"{fn}: w_gate_up must be [2f][d] and w_down [d][f]")
+    f = w_down.shape[1]
+    if f >= 1 << 30:
+        raise ValueError(f"{fn}: f = {f}, sizes must be below 2^31")
+    _rows(fn, "w_gate_up", w_gate_up, (2 * f, d), bf, like)
+    _rows(fn, "w_down", w_down, (d, f), bf, like)
+    return f
+
+
+def moe_gated_ffn_ws_bytes(T, d, f):
+    return int(load_library().moe_gated_ffn_ws_bytes(T, d, f))
+
+
+@_on_device
+def moe_gated_ffn(x, w_gate_up, w_down, out=None, out_dtype=MOE_OUT_BF16, save=False,
+                  gate_up=None, ws=None):
+    """A gated feed-forward block, (silu(x Wg^T) * (x Wu^T)) Wd^T -> (out,
+    gate_up).
+
+    x bf16 [T][d], w_gate_up bf16 [2f][d] (gate rows, then up rows), w_down
+    bf16 [d][f], out [T][d] (bf16 or fp32).  gate_up bf16 [T][2f], the
+    pre-activations that the gradient can use, is stored when `save` is true or
+    a tensor for it is given, otherwise it is None.
+    """
+    fn = "moe_gated_ffn"
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: x must be [T][d]")
+    T, d = x.shape
+    _rows(fn, "x", x, (T, d), _types()[0])
+    f = _gated_weights(fn, w_gate_up, w_down, d, x)
+    out = _out_rows(fn, "out", out, (T, d), out_dtype, x)
+    if save or gate_up is not None:
+        gate_up = _out_rows(fn, "gate_up", gate_up, (T, 2 * f), MOE_OUT_BF16, x)
+    lib = _lib or load_library()
+    ws = _workspace(fn, ws, lib.moe_gated_ffn_ws_bytes(T, d, f), x)
+    rc = lib.moe_gated_ffn(x.data_ptr(), w_gate_up.data_ptr(), w_down.data_ptr(), T, d, f,
+                           out.data_ptr(), out_dtype, _addr(gate_up), *_ws_args(ws),
+                           _raw_stream(x))
+    if rc:
+        _check(fn, rc)
+    return out, gate_up
+
+
+GatedFfnGrads = collections.namedtuple("GatedFfnGrads", "dx dw_gate_up dw_down")
+
+
+def moe_gated_ffn_bwd_ws_bytes(T, d, f, dout_dtype=MOE_OUT_BF16, x_quantized=False,
+                               gate_up_kept=False):
+    return int(load_library().moe_gated_ffn_bwd_ws_bytes(T, d, f, dout_dtype, x_quantized,
+                                                         gate_up_kept))
+
+
+@_on_device
+def moe_gated_ffn_bwd(dout, x, w_gate_up, w_down, x_scales=None, gate_up=None,
+                      dw_dtype=MOE_OUT_BF16, dx=None, dw_gate_up=None, dw_down=None,
+                      need_dx=True, need_dw=True, ws=None):
+    """Gradient of moe_gated_ffn for dout [T][d] (bf16 or fp32), as a
+    GatedFfnGrads (dx bf16 [T][d]; dw_gate_up [2f][d] and dw_down [d][f] of
+    dw_dtype; None for what need_dx or need_dw leave out).
+
+    x as in the forward call, or an 8-bit checkpoint of it (the codes of
+    moe_quantize_i8, with its scales as x_scales).  gate_up: what the forward
+    call saved; without it the pre-activations are computed again from x.
+    """
+    fn = "moe_gated_ffn_bwd"
+    bf, row, f32, _ = _types()
+    if dout.dim() != 2:
+        raise ValueError(f"{fn}: dout must be [T][d]")
+    T, d = dout.shape
+    _rows(fn, "dout", dout, (T, d), row)
+    _rows(fn, "x", x, (T, d), bf if x_scales is None else _i8(), dout)
+    if x_scales is not None:
+        _rows(fn, "x_scales", x_scales, (T, _groups(d)), f32, dout)
+    f = _gated_weights(fn, w_gate_up, w_down, d, dout)
+    if gate_up is not None:
+        _rows(fn, "gate_up", gate_up, (T, 2 * f), bf, dout)
+    for name, g, need in (("dx", dx, need_dx), ("dw_gate_up", dw_gate_up, need_dw),
+                          ("dw_down", dw_down, need_dw)):
+        if g is not None and not need:
+            raise ValueError(f"{fn}: {name} given, but not needed")
+    if need_dx:
+        dx = _out_rows(fn, "dx", dx, (T, d), MOE_OUT_BF16, dout)
+    if need_dw:
+        dw_gate_up = _out_rows(fn, "dw_gate_up", dw_gate_up, (2 * f, d), dw_dtype, dout)
+        dw_down = _out_rows(fn, "dw_down", dw_down, (d, f), dw_dtype, dout)
+    lib = _lib or load_library()
+    code = _code(dout)
+    ws = _workspace(fn, ws, lib.moe_gated_ffn_bwd_ws_bytes(T, d, f, code, x_scales is not None,
+                                                           gate_up is not None), dout)
+    rc = lib.moe_gated_ffn_bwd(dout.data_ptr(), code, x.data_ptr(), _addr(x_scales),
+                               _addr(gate_up), w_gate_up.data_ptr(), w_down.data_ptr(), T, d, f,
+                               _addr(dx), _addr(dw_gate_up), _addr(dw_down), dw_dtype,
+                               *_ws_args(ws), _raw_stream(dout))
+    if rc:
+        _check(fn, rc)
+    return GatedFfnGrads(dx, dw_gate_up, dw_down)
+
+
 # ------------------------------------------------------ expert slot cache
 def _np_ptr(a):
     return ctypes.c_void_p(a.ctypes.data)
@@ -1130,11 +1380,18 @@ class MoeLayer(_StepBuffers):
 
     def forward_block(self, residual, gain=None, eps=1e-6, add=None, post_gain=None, gate=None,
                       gate_mode=MOE_GATE_NONE, res_scale=1.0, next_gain=None, out=None,
-                      next_out=None, path=MOE_PATH_AUTO, stream=None):
+                      next_out=None, path=MOE_PATH_AUTO, stream=None, shared=None):
         """The layer as a residual block of a model: moe_rmsnorm of the
         residual stream, routing, expert FFN, and moe_combine_residual in the
         place of the combine -> (out, next_out or None), as that call.
-        residual [T][d] (bf16 or fp32) on the layer's device."""
+        residual [T][d] (bf16 or fp32) on the layer's device.  shared: a
+        GatedFfn that runs beside the routed experts on the same normed rows
+        and takes the place of `add`."""
+        if shared is not None and add is not None:
+            raise ValueError("forward_block: shared and add are given, one is the other's place")
+        if shared is not None and (shared.d != self.d or shared.w_down.device != self.wr.device):
+            raise ValueError(f"forward_block: shared has width {shared.d} on "
+                             f"{shared.w_down.device}, the layer {self.d} on {self.wr.device}")
         if residual.dim() != 2 or residual.shape[1] != self.d:
             raise ValueError(f"forward_block: residual has shape {tuple(residual.shape)}, "
                              f"expected [T][{self.d}]")
@@ -1148,13 +1405,17 @@ class MoeLayer(_StepBuffers):
             with _launch_on(stream, (residual, gain, add, post_gain, gate, next_gain, out,
                                      next_out)):
                 return self.forward_block(residual, gain, eps, add, post_gain, gate, gate_mode,
-                                          res_scale, next_gain, out, next_out, path)
+                                          res_scale, next_gain, out, next_out, path,
+                                          shared=shared)
         if residual.is_cuda and residual.get_device() != _current_device():
             import torch
             with torch.cuda.device(residual.device):
                 return self.forward_block(residual, gain, eps, add, post_gain, gate, gate_mode,
-                                          res_scale, next_gain, out, next_out, path)
+                                          res_scale, next_gain, out, next_out, path,
+                                          shared=shared)
         x = moe_rmsnorm(residual, gain, eps=eps)
+        if shared is not None:
+            add = shared.forward(x, out_dtype=_code(residual))
         self._buffers(residual.shape[0], x)
         moe_route_permute(x, self.wr, self.bias, self.k, self.ws_rp, self.topk_idx,
                           self.topk_w, self.offsets, self.sorted_pair, self.pair_pos)
@@ -1213,3 +1474,56 @@ class MoeLayer(_StepBuffers):
         with torch.cuda.graph(g):  # binds to the capture stream
             self.bind(x, out, weights, path, out_dtype)()
         return g
+
+
+# ------------------------------------------------------------ a shared expert
+class GatedFfn:
+    """Resident bf16 weights of a gated feed-forward block: a shared expert
+    (`MoeLayer.forward_block(shared=...)`), or a dense block of its own in a
+    model that is trained with 8-bit checkpoints (forward_block keeps one of
+    the residual stream, backward_block computes the rest again from it)."""
+
+    def __init__(self, w_gate_up, w_down):
+        _rows("GatedFfn", "w_down", w_down, tuple(w_down.shape), _types()[0])
+        self.f = _gated_weights("GatedFfn", w_gate_up, w_down, w_down.shape[0], w_down)
+        self.d = w_down.shape[0]
+        self.w_gate_up, self.w_down = w_gate_up, w_down
+
+    def forward(self, x, out=None, out_dtype=MOE_OUT_BF16, stream=None):
+        """moe_gated_ffn of x [T][d] -> out."""
+        return moe_gated_ffn(x, self.w_gate_up, self.w_down, out=out, out_dtype=out_dtype,
+                             stream=stream)[0]
+
+    @contextlib.contextmanager
+    def _stream_of(self, fn, first, stream, *values):
+        if first.is_cuda and stream.device != first.device:
+            raise ValueError(f"{fn}: stream of {stream.device}, tensors on {first.device}")
+        with _launch_on(stream, (first, self.w_gate_up, self.w_down, *values)):
+            yield
+
+    def forward_block(self, residual, gain=None, eps=1e-6, keep=True, stream=None):
+        """residual + block(moe_rmsnorm(residual)) -> (out, kept); residual
+        [T][d] (bf16 or fp32).  kept: the residual as an 8-bit checkpoint
+        (codes, scales), None if not `keep`."""
+        if stream is not None:
+            with self._stream_of("forward_block", residual, stream, gain):
+                return self.forward_block(residual, gain, eps, keep)
+        x = moe_rmsnorm(residual, gain, eps=eps)
+        kept = moe_quantize_i8(residual) if keep else None
+        y = self.forward(x, out_dtype=_code(residual))
+        return moe_combine_residual(residual, add=y)[0], kept
+
+    def backward_block(self, dout, kept, gain=None, eps=1e-6, dw_dtype=MOE_OUT_BF16,
+                       stream=None):
+        """Gradient of forward_block at the checkpointed residual, for dout
+        [T][d] in the residual's type -> (dresidual in that type, dgain fp32 [d]
+        or None, dw_gate_up, dw_down)."""
+        codes, scales = kept
+        if stream is not None:
+            with self._stream_of("backward_block", dout, stream, gain, codes, scales):
+                return self.backward_block(dout, kept, gain, eps, dw_dtype)
+        x = moe_rmsnorm(codes, gain, eps=eps, x_scales=scales)
+        g = moe_gated_ffn_bwd(dout, x, self.w_gate_up, self.w_down, dw_dtype=dw_dtype)
+        dres, dgain = moe_rmsnorm_bwd(g.dx, codes, gain, eps=eps, dres=dout, x_scales=scales,
+                                      dx_dtype=_code(dout))
+        return dres, dgain, g.dw_gate_up, g.dw_down

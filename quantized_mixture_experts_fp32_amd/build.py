@@ -12,7 +12,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["abi.cpp", "route.hip", "permute.hip", "quant.hip", "ffn.hip",
            "ffn_decode.hip", "ffn_bitplane.hip", "ffn_prefill.hip",
            "combine.hip", "alloc.hip", "cache.hip", "cache.cpp", "noalloc.hip", "retile.hip",
-           "norm.hip", "block_out.hip", "sort.hip", "linear.hip"]
+           "norm.hip", "block_out.hip", "sort.hip", "linear.hip", "quant_i8.hip", "linear_i8.hip",
+           "gated_ffn.hip"]
 # Packed fp32 VALU instructions stay disabled in every HIP build here.
 # MFMA accumulators are allocated in ordinary VGPRs (not AGPRs): the kernels
 # rescale and convert accumulators with VALU instructions, which would

@@ -593,9 +593,24 @@ int moe_rmsnorm(const void* x, int x_dtype, const float* gain, int T, int d, flo
   if (!x || !out) return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: null pointer");
   if (!aligned(x, 16) || !aligned(out, 16) || !aligned(gain, 16))
     return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: misaligned pointer");
-  return hip_status(moe::launch_rmsnorm(x, x_dtype == MOE_OUT_F32, gain, T, d, eps, out,
+  return hip_status(moe::launch_rmsnorm(x, x_dtype == MOE_OUT_F32, nullptr, gain, T, d, eps, out,
                                         out_dtype == MOE_OUT_F32, (hipStream_t)stream),
                     "moe_rmsnorm");
+}
+
+int moe_rmsnorm_i8(const int8_t* codes, const float* scales, const float* gain, int T, int d,
+                   float eps, void* out, int out_dtype, void* stream) {
+  const char* what = "moe_rmsnorm_i8";
+  int rc = row_check(what, T, d, 0, 0, out_dtype, out_dtype);
+  if (!rc) rc = eps_check(what, eps);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if (!codes || !scales || !out) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16) || !aligned(gain, 16))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  return hip_status(moe::launch_rmsnorm(codes, 0, scales, gain, T, d, eps, out,
+                                        out_dtype == MOE_OUT_F32, (hipStream_t)stream),
+                    what);
 }
 
 size_t moe_rmsnorm_bwd_ws_bytes(int T, int d) {
@@ -617,8 +632,28 @@ int moe_rmsnorm_bwd(const void* dout, int dout_dtype, const void* x, int x_dtype
     return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
   if (T == 0 && !dgain) return ok();
   return hip_status(moe::launch_rmsnorm_bwd(dout, dout_dtype == MOE_OUT_F32, x,
-                                            x_dtype == MOE_OUT_F32, gain, dres, T, d, eps, dx,
-                                            dgain, ws, (hipStream_t)stream),
+                                            x_dtype == MOE_OUT_F32, nullptr, gain, dres, T, d,
+                                            eps, dx, dgain, ws, (hipStream_t)stream),
+                    what);
+}
+
+int moe_rmsnorm_bwd_i8(const void* dout, int dout_dtype, const int8_t* codes, const float* scales,
+                       const float* gain, const void* dres, int T, int d, float eps, void* dx,
+                       int dx_dtype, float* dgain, void* ws, size_t ws_bytes, void* stream) {
+  const char* what = "moe_rmsnorm_bwd_i8";
+  int rc = row_check(what, T, d, 0, 0, dout_dtype, dx_dtype);
+  if (!rc) rc = eps_check(what, eps);
+  if (!rc) rc = colsum_ws_check(what, dgain, moe_rmsnorm_bwd_ws_bytes(T, d), ws, ws_bytes);
+  if (rc) return rc;
+  if (T > 0 && (!dout || !codes || !scales || !dx))
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(dout, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(dres, 16) ||
+      !aligned(dx, 16) || !aligned(gain, 16) || !aligned(dgain, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  if (T == 0 && !dgain) return ok();
+  return hip_status(moe::launch_rmsnorm_bwd(dout, dout_dtype == MOE_OUT_F32, codes,
+                                            dx_dtype == MOE_OUT_F32, scales, gain, dres, T, d,
+                                            eps, dx, dgain, ws, (hipStream_t)stream),
                     what);
 }
 
@@ -750,4 +785,191 @@ int moe_combine_bwd(const void* dout, int dout_dtype, const float* y_pairs,
                                             topk_w, T, k, d, dy_pairs, dy_dtype == MOE_OUT_F32,
                                             dtopk_w, (hipStream_t)stream),
                     what);
+}
+
+// ------------------------------------------ 8-bit rows, the gated block
+
+// Why a call on T rows of K values, eight a chunk, refuses these sizes, or null.
+static const char* rows_refusal(int T, int K, int* status) {
+  *status = MOE_ERR_INVALID_ARG;
+  if (T < 0 || K <= 0) return "bad size";
+  *status = MOE_ERR_UNSUPPORTED;
+  if (K % 8) return "row length not a multiple of 8";
+  if (K >= 1 << 20) return "row length not below 2^20";
+  if (T >= 1 << 23 || (long long)T * K >= (1LL << 34)) return "T not below 2^23 or T*K below 2^34";
+  return nullptr;
+}
+
+static int i8_rows_check(const char* what, int T, int K, int group_size, int dtype) {
+  int status;
+  if (const char* why = rows_refusal(T, K, &status))
+    return fail(status, "%s: %s (T=%d K=%d)", what, why, T, K);
+  if (!known_dtype(dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+  if (group_size != 0 && group_size != MOE_GROUP)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: group_size=%d (only 128, or 0: a whole row)", what,
+                group_size);
+  return MOE_OK;
+}
+
+int moe_quantize_i8(const void* x, int x_dtype, int T, int K, int group_size, int8_t* codes,
+                    float* scales, void* stream) {
+  const char* what = "moe_quantize_i8";
+  if (int rc = i8_rows_check(what, T, K, group_size, x_dtype)) return rc;
+  if (T == 0) return ok();
+  if (!x || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  return hip_status(moe::launch_quantize_i8(x, x_dtype == MOE_OUT_F32, T, K, group_size == 0,
+                                            codes, scales, (hipStream_t)stream),
+                    what);
+}
+
+int moe_dequantize_i8(const int8_t* codes, const float* scales, int T, int K, int group_size,
+                      void* out, int out_dtype, void* stream) {
+  const char* what = "moe_dequantize_i8";
+  if (int rc = i8_rows_check(what, T, K, group_size, out_dtype)) return rc;
+  if (T == 0) return ok();
+  if (!codes || !scales || !out) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(out, 16))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  return hip_status(moe::launch_dequantize_i8(codes, scales, T, K, group_size == 0, out,
+                                              out_dtype == MOE_OUT_F32, (hipStream_t)stream),
+                    what);
+}
+
+static int ws_check(const char* what, size_t need, const void* ws, size_t ws_bytes) {
+  if (!need) return MOE_OK;
+  if (!ws || ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", what,
+                ws ? ws_bytes : (size_t)0, need);
+  if (!aligned(ws, 256))
+    return fail(MOE_ERR_INVALID_ARG, "%s: workspace not 256-byte aligned", what);
+  return MOE_OK;
+}
+
+static const char* linear_i8_refusal(int T, int N, int K, int* status) {
+  *status = MOE_ERR_INVALID_ARG;
+  if (T < 0 || N <= 0 || K <= 0) return "bad size";
+  *status = MOE_ERR_UNSUPPORTED;
+  if (K % 16) return "K not a multiple of 16";
+  if (N % 8) return "N not a multiple of 8";
+  if (K >= 1 << 17) return "K not below 2^17 (int32 sums)";
+  if (T >= 1 << 23 || N >= 1 << 28) return "T not below 2^23 or N not below 2^28";
+  if ((long long)T * K >= (1LL << 34) || (long long)T * N >= (1LL << 34))
+    return "T*K and T*N must be below 2^34";
+  return nullptr;
+}
+
+size_t moe_linear_i8_ws_bytes(int T, int N, int K, int x_quantized) {
+  int status;
+  if (T == 0 || linear_i8_refusal(T, N, K, &status)) return 0;
+  return moe::linear_i8_ws_bytes(T, N, K, !x_quantized);
+}
+
+int moe_linear_i8(const void* x, const float* x_scales, int T, int N, int K, const int8_t* codes,
+                  const float* scales, const float* bias, void* out, int out_dtype, void* ws,
+                  size_t ws_bytes, void* stream) {
+  const char* what = "moe_linear_i8";
+  int status;
+  if (const char* why = linear_i8_refusal(T, N, K, &status))
+    return fail(status, "%s: %s (T=%d N=%d K=%d)", what, why, T, N, K);
+  if (!known_dtype(out_dtype))
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown out_dtype %d", what, out_dtype);
+  if (T == 0) return ok();
+  if (!x || !codes || !scales || !out) return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(x, 16) || !aligned(x_scales, 4) || !aligned(codes, 16) || !aligned(scales, 16) ||
+      !aligned(bias, 16) || !aligned(out, 16))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  if (int rc = ws_check(what, moe::linear_i8_ws_bytes(T, N, K, !x_scales), ws, ws_bytes))
+    return rc;
+  return hip_status(moe::launch_linear_i8(x, x_scales, T, N, K, codes, scales, bias, out,
+                                          out_dtype == MOE_OUT_F32, ws, (hipStream_t)stream),
+                    what);
+}
+
+static const char* gated_refusal(int T, int d, int f, int* status) {
+  *status = MOE_ERR_INVALID_ARG;
+  if (T < 0 || d <= 0 || f <= 0) return "bad size";
+  *status = MOE_ERR_UNSUPPORTED;
+  if (d % 8 || f % 8) return "d and f must be multiples of 8";
+  if (d > 1 << 16 || f > 1 << 16) return "d or f above 65536";
+  if (T >= 1 << 23 || (long long)T * d >= (1LL << 34) || (long long)T * f >= (1LL << 33))
+    return "T not below 2^23, T*d below 2^34 or T*f below 2^33";
+  return nullptr;
+}
+
+size_t moe_gated_ffn_ws_bytes(int T, int d, int f) {
+  int status;
+  if (T == 0 || gated_refusal(T, d, f, &status)) return 0;
+  return moe::gated_ffn_ws_bytes(T, d, f);
+}
+
+int moe_gated_ffn(const void* x_bf16, const void* w_gate_up_bf16, const void* w_down_bf16, int T,
+                  int d, int f, void* out, int out_dtype, void* gate_up_bf16, void* ws,
+                  size_t ws_bytes, void* stream) {
+  const char* what = "moe_gated_ffn";
+  int status;
+  if (const char* why = gated_refusal(T, d, f, &status))
+    return fail(status, "%s: %s (T=%d d=%d f=%d)", what, why, T, d, f);
+  if (!known_dtype(out_dtype))
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown out_dtype %d", what, out_dtype);
+  if (T == 0) return ok();
+  if (!x_bf16 || !w_gate_up_bf16 || !w_down_bf16 || !out)
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(x_bf16, 16) || !aligned(w_gate_up_bf16, 16) || !aligned(w_down_bf16, 16) ||
+      !aligned(out, 16) || !aligned(gate_up_bf16, 16))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  if (int rc = ws_check(what, moe::gated_ffn_ws_bytes(T, d, f), ws, ws_bytes)) return rc;
+  return hip_status(
+      moe::launch_gated_ffn((const uint16_t*)x_bf16, (const uint16_t*)w_gate_up_bf16,
+                            (const uint16_t*)w_down_bf16, T, d, f, out, out_dtype == MOE_OUT_F32,
+                            (uint16_t*)gate_up_bf16, ws, (hipStream_t)stream),
+      what);
+}
+
+size_t moe_gated_ffn_bwd_ws_bytes(int T, int d, int f, int dout_dtype, int x_quantized,
+                                  int gate_up_kept) {
+  int status;
+  if (gated_refusal(T, d, f, &status)) return 0;
+  return moe::gated_ffn_bwd_ws_bytes(T, d, f, dout_dtype == MOE_OUT_F32, x_quantized != 0,
+                                     gate_up_kept != 0);
+}
+
+int moe_gated_ffn_bwd(const void* dout, int dout_dtype, const void* x, const float* x_scales,
+                      const void* gate_up_bf16, const void* w_gate_up_bf16,
+                      const void* w_down_bf16, int T, int d, int f, void* dx_bf16,
+                      void* dw_gate_up, void* dw_down, int dw_dtype, void* ws, size_t ws_bytes,
+                      void* stream) {
+  const char* what = "moe_gated_ffn_bwd";
+  int status;
+  if (const char* why = gated_refusal(T, d, f, &status))
+    return fail(status, "%s: %s (T=%d d=%d f=%d)", what, why, T, d, f);
+  if (!known_dtype(dout_dtype) || !known_dtype(dw_dtype))
+    return fail(MOE_ERR_INVALID_ARG, "%s: unknown dtype", what);
+  const bool weights = dw_gate_up || dw_down;
+  if (!weights && (T == 0 || !dx_bf16)) return ok();
+  if (T > 0 && (!dout || !x || !w_gate_up_bf16 || !w_down_bf16))
+    return fail(MOE_ERR_INVALID_ARG, "%s: null pointer", what);
+  if (!aligned(dout, 16) || !aligned(x, 16) || !aligned(x_scales, 4) ||
+      !aligned(gate_up_bf16, 16) || !aligned(w_gate_up_bf16, 16) || !aligned(w_down_bf16, 16) ||
+      !aligned(dx_bf16, 16) || !aligned(dw_gate_up, 16) || !aligned(dw_down, 16))
+    return fail(MOE_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+  const moe::GatedBwdArgs a{dout,
+                            dout_dtype == MOE_OUT_F32,
+                            x,
+                            x_scales,
+                            (const uint16_t*)gate_up_bf16,
+                            (const uint16_t*)w_gate_up_bf16,
+                            (const uint16_t*)w_down_bf16,
+                            T,
+                            d,
+                            f,
+                            (uint16_t*)dx_bf16,
+                            dw_gate_up,
+                            dw_down,
+                            dw_dtype == MOE_OUT_F32};
+  const size_t need = moe::gated_ffn_bwd_ws_bytes(T, d, f, a.do_f32, x_scales != nullptr,
+                                                  gate_up_bf16 != nullptr);
+  if (int rc = ws_check(what, need, ws, ws_bytes)) return rc;
+  return hip_status(moe::launch_gated_ffn_bwd(a, ws, (hipStream_t)stream), what);
 }

@@ -1,0 +1,202 @@
+// Gated feed-forward block with bf16 weights (a shared expert beside the routed
+// ones) and its gradient.  Wgu [2f][d]: gate rows, then up rows; Wd [d][f].
+//   g = x Wg^T, u = x Wu^T, h = silu(g) u, out = h Wd^T
+// forward: one product over both projections, whose tiles hold a gate and the
+// up feature beside it in one lane, so that activation and product are formed in
+// registers; h goes to memory once, as bf16 (as the experts' does), for the
+// second product.
+// gradient, for dout, with s = 1 / (1 + e^-g) and g, u kept as bf16 or computed
+// again:
+//   dh = dout Wd
+//   du = dh g s,  dg = dh u s (1 + g (1 - s)),  h = g s u       (its epilogue)
+//   dx = [dg du] Wgu,  dWgu = [dg du]^T x,  dWd = dout^T h
+// dg, du and h are rounded to bf16, the matrix cores' operand type; all sums are
+// fp32 in a fixed order.
+#include "mm_launch.hpp"
+
+namespace moe {
+namespace {
+using namespace mm;
+
+// h = silu(g) u, and the pre-activations where they are kept (either null: not
+// wanted).
+struct GatedStore {
+  uint16_t* h;
+  uint16_t* gate_up;
+  int f;
+  __device__ __forceinline__ void operator()(int m, int n, f32x4 g, f32x4 u) const {
+    if (h) {
+      f32x4 v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = silu_f32(g[r]) * u[r];
+      store4(h, 0, (size_t)m * f + n, v);
+    }
+    if (gate_up) {
+      store4(gate_up, 0, (size_t)m * (2 * f) + n, g);
+      store4(gate_up, 0, (size_t)m * (2 * f) + f + n, u);
+    }
+  }
+};
+
+struct Store {
+  void* out;
+  long long N;
+  int f32;
+  __device__ __forceinline__ void operator()(int m, int n, f32x4 v) const {
+    store4(out, f32, (size_t)m * N + n, v);
+  }
+};
+
+// dh -> dg, du and h.
+struct GatedBwdStore {
+  const uint16_t* gate_up;
+  uint16_t* dgu;
+  uint16_t* h;
+  int f;
+  __device__ __forceinline__ void operator()(int m, int n, f32x4 dh) const {
+    const size_t at = (size_t)m * (2 * f) + n;
+    const uint2 gb = *(const uint2*)(gate_up + at), ub = *(const uint2*)(gate_up + at + f);
+    const float g[4] = {bf16_bits_to_f32(gb.x & 0xFFFF), bf16_bits_to_f32(gb.x >> 16),
+                        bf16_bits_to_f32(gb.y & 0xFFFF), bf16_bits_to_f32(gb.y >> 16)};
+    const float u[4] = {bf16_bits_to_f32(ub.x & 0xFFFF), bf16_bits_to_f32(ub.x >> 16),
+                        bf16_bits_to_f32(ub.y & 0xFFFF), bf16_bits_to_f32(ub.y >> 16)};
+    f32x4 dg, du, hv;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[r])), a = g[r] * s;
+      du[r] = dh[r] * a;
+      dg[r] = dh[r] * u[r] * (s + a * (1.0f - s));
+      hv[r] = a * u[r];
+    }
+    store4(dgu, 0, at, dg);
+    store4(dgu, 0, at + f, du);
+    store4(h, 0, (size_t)m * f + n, hv);
+  }
+};
+
+// fp32 rows to bf16, eight values a thread.
+__global__ __launch_bounds__(256) void to_bf16_kernel(const float* __restrict__ x,
+                                                      long long chunks,
+                                                      uint16_t* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= chunks) return;
+  const f32x4 a = *(const f32x4*)(x + 8 * i), b = *(const f32x4*)(x + 8 * i + 4);
+  store4(out, 0, 8 * (size_t)i, a);
+  store4(out, 0, 8 * (size_t)i + 4, b);
+}
+
+size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
+int stages_of(int k) { return (int)up(2LL * k, kStageBytes); }
+
+Operand rows(const void* p, int stride, int n) {
+  return {(const char*)p, nullptr, 2LL * stride, n};
+}
+
+// The gate and up rows of Wgu, in pairs.
+Operand pairs(const uint16_t* w, int d, int f) {
+  return {(const char*)w, (const char*)(w + (size_t)f * d), 2LL * d, f};
+}
+
+}  // namespace
+
+size_t gated_ffn_ws_bytes(int T, int d, int f) {
+  return round_up(2 * (size_t)T * f) + std::max(partial_bytes(T, 2LL * f, stages_of(d), true),
+                                                partial_bytes(T, d, stages_of(f), true));
+}
+
+hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* w_gate_up, const uint16_t* w_down,
+                            int T, int d, int f, void* out, int out_f32, uint16_t* gate_up,
+                            void* ws, hipStream_t s) {
+  uint16_t* h = (uint16_t*)ws;
+  void* part = (char*)ws + round_up(2 * (size_t)T * f);
+  const hipError_t e = launch_product<Bf16, false, false, true>(
+      rows(x, d, T), pairs(w_gate_up, d, f), T, f, d, 2, GatedStore{h, gate_up, f}, part, s);
+  if (e != hipSuccess) return e;
+  return launch_product<Bf16, false, false, false>(rows(h, f, T), rows(w_down, f, d), T, d, f, 2,
+                                                   Store{out, d, out_f32}, part, s);
+}
+
+namespace {
+
+// Workspace of the gradient, in bytes from its start.
+struct BwdSpace {
+  size_t dgu, h, gate_up, x, dout, part, bytes;
+  BwdSpace(int T, int d, int f, int do_f32, int x_i8, int kept) {
+    size_t at = 0;
+    auto take = [&](bool wanted, size_t values) {
+      const size_t p = at;
+      if (wanted) at += round_up(2 * values);
+      return p;
+    };
+    dgu = take(true, (size_t)T * 2 * f);
+    h = take(true, (size_t)T * f);
+    gate_up = take(!kept, (size_t)T * 2 * f);
+    x = take(x_i8, (size_t)T * d);
+    dout = take(do_f32, (size_t)T * d);
+    part = at;
+    size_t n = kept ? 0 : partial_bytes(T, 2LL * f, stages_of(d), true);
+    n = std::max(n, partial_bytes(T, f, stages_of(d), true));
+    n = std::max(n, partial_bytes(T, d, stages_of(2 * f), true));
+    n = std::max(n, partial_bytes(2LL * f, d, stages_of(T), false));
+    n = std::max(n, partial_bytes(d, f, stages_of(T), false));
+    bytes = at + n;
+  }
+};
+
+}  // namespace
+
+size_t gated_ffn_bwd_ws_bytes(int T, int d, int f, int do_f32, int x_i8, int kept) {
+  return BwdSpace(T, d, f, do_f32, x_i8, kept).bytes;
+}
+
+hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) {
+  const int T = a.T, d = a.d, f = a.f;
+  const BwdSpace at(T, d, f, a.do_f32, a.x_scales != nullptr, a.gate_up != nullptr);
+  auto place = [&](size_t p) { return (uint16_t*)((char*)ws + p); };
+  uint16_t *dgu = place(at.dgu), *h = place(at.h);
+  void* part = place(at.part);
+  const uint16_t* x = (const uint16_t*)a.x;
+  const uint16_t* dout = (const uint16_t*)a.dout;
+  const uint16_t* gate_up = a.gate_up;
+  hipError_t e = hipSuccess;
+  if (T > 0) {
+    if (a.do_f32) {
+      const long long chunks = (long long)T * (d / 8);
+      hipLaunchKernelGGL(to_bf16_kernel, dim3((uint32_t)up(chunks, 256)), dim3(256), 0, s,
+                         (const float*)a.dout, chunks, place(at.dout));
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      dout = place(at.dout);
+    }
+    if (a.x_scales && (!gate_up || a.dw_gate_up)) {
+      e = launch_dequantize_i8((const int8_t*)a.x, a.x_scales, T, d, 0, place(at.x), 0, s);
+      if (e != hipSuccess) return e;
+      x = place(at.x);
+    }
+    if (!gate_up) {
+      e = launch_product<Bf16, false, false, true>(
+          rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d, 2,
+          GatedStore{nullptr, place(at.gate_up), f}, part, s);
+      if (e != hipSuccess) return e;
+      gate_up = place(at.gate_up);
+    }
+    e = launch_product<Bf16, false, true, false>(rows(dout, d, T), rows(a.w_down, f, f), T, f, d,
+                                                 2, GatedBwdStore{gate_up, dgu, h, f}, part, s);
+    if (e != hipSuccess) return e;
+    if (a.dx) {
+      e = launch_product<Bf16, false, true, false>(rows(dgu, 2 * f, T), rows(a.w_gate_up, d, d), T,
+                                                   d, 2 * f, 2, Store{a.dx, d, 0}, part, s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (a.dw_gate_up) {
+    e = launch_product<Bf16, true, true, false>(rows(dgu, 2 * f, 2 * f), rows(x, d, d), 2 * f, d, T,
+                                                2, Store{a.dw_gate_up, d, a.dw_f32}, part, s);
+    if (e != hipSuccess) return e;
+  }
+  if (a.dw_down)
+    e = launch_product<Bf16, true, true, false>(rows(dout, d, d), rows(h, f, f), d, f, T, 2,
+                                                Store{a.dw_down, f, a.dw_f32}, part, s);
+  return e;
+}
+
+}  // namespace moe

@@ -138,13 +138,15 @@ hipError_t launch_combine(const float* y, const int32_t* pair_pos,
                           const float* topk_w, int T, int k, int d, void* out,
                           int out_f32, hipStream_t s);
 
-// Norm in front of a block and its gradient (norm.hip).
-hipError_t launch_rmsnorm(const void* x, int x_f32, const float* gain, int T, int d, float eps,
-                          void* out, int out_f32, hipStream_t s);
+// Norm in front of a block and its gradient (norm.hip).  x_scales not null: x
+// is 8-bit codes with a scale for each 128 (the gradient's x_f32 is then dx's
+// and dres' type alone).
+hipError_t launch_rmsnorm(const void* x, int x_f32, const float* x_scales, const float* gain,
+                          int T, int d, float eps, void* out, int out_f32, hipStream_t s);
 size_t rmsnorm_bwd_ws_bytes(int T, int d);
 hipError_t launch_rmsnorm_bwd(const void* dout, int do_f32, const void* x, int x_f32,
-                              const float* gain, const void* dres, int T, int d, float eps,
-                              void* dx, float* dgain, void* ws, hipStream_t s);
+                              const float* x_scales, const float* gain, const void* dres, int T,
+                              int d, float eps, void* dx, float* dgain, void* ws, hipStream_t s);
 // Column sums S of n rows of partial sums: out1 = S f1, out2 = S f2 (norm.hip).
 hipError_t launch_colsum(const float* rows, int n, int d, float* out1, const float* f1,
                          float* out2, const float* f2, hipStream_t s);
@@ -194,6 +196,42 @@ const char* linear_w4_kernel(int T, int N, int K);  // the chosen kernel's name
 hipError_t launch_linear_w4(const uint16_t* x, const uint8_t* codes, const uint16_t* scales,
                             const float* bias, int T, int N, int K, void* out, int out_f32,
                             void* ws, hipStream_t s);
+
+// Rows in 8-bit integers (quant_i8.hip); by_row: one scale a row, otherwise one
+// for each 128 values.
+hipError_t launch_quantize_i8(const void* x, int x_f32, int T, int K, int by_row, int8_t* codes,
+                              float* scales, hipStream_t s);
+hipError_t launch_dequantize_i8(const int8_t* codes, const float* scales, int T, int K, int by_row,
+                                void* out, int out_f32, hipStream_t s);
+
+// Linear map in 8-bit integers (linear_i8.hip).  x_scales null: x is bf16 and
+// quantised by row into ws.
+size_t linear_i8_ws_bytes(int T, int N, int K, int x_bf16);
+hipError_t launch_linear_i8(const void* x, const float* x_scales, int T, int N, int K,
+                            const int8_t* codes, const float* scales, const float* bias, void* out,
+                            int out_f32, void* ws, hipStream_t s);
+
+// Gated feed-forward block and its gradient (gated_ffn.hip).
+size_t gated_ffn_ws_bytes(int T, int d, int f);
+hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* w_gate_up, const uint16_t* w_down,
+                            int T, int d, int f, void* out, int out_f32, uint16_t* gate_up,
+                            void* ws, hipStream_t s);
+struct GatedBwdArgs {
+  const void* dout;
+  int do_f32;
+  const void* x;          // bf16, or 8-bit codes with x_scales
+  const float* x_scales;  // null: x is bf16
+  const uint16_t* gate_up;  // kept pre-activations, or null
+  const uint16_t* w_gate_up;
+  const uint16_t* w_down;
+  int T, d, f;
+  uint16_t* dx;  // outputs, null where not wanted
+  void* dw_gate_up;
+  void* dw_down;
+  int dw_f32;
+};
+size_t gated_ffn_bwd_ws_bytes(int T, int d, int f, int do_f32, int x_i8, int kept);
+hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s);
 
 // Canonical -> streaming code layouts (retile.hip).
 hipError_t launch_retile_w4(const uint8_t* canon, long long R, int K, uint8_t* tiled,

@@ -24,8 +24,9 @@ using namespace row;
 // floats, 3 % of the bytes of 8192 bf16 rows.
 constexpr int kBwdBlocks = 512;
 
-template <bool kXF32, bool kOutF32, int NC, int kThreads>
+template <int kX, bool kOutF32, int NC, int kThreads>
 __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(const void* __restrict__ x,
+                                                           const float* __restrict__ x_scales,
                                                            const float* __restrict__ gain, int d,
                                                            float eps, void* __restrict__ out) {
   constexpr int kWaves = kThreads / kWave;
@@ -39,7 +40,9 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(const void* __restric
     const int c = threadIdx.x + kThreads * i;
     g[i] = 1.0f;
     if (c < nch) {
-      v[i] = load8<kXF32>(x, base + 8 * c);
+      RowChunk<kX> r;
+      r.load(x, x_scales, blockIdx.x, d, 8 * c);
+      v[i] = r.get();
       if (gain) g[i] = load8<true>(gain, 8 * c);
       s[0] += sum8(v[i], v[i]);
     }
@@ -53,10 +56,11 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_kernel(const void* __restric
   }
 }
 
-template <bool kDoF32, bool kXF32, int NC, int kThreads>
+template <bool kDoF32, int kX, bool kXF32, int NC, int kThreads>
 __global__ __launch_bounds__(kThreads) void rmsnorm_bwd_kernel(
-    const void* __restrict__ dout, const void* __restrict__ x, const float* __restrict__ gain,
-    const void* dres, int T, int d, float eps, void* dx, float* __restrict__ partial) {
+    const void* __restrict__ dout, const void* __restrict__ x, const float* __restrict__ x_scales,
+    const float* __restrict__ gain, const void* dres, int T, int d, float eps, void* dx,
+    float* __restrict__ partial) {
   constexpr int kWaves = kThreads / kWave;
   __shared__ float red[2][2 * kWaves];
   const int nch = d >> 3;
@@ -72,13 +76,14 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_bwd_kernel(
   }
   // the next row is asked for before this one's sums (past the last row: the
   // last again, for nothing)
-  Raw8<kXF32> rx[NC], rr[NC];
+  RowChunk<kX> rx[NC];
+  Raw8<kXF32> rr[NC];
   Raw8<kDoF32> ru[NC];
   auto ask = [&](int t) {
-    const size_t base = (size_t)min(t, T - 1) * d;
+    const size_t row = (size_t)min(t, T - 1), base = row * d;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      rx[i].load(x, base + at[i]);
+      rx[i].load(x, x_scales, row, d, at[i]);
       ru[i].load(dout, base + at[i]);
       if (dres) rr[i].load(dres, base + at[i]);
     }
@@ -159,14 +164,20 @@ hipError_t launch_colsum(const float* rows, int n, int d, float* out1, const flo
   return hipGetLastError();
 }
 
-hipError_t launch_rmsnorm(const void* x, int x_f32, const float* gain, int T, int d, float eps,
-                          void* out, int out_f32, hipStream_t s) {
+hipError_t launch_rmsnorm(const void* x, int x_f32, const float* x_scales, const float* gain,
+                          int T, int d, float eps, void* out, int out_f32, hipStream_t s) {
   with_shape(T, d, [&](auto th, auto nc) {
-    with_bools(x_f32, out_f32, [&](auto xf, auto of) {
-      constexpr int TH = decltype(th)::value, NC = decltype(nc)::value;
-      hipLaunchKernelGGL((rmsnorm_kernel<decltype(xf)::value, decltype(of)::value, NC, TH>),
-                         dim3(T), dim3(TH), 0, s, x, gain, d, eps, out);
-    });
+    constexpr int TH = decltype(th)::value, NC = decltype(nc)::value;
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(T), dim3(TH), 0, s, x, x_scales, gain, d, eps, out);
+    };
+    if (x_scales)
+      out_f32 ? go(rmsnorm_kernel<kRowI8, true, NC, TH>) : go(rmsnorm_kernel<kRowI8, false, NC, TH>);
+    else
+      with_bools(x_f32, out_f32, [&](auto xf, auto of) {
+        constexpr int X = decltype(xf)::value ? kRowF32 : kRowBf16;
+        go(rmsnorm_kernel<X, decltype(of)::value, NC, TH>);
+      });
   });
   return hipGetLastError();
 }
@@ -176,7 +187,7 @@ size_t rmsnorm_bwd_ws_bytes(int T, int d) {
 }
 
 hipError_t launch_rmsnorm_bwd(const void* dout, int do_f32, const void* x, int x_f32,
-                              const float* gain, const void* dres, int T, int d, float eps,
+                              const float* x_scales, const float* gain, const void* dres, int T, int d, float eps,
                               void* dx, float* dgain, void* ws, hipStream_t s) {
   const int nb = T < kBwdBlocks ? T : kBwdBlocks;
   float* partial = dgain ? (float*)ws : nullptr;
@@ -184,8 +195,12 @@ hipError_t launch_rmsnorm_bwd(const void* dout, int do_f32, const void* x, int x
     with_shape(kWideRows, d, [&](auto th, auto nc) {
       with_bools(do_f32, x_f32, [&](auto df, auto xf) {
         constexpr int TH = decltype(th)::value, NC = decltype(nc)::value;
-        hipLaunchKernelGGL((rmsnorm_bwd_kernel<decltype(df)::value, decltype(xf)::value, NC, TH>),
-                           dim3(nb), dim3(TH), 0, s, dout, x, gain, dres, T, d, eps, dx, partial);
+        constexpr bool DF = decltype(df)::value, XF = decltype(xf)::value;
+        constexpr int X = XF ? kRowF32 : kRowBf16;
+        auto kernel = x_scales ? rmsnorm_bwd_kernel<DF, kRowI8, XF, NC, TH>
+                               : rmsnorm_bwd_kernel<DF, X, XF, NC, TH>;
+        hipLaunchKernelGGL(kernel, dim3(nb), dim3(TH), 0, s, dout, x, x_scales, gain, dres, T, d,
+                           eps, dx, partial);
       });
     });
   }

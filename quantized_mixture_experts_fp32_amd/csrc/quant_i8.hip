@@ -1,0 +1,172 @@
+// Rows in 8-bit integers: activation checkpoints (a scale for each 128 values
+// of a row) and the operands of the 8-bit linear map (one scale a row).
+//   m = max |x| over the group, scale = m / 127, q = rne(x * (127 / m)),
+//   restored as q * scale
+// (fp32 divisions and one fp32 product, correctly rounded, so codes and scales
+// are the same everywhere).  |x - q scale| <= scale / 2 and the roundings of
+// three fp32 steps.  A group below 2^-119 is stored as zeros (127 / m stays
+// finite), one with an infinity or NaN restores as NaN.
+//
+// HBM-bound: x is read once and the codes are written once.
+#include "launch.hpp"
+#include "rowops.hpp"
+
+namespace moe {
+namespace {
+using namespace row;
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr float kTiny = 0x1p-119f;
+
+// Largest magnitude of eight values as bits, which order as the values do, an
+// infinity above all numbers and NaN above it.
+__device__ __forceinline__ uint32_t top8(const f32x8 v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+  return m;
+}
+
+struct Scaling {
+  float scale, inv;  // inv 0: every code is 0
+  __device__ __forceinline__ explicit Scaling(uint32_t top) {
+    const float m = __uint_as_float(top);
+    const bool bad = top >= kInfBits, zero = m < kTiny;
+    scale = bad ? __uint_as_float(0x7FC00000u) : zero ? 0.0f : m / 127.0f;
+    inv = bad || zero ? 0.0f : 127.0f / m;
+  }
+};
+
+__device__ __forceinline__ u32x2 codes8(const f32x8 v, float inv) {
+  u32x2 r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // (a product with inv 0 may be NaN; it is not used)
+      const int c = inv == 0.0f ? 0 : (int)__builtin_rintf(v[4 * h + q] * inv);
+      w |= (uint32_t)(c & 255) << (8 * q);
+    }
+    r[h] = w;
+  }
+  return r;
+}
+
+// Sixteen lanes a group of 128, eight values each; the last group of a row may
+// be shorter.
+template <bool kF32>
+__global__ __launch_bounds__(256) void quantize_i8_groups(const void* __restrict__ x, int K, int G,
+                                                          long long groups,
+                                                          int8_t* __restrict__ codes,
+                                                          float* __restrict__ scales) {
+  const long long i = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (i >= groups) return;
+  const int l = threadIdx.x & 15;
+  const uint32_t row = (uint32_t)i / (uint32_t)G, g = (uint32_t)i - row * (uint32_t)G;
+  const int at = (int)g * 128 + 8 * l;
+  const size_t p = (size_t)row * K + at;
+  f32x8 v = 0.0f;
+  if (at < K) v = load8<kF32>(x, p);
+  uint32_t m = top8(v);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 16));
+  const Scaling s(m);
+  if (at < K) *(u32x2*)(codes + p) = codes8(v, s.inv);
+  if (l == 0) scales[i] = s.scale;
+}
+
+// A block a row, which it holds in registers (kNC chunks of eight a thread), or
+// reads twice (kNC = 0).
+template <bool kF32, int kNC>
+__global__ __launch_bounds__(256) void quantize_i8_rows(const void* __restrict__ x, int K,
+                                                        int8_t* __restrict__ codes,
+                                                        float* __restrict__ scales) {
+  __shared__ uint32_t red[4];
+  const size_t base = (size_t)blockIdx.x * K;
+  const int nch = K >> 3, tid = threadIdx.x;
+  f32x8 v[kNC > 0 ? kNC : 1];
+  uint32_t m = 0;
+  if (kNC > 0) {
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) {
+      const int c = tid + 256 * i;
+      v[i] = 0.0f;
+      if (c < nch) v[i] = load8<kF32>(x, base + 8 * c);
+    }
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) m = max(m, top8(v[i]));
+  } else {
+    for (int c = tid; c < nch; c += 256) m = max(m, top8(load8<kF32>(x, base + 8 * c)));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
+  if ((tid & 63) == 0) red[tid >> 6] = m;
+  __syncthreads();
+  const Scaling s(max(max(red[0], red[1]), max(red[2], red[3])));
+  if (kNC > 0) {
+#pragma unroll
+    for (int i = 0; i < kNC; ++i) {
+      const int c = tid + 256 * i;
+      if (c < nch) *(u32x2*)(codes + base + 8 * c) = codes8(v[i], s.inv);
+    }
+  } else {
+    for (int c = tid; c < nch; c += 256)
+      *(u32x2*)(codes + base + 8 * c) = codes8(load8<kF32>(x, base + 8 * c), s.inv);
+  }
+  if (tid == 0) scales[blockIdx.x] = s.scale;
+}
+
+// Codes back to values, eight a thread; G groups a row (128 each, or one).
+template <bool kF32>
+__global__ __launch_bounds__(256) void dequantize_i8(const int8_t* __restrict__ codes,
+                                                     const float* __restrict__ scales, int nch,
+                                                     int G, long long chunks,
+                                                     void* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= chunks) return;
+  const uint32_t row = (uint32_t)i / (uint32_t)nch, c = (uint32_t)i - row * (uint32_t)nch;
+  const float s = scales[(size_t)row * G + (G == 1 ? 0 : c >> 4)];
+  store8<kF32>(out, 8 * (size_t)i, i8x8_to_f32(*(const u32x2*)(codes + 8 * (size_t)i)) * s);
+}
+
+}  // namespace
+
+hipError_t launch_quantize_i8(const void* x, int x_f32, int T, int K, int by_row, int8_t* codes,
+                              float* scales, hipStream_t s) {
+  if (!by_row) {
+    const int G = (K + 127) / 128;
+    const long long groups = (long long)T * G;
+    auto k = x_f32 ? quantize_i8_groups<true> : quantize_i8_groups<false>;
+    hipLaunchKernelGGL(k, dim3((uint32_t)((groups + 15) / 16)), dim3(256), 0, s, x, K, G, groups,
+                       codes, scales);
+    return hipGetLastError();
+  }
+  auto go = [&](auto nc) {
+    constexpr int NC = decltype(nc)::value;
+    auto k = x_f32 ? quantize_i8_rows<true, NC> : quantize_i8_rows<false, NC>;
+    hipLaunchKernelGGL(k, dim3(T), dim3(256), 0, s, x, K, codes, scales);
+  };
+  using std::integral_constant;
+  if (K <= 2048)
+    go(integral_constant<int, 1>{});
+  else if (K <= 4096)
+    go(integral_constant<int, 2>{});
+  else if (K <= 8192)
+    go(integral_constant<int, 4>{});
+  else
+    go(integral_constant<int, 0>{});
+  return hipGetLastError();
+}
+
+hipError_t launch_dequantize_i8(const int8_t* codes, const float* scales, int T, int K, int by_row,
+                                void* out, int out_f32, hipStream_t s) {
+  const int nch = K >> 3, G = by_row ? 1 : (K + 127) / 128;
+  const long long chunks = (long long)T * nch;
+  auto k = out_f32 ? dequantize_i8<true> : dequantize_i8<false>;
+  hipLaunchKernelGGL(k, dim3((uint32_t)((chunks + 255) / 256)), dim3(256), 0, s, codes, scales,
+                     nch, G, chunks, out);
+  return hipGetLastError();
+}
+
+}  // namespace moe

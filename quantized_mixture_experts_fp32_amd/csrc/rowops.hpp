@@ -65,6 +65,38 @@ __device__ __forceinline__ void store8(void* p, size_t i, const f32x8 v) {
   }
 }
 
+// Eight 8-bit codes as fp32.
+__device__ __forceinline__ f32x8 i8x8_to_f32(u32x2 w) {
+  f32x8 v;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = (float)((int)(w[q >> 2] << (24 - 8 * (q & 3))) >> 24);
+  return v;
+}
+
+// What a row is stored as: its values, or 8-bit codes with a scale for each 128
+// (a chunk's codes and its group's scale; restored as quant_i8.hip says).
+enum RowKind { kRowBf16, kRowF32, kRowI8 };
+
+template <int kKind>
+struct RowChunk {
+  Raw8<kKind == kRowF32> r;
+  __device__ __forceinline__ void load(const void* p, const float*, size_t row, int d, int at) {
+    r.load(p, row * d + at);
+  }
+  __device__ __forceinline__ f32x8 get() const { return r.get(); }
+};
+template <>
+struct RowChunk<kRowI8> {
+  u32x2 q;
+  float s;
+  __device__ __forceinline__ void load(const void* p, const float* scales, size_t row, int d,
+                                       int at) {
+    q = *(const u32x2*)((const int8_t*)p + row * d + at);
+    s = scales[row * ((d + 127) >> 7) + (at >> 7)];
+  }
+  __device__ __forceinline__ f32x8 get() const { return i8x8_to_f32(q) * s; }
+};
+
 __device__ __forceinline__ float sum8(const f32x8 a, const f32x8 b) {
   float s = a[0] * b[0];
 #pragma unroll

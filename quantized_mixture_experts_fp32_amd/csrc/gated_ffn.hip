@@ -100,20 +100,18 @@ Operand pairs(const uint16_t* w, int d, int f) {
 }  // namespace
 
 size_t gated_ffn_ws_bytes(int T, int d, int f) {
-  return round_up(2 * (size_t)T * f) + std::max(partial_bytes(T, 2LL * f, stages_of(d), true),
-                                                partial_bytes(T, d, stages_of(f), true));
+  return round_up(2 * (size_t)T * f);
 }
 
 hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* w_gate_up, const uint16_t* w_down,
                             int T, int d, int f, void* out, int out_f32, uint16_t* gate_up,
                             void* ws, hipStream_t s) {
   uint16_t* h = (uint16_t*)ws;
-  void* part = (char*)ws + round_up(2 * (size_t)T * f);
-  const hipError_t e = launch_product<Bf16, false, false, true>(
-      rows(x, d, T), pairs(w_gate_up, d, f), T, f, d, 2, GatedStore{h, gate_up, f}, part, s);
+  const hipError_t e = launch_product<Bf16, kInner, true>(
+      rows(x, d, T), pairs(w_gate_up, d, f), T, f, d, 2, GatedStore{h, gate_up, f}, nullptr, s);
   if (e != hipSuccess) return e;
-  return launch_product<Bf16, false, false, false>(rows(h, f, T), rows(w_down, f, d), T, d, f, 2,
-                                                   Store{out, d, out_f32}, part, s);
+  return launch_product<Bf16, kInner, false>(rows(h, f, T), rows(w_down, f, d), T, d, f, 2,
+                                             Store{out, d, out_f32}, nullptr, s);
 }
 
 namespace {
@@ -134,12 +132,8 @@ struct BwdSpace {
     x = take(x_i8, (size_t)T * d);
     dout = take(do_f32, (size_t)T * d);
     part = at;
-    size_t n = kept ? 0 : partial_bytes(T, 2LL * f, stages_of(d), true);
-    n = std::max(n, partial_bytes(T, f, stages_of(d), true));
-    n = std::max(n, partial_bytes(T, d, stages_of(2 * f), true));
-    n = std::max(n, partial_bytes(2LL * f, d, stages_of(T), false));
-    n = std::max(n, partial_bytes(d, f, stages_of(T), false));
-    bytes = at + n;
+    bytes = at + std::max(partial_bytes(2LL * f, d, stages_of(T)),
+                          partial_bytes(d, f, stages_of(T)));
   }
 };
 
@@ -173,28 +167,28 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
       x = place(at.x);
     }
     if (!gate_up) {
-      e = launch_product<Bf16, false, false, true>(
+      e = launch_product<Bf16, kInner, true>(
           rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d, 2,
           GatedStore{nullptr, place(at.gate_up), f}, part, s);
       if (e != hipSuccess) return e;
       gate_up = place(at.gate_up);
     }
-    e = launch_product<Bf16, false, true, false>(rows(dout, d, T), rows(a.w_down, f, f), T, f, d,
+    e = launch_product<Bf16, kOuterB, false>(rows(dout, d, T), rows(a.w_down, f, f), T, f, d,
                                                  2, GatedBwdStore{gate_up, dgu, h, f}, part, s);
     if (e != hipSuccess) return e;
     if (a.dx) {
-      e = launch_product<Bf16, false, true, false>(rows(dgu, 2 * f, T), rows(a.w_gate_up, d, d), T,
+      e = launch_product<Bf16, kOuterB, false>(rows(dgu, 2 * f, T), rows(a.w_gate_up, d, d), T,
                                                    d, 2 * f, 2, Store{a.dx, d, 0}, part, s);
       if (e != hipSuccess) return e;
     }
   }
   if (a.dw_gate_up) {
-    e = launch_product<Bf16, true, true, false>(rows(dgu, 2 * f, 2 * f), rows(x, d, d), 2 * f, d, T,
+    e = launch_product<Bf16, kOuterBoth, false>(rows(dgu, 2 * f, 2 * f), rows(x, d, d), 2 * f, d, T,
                                                 2, Store{a.dw_gate_up, d, a.dw_f32}, part, s);
     if (e != hipSuccess) return e;
   }
   if (a.dw_down)
-    e = launch_product<Bf16, true, true, false>(rows(dout, d, d), rows(h, f, f), d, f, T, 2,
+    e = launch_product<Bf16, kOuterBoth, false>(rows(dout, d, d), rows(h, f, f), d, f, T, 2,
                                                 Store{a.dw_down, f, a.dw_f32}, part, s);
   return e;
 }

@@ -33,26 +33,28 @@ size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
 }  // namespace
 
 size_t linear_i8_ws_bytes(int T, int N, int K, int x_bf16) {
-  size_t n = partial_bytes(T, N, (int)up(K, kStageBytes), true);
-  if (x_bf16) n = round_up(n) + round_up((size_t)T * K) + round_up(4 * (size_t)T);
-  return n;
+  if (!x_bf16 || (T <= kQuantRows && direct_applies(T, N, K, false))) return 0;
+  return round_up((size_t)T * K) + round_up(4 * (size_t)T);
 }
 
 hipError_t launch_linear_i8(const void* x, const float* x_scales, int T, int N, int K,
                             const int8_t* codes, const float* scales, const float* bias, void* out,
                             int out_f32, void* ws, hipStream_t s) {
+  if (!x_scales && T <= kQuantRows && direct_applies(T, N, K, false))
+    return launch_direct<I8, false, true>(
+        {(const char*)x, (const char*)codes, 2LL * K, K, T, N, K, 0},
+        ScaleStore{nullptr, scales, bias, out, N, out_f32}, s);
   if (!x_scales) {
     int8_t* q = (int8_t*)ws;
     float* sx = (float*)((char*)ws + round_up((size_t)T * K));
-    ws = (char*)sx + round_up(4 * (size_t)T);
     const hipError_t e = launch_quantize_i8(x, 0, T, K, 1, q, sx, s);
     if (e != hipSuccess) return e;
     x = q;
     x_scales = sx;
   }
   const Operand a = {(const char*)x, nullptr, K, T}, b = {(const char*)codes, nullptr, K, N};
-  return launch_product<I8, false, false, false>(
-      a, b, T, N, K, 1, ScaleStore{x_scales, scales, bias, out, N, out_f32}, ws, s);
+  return launch_product<I8, kInner, false>(
+      a, b, T, N, K, 1, ScaleStore{x_scales, scales, bias, out, N, out_f32}, nullptr, s);
 }
 
 }  // namespace moe

@@ -18,6 +18,8 @@
 //     k & 3 | (k >> 1) & 4; fragments come through the LDS transpose read, which
 //     turns four rows of 16 values into four values for each of 16 lanes.
 #pragma once
+#include <type_traits>
+
 #include "kcommon.hpp"
 
 namespace moe {
@@ -39,9 +41,11 @@ struct Operand {
   int rows;            // rows of the product (m or n), per matrix
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const char* p, long long bytes) {
-  const long long n = bytes < 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes;
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)n, 0x00020000);
+typedef __attribute__((address_space(3))) void* Lds;
+
+// Offsets are below 2^31 where they are in range.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const char* p) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, 0x7FFFFFFF, 0x00020000);
 }
 
 template <int vm>  // all but vm of this wave's vector loads are done, its LDS reads too
@@ -51,75 +55,75 @@ __device__ __forceinline__ void wait_stage() {
 
 // Loader of one operand's stages.  kRows: rows (K-inner) or columns (K-outer)
 // of the tile; kPair: rows of two matrices, interleaved by 16.
-template <bool kOuter, bool kPair, int kRows, int kWaves>
+// kGroups: the stages are dealt to so many loaders in turn.
+template <bool kOuter, bool kPair, int kRows, int kWaves, int kGroups>
 struct Loader {
   static constexpr int kLoads = kRows / 8 / kWaves;  // a wave's loads a stage
   static_assert(kRows % (8 * kWaves) == 0, "whole loads a wave");
-  uint32_t off[kLoads];
-  const char* base;
-  const char* base2;
-  long long left, left2, step;  // bytes to the end of the matrix; bytes a stage
-  int kleft;                    // bytes of k to the end of a row (K-inner)
-  int w;
+  uint32_t off[kLoads];    // bytes from the stage's base
+  const char* base;        // of the next stage
+  const char* base2;       // of the second matrix (pair form)
+  long long step;          // bytes from one of its stages to the next
+  int full;                // whole stages of k from the next one on
+  int rest;                // bytes (K-inner) or rows (K-outer) of k after them
+  int w, lane;
 
-  // tile: first row (K-inner, of each matrix) or column (K-outer)
-  __device__ __forceinline__ void init(const Operand& o, int row0, int kbytes, int stage0,
-                                       int stages_k, int wave, int lane) {
-    w = wave;
-    if (kOuter) {
-      constexpr int kChunks = kRows / 8;  // 16-byte chunks a row
-      const long long at = (long long)stage0 * kStageK * o.stride + 2LL * row0;
-      base = o.p + at;
-      left = (long long)stages_k * o.stride - at;  // stages_k: rows of k
-      step = kStageK * o.stride;
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int i = (wave * kLoads + j) * 64 + lane;
-        const int k = i / kChunks, pos = i % kChunks;
-        const int g = (pos >> 1) ^ (((k & 3) | ((k >> 1) & 4)) & (kChunks / 2 - 1));
-        off[j] = (uint32_t)(k * o.stride) + 32 * g + 16 * (pos & 1);
-      }
-    } else {
-      const long long at = (long long)row0 * o.stride;
-      const long long k0 = (long long)stage0 * kStageBytes;
-      base = o.p + at + k0;
-      left = (long long)o.rows * o.stride - at - k0;
-      if (kPair) {
-        base2 = o.p2 + at + k0;
-        left2 = left;
-      }
-      step = kStageBytes;
-      kleft = kbytes - (int)k0;
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int r = (wave * kLoads + j) * 8 + (lane >> 3);
-        const int row = kPair ? (r >> 5) * 16 + (r & 15) : r;
-        off[j] = (uint32_t)(row * o.stride) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-      }
-    }
+  // load j's row (K-inner) or row of k (K-outer), and its chunk of 16 bytes there
+  __device__ __forceinline__ int row_of(int j) const {
+    return kOuter ? ((w * kLoads + j) * 64 + lane) / (kRows / 8) : (w * kLoads + j) * 8 + (lane >> 3);
+  }
+  __device__ __forceinline__ int chunk_of(int j) const {
+    const int r = row_of(j);
+    if (!kOuter) return (lane & 7) ^ ((r >> 1) & 7);
+    const int pos = ((w * kLoads + j) * 64 + lane) % (kRows / 8);
+    const int f = ((r & 3) | ((r >> 1) & 4)) & (kRows / 16 - 1);
+    return 2 * ((pos >> 1) ^ f) + (pos & 1);
   }
 
-  // asks for the next stage into lds (the tile's first byte)
-  __device__ __forceinline__ void load(char* lds, int lane) {
-    const __amdgpu_buffer_rsrc_t r0 = rsrc_of(base, left);
-    __amdgpu_buffer_rsrc_t r1 = r0;
-    if (kPair) r1 = rsrc_of(base2, left);
+  // row0: the tile's first row (K-inner, of each matrix) or column (K-outer);
+  // k: bytes (K-inner) or rows (K-outer) of k in all
+  __device__ __forceinline__ void init(const Operand& o, int row0, int k, int stage0, int wave,
+                                       int ln) {
+    constexpr int kStage = kOuter ? kStageK : kStageBytes;
+    w = wave;
+    lane = ln;
+    step = kOuter ? kStageK * o.stride : kStageBytes;
+    const long long at = (kOuter ? 2LL * row0 : row0 * o.stride) + stage0 * step;
+    base = o.p + at;
+    if (kPair) base2 = o.p2 + at;
+    step *= kGroups;
+    full = k / kStage - stage0;
+    rest = k % kStage;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const int i = w * kLoads + j;
-      uint32_t o = off[j];
-      if (!kOuter && kleft < kStageBytes) {
-        const int r = i * 8 + (lane >> 3);
-        if (16 * ((lane & 7) ^ ((r >> 1) & 7)) >= kleft) o = kOutOfRange;
-      }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          kPair && ((i >> 1) & 1) ? r1 : r0, (__attribute__((address_space(3))) void*)(lds + i * 1024),
-          16, (int)o, 0, 0, 0);
+      const int r = row_of(j), c = chunk_of(j);
+      const int row = kPair ? (r >> 5) * 16 + (r & 15) : r;
+      off[j] = (uint32_t)(row * o.stride) + 16 * c;
+      if (row0 + (kOuter ? 8 * c : row) >= o.rows) off[j] = kOutOfRange;
     }
+    if (full <= 0) last();
+  }
+
+  // the stage that k ends in: what is past its end is out of range, and in the
+  // stages after it everything
+  __device__ __forceinline__ void last() {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      if (full < 0 || (kOuter ? row_of(j) : 16 * chunk_of(j)) >= rest) off[j] = kOutOfRange;
+  }
+
+  // load j of the next stage into lds (the tile's first byte)
+  __device__ __forceinline__ void load(int j, char* lds) const {
+    const int i = w * kLoads + j;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc_of(kPair && ((i >> 1) & 1) ? base2 : base), (Lds)(lds + i * 1024), 16, (int)off[j], 0,
+        0, 0);
+  }
+  __device__ __forceinline__ void next() {
     base += step;
-    left -= step;
     if (kPair) base2 += step;
-    kleft -= kStageBytes;
+    full -= kGroups;
+    if (full <= 0) last();
   }
 };
 
@@ -184,12 +188,14 @@ __device__ __forceinline__ void store4(void* p, int f32, size_t i, f32x4 v) {
   }
 }
 
-// Tile and wave counts of a configuration.
-template <int bm, int bn, int wm, int wn, int stages>
+// A configuration: tile, waves along m and n, stages in the ring, and groups of
+// waves that share the tile's k (each with a ring of its own, joined in LDS).
+template <int bm, int bn, int wm, int wn, int stages, int groups = 1>
 struct Shape {
-  static constexpr int BM = bm, BN = bn, WM = wm, WN = wn, S = stages;
-  static constexpr int kWaves = wm * wn, kThreads = 64 * kWaves;
-  static constexpr int kLds = (bm + bn) * kStageBytes * stages;
+  static constexpr int BM = bm, BN = bn, WM = wm, WN = wn, S = stages, G = groups;
+  static constexpr int kWaves = wm * wn, kThreads = 64 * kWaves * groups;  // waves: of a group
+  static constexpr int kRing = (bm + bn) * kStageBytes * stages;
+  static constexpr int kLds = groups * (kRing + 256 * kWaves);  // and a place for touched lines
 };
 
 struct Problem {
@@ -198,7 +204,7 @@ struct Problem {
   int kbytes;     // bytes of k in a row (K-inner)
   int krows;      // values of k: rows of a K-outer operand
   int stages;     // stages of k in all
-  int per_split;  // stages of k a split
+  int per_group;  // stages of k a group of waves
   int nm, nn;     // tiles
 };
 
@@ -218,24 +224,29 @@ __device__ __forceinline__ void tile_of(int id, int nm, int nn, int& tm, int& tn
 // Epi: operator()(m, n, Acc) for four consecutive n, or in the pair form
 // operator()(m, n, Acc first, Acc second).
 template <typename Mma, typename Sh, bool kAOuter, bool kBOuter, bool kPair, typename Epi>
-__global__ __launch_bounds__(Sh::kThreads, Sh::kWaves == 8 ? 2 : 1) void product_kernel(
+__global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kernel(
     const Problem p, const Epi epi) {
   extern __shared__ __align__(1024) char lds[];
   constexpr int TM = Sh::BM / Sh::WM, TN = Sh::BN / Sh::WN, MI = TM / 16, NI = TN / 16;
   constexpr int kA = Sh::BM * kStageBytes, kStage = kA + Sh::BN * kStageBytes;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = id / Sh::kWaves, wave = id % Sh::kWaves;
   const int wm = wave / Sh::WN, wn = wave % Sh::WN;
+  char* const ring = lds + group * Sh::kRing;
   int tm, tn;
   tile_of(blockIdx.x, p.nm, p.nn, tm, tn);
   const int m0 = tm * Sh::BM, n0 = tn * Sh::BN;
-  const int stage0 = blockIdx.y * p.per_split;
-  const int count = min(p.per_split, p.stages - stage0);
+  // The groups take the block's stages in turn, so that together they read long
+  // pieces of a row (the groups' ranges side by side in k: .. of HBM's rate);
+  // past the end of k stages are zeros.
+  const int block0 = blockIdx.y * Sh::G * p.per_group, stage0 = block0 + group;
+  const int count = min(p.per_group, (p.stages - block0 + Sh::G - 1) / Sh::G);
 
-  Loader<kAOuter, false, Sh::BM, Sh::kWaves> la;
-  Loader<kBOuter, kPair, Sh::BN, Sh::kWaves> lb;
-  la.init(p.a, m0, p.kbytes, stage0, p.krows, wave, lane);
-  lb.init(p.b, kPair ? n0 / 2 : n0, p.kbytes, stage0, p.krows, wave, lane);
+  Loader<kAOuter, false, Sh::BM, Sh::kWaves, Sh::G> la;
+  Loader<kBOuter, kPair, Sh::BN, Sh::kWaves, Sh::G> lb;
+  la.init(p.a, m0, kAOuter ? p.krows : p.kbytes, stage0, wave, lane);
+  lb.init(p.b, kPair ? n0 / 2 : n0, kBOuter ? p.krows : p.kbytes, stage0, wave, lane);
   Reader<kAOuter, Sh::BM, MI> ra;
   Reader<kBOuter, Sh::BN, NI> rb;
   ra.init(wm * TM, lane);
@@ -247,39 +258,109 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kWaves == 8 ? 2 : 1) void product
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = typename Mma::Acc{0, 0, 0, 0};
 
-  constexpr int kLoads = decltype(la)::kLoads + decltype(lb)::kLoads;
+  // Lines that this lane touches ahead of their loads, so that they are in L2
+  // then.  The tiles that run on an XCD at a time share rows of A four at a time
+  // and columns of B eight at a time (tile_of), so a tile touches its share of
+  // each; half the waves see to A, half to B.  What comes back goes to a spare
+  // place in LDS.
+  // Two stages a ring leave a stage's loads too little time for HBM; with more,
+  // and in the largest tiles of inner operands, touches cost more than they give
+  // (1024 x 4096 x 4096 in tiles of 128 x 128: 57 -> 42 us; 4096 x 4096 x 4096,
+  // outer operands, tiles of 256 x 256: 138 -> 115 us, inner 106 -> 110 us).
+  constexpr bool kTouch = Sh::S == 2 && (kAOuter || kBOuter || Sh::kWaves == 4);
+  constexpr int kHalfWaves = Sh::kWaves / 2;
+  const bool for_a = wave < kHalfWaves, outer = for_a ? kAOuter : kBOuter;
+  const int parts = for_a ? (p.nn >= 4 ? 4 : p.nn >= 2 ? 2 : 1)
+                          : (p.nm >= 8 ? 8 : p.nm >= 4 ? 4 : p.nm >= 2 ? 2 : 1);
+  const Operand& to = for_a ? p.a : p.b;
+  const bool second = kPair && !for_a && (wave & 1);  // pair form: its waves take turns
+  const int mine = (for_a ? Sh::BM : Sh::BN) / parts / kHalfWaves;
+  const int line = ((for_a ? tn : tm) & (parts - 1)) * (mine * kHalfWaves) +
+                   (wave % kHalfWaves) * mine + lane;
+  const int first = for_a ? m0 : kPair ? n0 / 2 : n0;
+  const int trow = outer ? line / ((for_a ? Sh::BM : Sh::BN) / 64)
+                         : kPair && !for_a ? line / 2 : line;
+  const int tcol = outer ? 64 * (line % ((for_a ? Sh::BM : Sh::BN) / 64)) : 0;
+  const long long tstep = for_a ? la.step : lb.step;
+  uint32_t toff = (uint32_t)(trow * to.stride) + 2 * tcol;
+  if (lane >= mine || first + (outer ? tcol : trow) >= to.rows) toff = kOutOfRange;
+  // stages that can be touched whole; past them the lines are out of range
+  int tleft = (outer ? p.krows / kStageK : p.kbytes / kStageBytes) - stage0 - Sh::S * Sh::G;
+  const char* tbase = (second ? to.p2 : to.p) + (outer ? 2LL * first : first * to.stride) +
+                      (stage0 + Sh::S * Sh::G) * (tstep / Sh::G);
+  auto touch = [&]() {
+    if (!kTouch) return;
+    if (tleft <= 0) toff = kOutOfRange;
+    tleft -= Sh::G;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_of(tbase), (Lds)(lds + Sh::G * Sh::kRing + 256 * id),
+                                             4, (int)toff, 0, 0, 0);
+    tbase += tstep;
+  };
+  constexpr int kLA = decltype(la)::kLoads, kLoads = kLA + decltype(lb)::kLoads;
   int put = 0, get = 0;
-  auto ask = [&]() {  // past the last stage the loads are out of range
-    char* s = lds + put * kStage;
-    la.load(s, lane);
-    lb.load(s + kA, lane);
+  auto ask = [&](int j) {  // past the last stage the loads are out of range
+    char* s = ring + put * kStage;
+    if (j < kLA)
+      la.load(j, s);
+    else
+      lb.load(j - kLA, s + kA);
+  };
+  auto asked = [&]() {
+    la.next();
+    lb.next();
     put = put + 1 == Sh::S ? 0 : put + 1;
   };
+  struct Frags {
+    u32x4 a[MI], b[NI];
+  } f0, f1;
+  auto read = [&](Frags& f, int i, int ks) {
+    const char* s = ring + get * kStage;
+    if (i < NI)
+      f.b[i] = rb.get(s + kA, i, ks);
+    else
+      f.a[i - NI] = ra.get(s, i - NI, ks);
+  };
+  // The products of one k step; between its rows the fragments of the next step
+  // are asked for (in its first rows) and, `loads`, the next stage's loads: all
+  // at once they would hold the wave up while the memory pipe takes them in.
+  constexpr int kReads = MI + NI, kHalf = kAOuter && kBOuter ? (MI + 3) / 4 : (MI + 1) / 2;
+  auto multiply = [&](const Frags& f, Frags& next, int ks, auto loads) {
 #pragma unroll
-  for (int s = 0; s < Sh::S - 1; ++s) ask();
+    for (int i = 0; i < MI; ++i) {
+      if (i < kHalf)
+#pragma unroll
+        for (int r = i * kReads / kHalf; r < (i + 1) * kReads / kHalf; ++r) read(next, r, ks);
+      if (decltype(loads)::value)
+#pragma unroll
+        for (int j = i * kLoads / MI; j < (i + 1) * kLoads / MI; ++j) ask(j);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = Mma::mma(f.b[j], f.a[i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < Sh::S; ++s) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) ask(j);
+    asked();
+  }
+  wait_stage<(Sh::S - 1) * kLoads>();
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int r = 0; r < kReads; ++r) read(f0, r, 0);
   for (int kt = 0; kt < count; ++kt) {
-    // this wave's loads of the stage are through, and its reads of the stage
-    // that the next loads overwrite; behind the barrier, every wave's
-    wait_stage<(Sh::S - 2) * kLoads>();
+    touch();
+    multiply(f0, f1, 1, std::false_type{});
+    // this wave's loads of the next stage are through (behind them are S - 2
+    // stages' loads, or a touch), and its reads of the one that the next loads
+    // overwrite; behind the barrier, every wave's
+    wait_stage<(Sh::S - 2) * kLoads + (kTouch ? 1 : 0)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    ask();
-    __builtin_amdgcn_sched_barrier(0);
-    const char* s = lds + get * kStage;
     get = get + 1 == Sh::S ? 0 : get + 1;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      u32x4 fa[MI], fb[NI];
-#pragma unroll
-      for (int j = 0; j < NI; ++j) fb[j] = rb.get(s + kA, j, ks);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = ra.get(s, i, ks);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = Mma::mma(fb[j], fa[i], acc[i][j]);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    multiply(f1, f0, 0, std::true_type{});
+    asked();
   }
   // The loads past the end land before the block's LDS is given back, and the
   // sums are formed before the branches below.
@@ -288,6 +369,26 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kWaves == 8 ? 2 : 1) void product
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[i][j]));
+  if constexpr (Sh::G > 1) {
+    typedef typename Mma::Acc Quad;
+    Quad* red = (Quad*)lds + wave * (MI * NI * 64) + lane;
+    constexpr int kGroup = Sh::kWaves * MI * NI * 64;
+    __syncthreads();  // the sums take the stages' place
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) red[(group - 1) * kGroup + (i * NI + j) * 64] = acc[i][j];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < Sh::G; ++g)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] += red[(g - 1) * kGroup + (i * NI + j) * 64];
+  }
   const int col = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {

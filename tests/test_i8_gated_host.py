@@ -110,10 +110,11 @@ def test_linear_refusals(lib):
     for name in ("x", "c", "s", "out"):
         assert f(**{name: NULL}) == INV and f(**{name: ODD}) == INV
     assert f(sx=ODD) == INV and f(b=ODD) == INV
-    need = lib.moe_linear_i8_ws_bytes(4, 64, 256, 0)
-    assert need >= 4 * 256 + 16 and lib.moe_linear_i8_ws_bytes(0, 64, 256, 0) == 0
-    assert lib.moe_linear_i8_ws_bytes(4, 64, 24, 0) == 0
-    assert f(wsb=need - 1) == WSP and f(ws=NULL) == WSP and f(ws=ctypes.c_void_p(0x10010)) == INV
+    need = lib.moe_linear_i8_ws_bytes(400, 64, 256, 0)
+    assert need >= 400 * 256 + 1600 and lib.moe_linear_i8_ws_bytes(0, 64, 256, 0) == 0
+    assert lib.moe_linear_i8_ws_bytes(400, 64, 24, 0) == 0
+    assert f(T=400, wsb=need - 1) == WSP and f(T=400, ws=NULL) == WSP
+    assert f(T=400, ws=ctypes.c_void_p(0x10010)) == INV
     assert f(T=0, x=NULL, c=NULL, s=NULL, out=NULL, ws=NULL, wsb=0) == OK
 
 

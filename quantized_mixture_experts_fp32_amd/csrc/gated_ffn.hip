@@ -11,29 +11,32 @@
 //   du = dh g s,  dg = dh u s (1 + g (1 - s)),  h = g s u       (its epilogue)
 //   dx = [dg du] Wgu,  dWgu = [dg du]^T x,  dWd = dout^T h
 // dg, du and h are rounded to bf16, the matrix cores' operand type; all sums are
-// fp32 in a fixed order.
+// fp32 in a fixed order, and g and u that are computed again stay fp32.
 #include "mm_launch.hpp"
 
 namespace moe {
 namespace {
 using namespace mm;
 
-// h = silu(g) u, and the pre-activations where they are kept (either null: not
-// wanted).
+// h = silu(g) u, and the pre-activations where they are kept: bf16 for a caller,
+// fp32 within a gradient (either null: not wanted).
 struct GatedStore {
   uint16_t* h;
-  uint16_t* gate_up;
+  void* gate_up;
+  int gu_f32;
   int f;
-  __device__ __forceinline__ void operator()(int m, int n, f32x4 g, f32x4 u) const {
+  template <typename V>
+  __device__ __forceinline__ void operator()(int m, int n, V g, V u) const {
     if (h) {
-      f32x4 v;
+      V v;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = silu_f32(g[r]) * u[r];
-      store4(h, 0, (size_t)m * f + n, v);
+      for (int r = 0; r < (int)(sizeof(V) / 4); ++r) v[r] = silu_f32(g[r]) * u[r];
+      store_as(h, 0, (size_t)m * f + n, v);
     }
     if (gate_up) {
-      store4(gate_up, 0, (size_t)m * (2 * f) + n, g);
-      store4(gate_up, 0, (size_t)m * (2 * f) + f + n, u);
+      const size_t at = (size_t)m * (2 * f) + n;
+      store_as(gate_up, gu_f32, at, g);
+      store_as(gate_up, gu_f32, at + f, u);
     }
   }
 };
@@ -42,35 +45,34 @@ struct Store {
   void* out;
   long long N;
   int f32;
-  __device__ __forceinline__ void operator()(int m, int n, f32x4 v) const {
-    store4(out, f32, (size_t)m * N + n, v);
+  template <typename V>
+  __device__ __forceinline__ void operator()(int m, int n, V v) const {
+    store_as(out, f32, (size_t)m * N + n, v);
   }
 };
 
 // dh -> dg, du and h.
 struct GatedBwdStore {
-  const uint16_t* gate_up;
+  const void* gate_up;
+  int gu_f32;
   uint16_t* dgu;
   uint16_t* h;
   int f;
-  __device__ __forceinline__ void operator()(int m, int n, f32x4 dh) const {
+  __device__ __forceinline__ void operator()(int m, int n, f32x8 dh) const {
     const size_t at = (size_t)m * (2 * f) + n;
-    const uint2 gb = *(const uint2*)(gate_up + at), ub = *(const uint2*)(gate_up + at + f);
-    const float g[4] = {bf16_bits_to_f32(gb.x & 0xFFFF), bf16_bits_to_f32(gb.x >> 16),
-                        bf16_bits_to_f32(gb.y & 0xFFFF), bf16_bits_to_f32(gb.y >> 16)};
-    const float u[4] = {bf16_bits_to_f32(ub.x & 0xFFFF), bf16_bits_to_f32(ub.x >> 16),
-                        bf16_bits_to_f32(ub.y & 0xFFFF), bf16_bits_to_f32(ub.y >> 16)};
-    f32x4 dg, du, hv;
+    const f32x8 g = load_as<f32x8>(gate_up, gu_f32, at);
+    const f32x8 u = load_as<f32x8>(gate_up, gu_f32, at + f);
+    f32x8 dg, du, hv;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < 8; ++r) {
       const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[r])), a = g[r] * s;
       du[r] = dh[r] * a;
       dg[r] = dh[r] * u[r] * (s + a * (1.0f - s));
       hv[r] = a * u[r];
     }
-    store4(dgu, 0, at, dg);
-    store4(dgu, 0, at + f, du);
-    store4(h, 0, (size_t)m * f + n, hv);
+    store_as(dgu, 0, at, dg);
+    store_as(dgu, 0, at + f, du);
+    store_as(h, 0, (size_t)m * f + n, hv);
   }
 };
 
@@ -80,9 +82,7 @@ __global__ __launch_bounds__(256) void to_bf16_kernel(const float* __restrict__ 
                                                       uint16_t* __restrict__ out) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= chunks) return;
-  const f32x4 a = *(const f32x4*)(x + 8 * i), b = *(const f32x4*)(x + 8 * i + 4);
-  store4(out, 0, 8 * (size_t)i, a);
-  store4(out, 0, 8 * (size_t)i + 4, b);
+  store_as(out, 0, 8 * (size_t)i, load_as<f32x8>(x, 1, 8 * (size_t)i));
 }
 
 size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -108,7 +108,7 @@ hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* w_gate_up, const 
                             void* ws, hipStream_t s) {
   uint16_t* h = (uint16_t*)ws;
   const hipError_t e = launch_product<Bf16, kInner, true>(
-      rows(x, d, T), pairs(w_gate_up, d, f), T, f, d, 2, GatedStore{h, gate_up, f}, nullptr, s);
+      rows(x, d, T), pairs(w_gate_up, d, f), T, f, d, 2, GatedStore{h, gate_up, 0, f}, nullptr, s);
   if (e != hipSuccess) return e;
   return launch_product<Bf16, kInner, false>(rows(h, f, T), rows(w_down, f, d), T, d, f, 2,
                                              Store{out, d, out_f32}, nullptr, s);
@@ -121,14 +121,14 @@ struct BwdSpace {
   size_t dgu, h, gate_up, x, dout, part, bytes;
   BwdSpace(int T, int d, int f, int do_f32, int x_i8, int kept) {
     size_t at = 0;
-    auto take = [&](bool wanted, size_t values) {
+    auto take = [&](bool wanted, size_t values, size_t size = 2) {
       const size_t p = at;
-      if (wanted) at += round_up(2 * values);
+      if (wanted) at += round_up(size * values);
       return p;
     };
     dgu = take(true, (size_t)T * 2 * f);
     h = take(true, (size_t)T * f);
-    gate_up = take(!kept, (size_t)T * 2 * f);
+    gate_up = take(!kept, (size_t)T * 2 * f, 4);  // fp32: not rounded on the way
     x = take(x_i8, (size_t)T * d);
     dout = take(do_f32, (size_t)T * d);
     part = at;
@@ -151,7 +151,8 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
   void* part = place(at.part);
   const uint16_t* x = (const uint16_t*)a.x;
   const uint16_t* dout = (const uint16_t*)a.dout;
-  const uint16_t* gate_up = a.gate_up;
+  const void* gate_up = a.gate_up;
+  const int gu_f32 = !gate_up;
   hipError_t e = hipSuccess;
   if (T > 0) {
     if (a.do_f32) {
@@ -169,12 +170,12 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
     if (!gate_up) {
       e = launch_product<Bf16, kInner, true>(
           rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d, 2,
-          GatedStore{nullptr, place(at.gate_up), f}, part, s);
+          GatedStore{nullptr, place(at.gate_up), 1, f}, part, s);
       if (e != hipSuccess) return e;
       gate_up = place(at.gate_up);
     }
     e = launch_product<Bf16, kOuterB, false>(rows(dout, d, T), rows(a.w_down, f, f), T, f, d,
-                                                 2, GatedBwdStore{gate_up, dgu, h, f}, part, s);
+                                                 2, GatedBwdStore{gate_up, gu_f32, dgu, h, f}, part, s);
     if (e != hipSuccess) return e;
     if (a.dx) {
       e = launch_product<Bf16, kOuterB, false>(rows(dgu, 2 * f, T), rows(a.w_gate_up, d, d), T,

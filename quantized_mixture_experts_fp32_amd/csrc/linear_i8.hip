@@ -16,15 +16,16 @@ struct ScaleStore {
   void* out;
   long long N;
   int f32;
-  __device__ __forceinline__ void operator()(int m, int n, i32x4 a) const {
+  template <typename I>
+  __device__ __forceinline__ void operator()(int m, int n, I a) const {
+    typedef std::conditional_t<sizeof(I) == 32, f32x8, f32x4> V;
     const float s = sx[m];
-    f32x4 v;
+    const V w = load_as<V>(sw, 1, n);
+    V v;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      v[r] = (float)a[r] * (s * sw[n + r]);
-      if (bias) v[r] += bias[n + r];
-    }
-    store4(out, f32, (size_t)m * N + n, v);
+    for (int r = 0; r < (int)(sizeof(I) / 4); ++r) v[r] = (float)a[r] * (s * w[r]);
+    if (bias) v += load_as<V>(bias, 1, n);
+    store_as(out, f32, (size_t)m * N + n, v);
   }
 };
 

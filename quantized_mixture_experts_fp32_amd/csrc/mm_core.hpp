@@ -20,12 +20,14 @@
 #pragma once
 #include <type_traits>
 
-#include "kcommon.hpp"
+#include "rowops.hpp"
 
 namespace moe {
 namespace mm {
 
+using row::f32x8;
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 typedef int16_t i16x8 __attribute__((ext_vector_type(8)));
 
@@ -162,12 +164,14 @@ struct Reader {
 // The matrix instruction on 64 bytes of k.
 struct Bf16 {
   typedef f32x4 Acc;
+  typedef f32x8 Acc8;
   static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
     return mfma16(as_bf16x8(a), as_bf16x8(b), c);
   }
 };
 struct I8 {
   typedef i32x4 Acc;
+  typedef i32x8 Acc8;
   // two instructions of 32 bytes of k: both operands give them in the same order
   static __device__ __forceinline__ i32x4 mma(u32x4 a, u32x4 b, i32x4 c) {
     const u64x2 x = __builtin_bit_cast(u64x2, a), y = __builtin_bit_cast(u64x2, b);
@@ -176,10 +180,25 @@ struct I8 {
   }
 };
 
-// Four consecutive values as fp32 or bf16 (round to nearest even).
-__device__ __forceinline__ void store4(void* p, int f32, size_t i, f32x4 v) {
-  if (f32) {
-    *(f32x4*)((float*)p + i) = v;
+// Four or eight consecutive values (V: f32x4, f32x8) of an array that is fp32 or
+// bf16 (stored: round to nearest even).
+template <typename V>
+__device__ __forceinline__ V load_as(const void* p, int f32, size_t i) {
+  if constexpr (sizeof(V) == 32) {
+    return f32 ? row::load8<true>(p, i) : row::load8<false>(p, i);
+  } else {
+    if (f32) return *(const V*)((const float*)p + i);
+    const u32x2 w = *(const u32x2*)((const uint16_t*)p + i);
+    return V{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
+             __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u)};
+  }
+}
+template <typename V>
+__device__ __forceinline__ void store_as(void* p, int f32, size_t i, V v) {
+  if constexpr (sizeof(V) == 32) {
+    f32 ? row::store8<true>(p, i, v) : row::store8<false>(p, i, v);
+  } else if (f32) {
+    *(V*)((float*)p + i) = v;
   } else {
     u32x2 w;
     w[0] = f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16);
@@ -221,8 +240,8 @@ __device__ __forceinline__ void tile_of(int id, int nm, int nn, int& tm, int& tn
   tn = i / rows;
 }
 
-// Epi: operator()(m, n, Acc) for four consecutive n, or in the pair form
-// operator()(m, n, Acc first, Acc second).
+// Epi: operator()(m, n, v) for eight consecutive n (N is a multiple of 8; the
+// direct kernel: four), or in the pair form operator()(m, n, first, second).
 template <typename Mma, typename Sh, bool kAOuter, bool kBOuter, bool kPair, typename Epi>
 __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kernel(
     const Problem p, const Epi epi) {
@@ -389,24 +408,39 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
 #pragma unroll
         for (int j = 0; j < NI; ++j) acc[i][j] += red[(g - 1) * kGroup + (i * NI + j) * 64];
   }
+  // A lane's four values of 16 rows would go to memory in pieces of 32 bytes, so
+  // each wave turns its rows around in LDS, 16 at a time, and writes 128 bytes of
+  // a row together (64 with TN = 32).
+  __syncthreads();  // the last stage has been read (or, of a group, the sums)
+  typedef typename Mma::Acc8 Acc8;
+  constexpr int kRow = TN * 4 + 16, kWidth = kPair ? TN / 2 : TN;  // features of the wave
+  constexpr int kLanes = kWidth / 8, kPass = 64 / kLanes < 16 ? 64 / kLanes : 16;  // rows at a time
+  char* const turn = lds + (Sh::G - 1) * (Sh::kWaves * MI * NI * 1024) + wave * (16 * kRow);
   const int col = lane & 15, q = lane >> 4;
+  const int row = lane / kLanes, at = 8 * (lane % kLanes);
+  const int n = (kPair ? n0 / 2 : n0) + wn * kWidth + at;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int m = m0 + wm * TM + 16 * i + col;
-    if (m >= p.M) continue;
-    if constexpr (kPair) {
 #pragma unroll
-      for (int j = 0; j < NI; j += 2) {
-        const int n = (n0 + wn * TN) / 2 + 8 * j + 4 * q;
-        if (n < p.N) epi(m, n, acc[i][j], acc[i][j + 1]);
-      }
-    } else {
+    for (int j = 0; j < NI; ++j) {
+      const int c = kPair ? (j & 1) * kWidth + 8 * (j & ~1) : 16 * j;  // the tile's columns
+      *(typename Mma::Acc*)(turn + col * kRow + 4 * (c + 4 * q)) = acc[i][j];
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        const int n = n0 + wn * TN + 16 * j + 4 * q;
-        if (n < p.N) epi(m, n, acc[i][j]);
+    for (int r = 0; r < 16; r += kPass) {
+      const int m = m0 + wm * TM + 16 * i + r + row;
+      if (r + row < 16 && m < p.M && n < p.N) {
+        const char* v = turn + (r + row) * kRow + 4 * at;
+        if constexpr (kPair)
+          epi(m, n, *(const Acc8*)v, *(const Acc8*)(v + 4 * kWidth));
+        else
+          epi(m, n, *(const Acc8*)v);
       }
     }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 

@@ -1,7 +1,7 @@
-// Product of few rows (up to 64 tokens) with a weight matrix: C[t][n] = sum_k
+// Product of few rows (up to 16 tokens) with a weight matrix: C[t][n] = sum_k
 // x[t][k] w[n][k], bound by the weights' bytes and by latency.  A block takes 16
-// kRT weight rows and its waves share k, 128 bytes of each row in turn.  Weights
-// are loaded straight into registers as fragments of the 16 x 16 matrix
+// weight rows and its waves share k, 128 bytes of each row in turn.  Weights are
+// loaded straight into registers as fragments of the 16 x 16 matrix
 // instruction (lane l: row l % 16, bytes 16 (l / 16) of each 64), two groups of
 // kU units ahead; the tokens' rows lie in LDS, chunk c of 16 bytes of row t at
 // c ^ (t & 15) (no bank conflicts), a piece of k at a time where they are long.
@@ -10,8 +10,8 @@
 // Buffer loads do the bounds: weight rows past the end and bytes past k are out
 // of range, read as zeros and cost no traffic.
 //
-// Pair form: gate and up rows in one block, 8 and 8 (kRT = 1) or 16 and 16, so
-// that the join has both of a feature.
+// Pair form: 8 gate and 8 up rows a block, so that the join has both of a
+// feature.
 // Quantising form (int8 weights, bf16 tokens): each wave turns whole rows into
 // codes on their way to LDS, while the weights are in flight.
 #pragma once
@@ -31,46 +31,34 @@ struct DirectArgs {
 };
 
 constexpr int kDirectWaves = 8;
-constexpr int kDirectLds = 64 << 10;  // two blocks a CU
+constexpr int kDirectLds = 64 << 10;      // two blocks a CU
+constexpr int kDirectLdsOne = 144 << 10;  // a block alone on its CU
 
-template <typename Mma, int kRT, int kNT, int kU, bool kPair, bool kQuant, typename Epi>
+template <typename Mma, int kU, bool kPair, bool kQuant, typename Epi>
 __global__ __launch_bounds__(kDirectWaves* kWave, 4) void direct_kernel(const DirectArgs p,
                                                                        Epi epi) {
   typedef typename Mma::Acc Quad;
   constexpr int W = kDirectWaves;
-  extern __shared__ __align__(1024) char lds[];  // tokens [T][piece]; then sums [W][kRT kNT][64]
+  extern __shared__ __align__(1024) char lds[];  // tokens [T][piece]; then sums [W][64]
   __shared__ float sx[16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  constexpr int kRows = kPair ? 8 * kRT : 16 * kRT;  // features a block
-  const int n0 = blockIdx.x * kRows, T = p.T;
+  const int n0 = blockIdx.x * (kPair ? 8 : 16), T = p.T;
 
-  uint32_t woff[kRT];
-#pragma unroll
-  for (int i = 0; i < kRT; ++i) {
-    const bool up = kPair && (kRT == 1 ? r >= 8 : i == 1);
-    const int n = kPair ? (kRT == 1 ? r & 7 : r) : 16 * i + r;
-    woff[i] = (uint32_t)((up ? p.N + n : n) * p.wstride) + 16 * q;
-    if (n0 + n >= p.N) woff[i] = kOutOfRange;
-  }
+  const int wrow = kPair ? r & 7 : r;
+  uint32_t woff = (uint32_t)((kPair && r >= 8 ? p.N + wrow : wrow) * p.wstride) + 16 * q;
+  if (n0 + wrow >= p.N) woff = kOutOfRange;
   const __amdgpu_buffer_rsrc_t wr = rsrc_of(p.w + (size_t)n0 * p.wstride);
-  uint32_t xat[kNT];  // the lane's row of tokens in LDS (rows past the last repeat it)
-#pragma unroll
-  for (int c = 0; c < kNT; ++c) xat[c] = min(16 * c + r, T - 1) * p.piece;
-  // chunk i of 16 bytes of token t lies at xat + 16 (i ^ (t & 15))
-  int sw[kNT];
-#pragma unroll
-  for (int c = 0; c < kNT; ++c) sw[c] = min(16 * c + r, T - 1) & 15;
+  // The lane's token in LDS (rows past the last repeat it); its chunk i of 16
+  // bytes lies at i ^ sw.
+  const int token = min(r, T - 1), sw = token & 15;
+  const char* const xrow = lds + token * p.piece;
 
   struct Unit {
-    u32x4 w[kRT][2];
+    u32x4 w[2];
   };
-  Quad acc[kRT][kNT];
-#pragma unroll
-  for (int i = 0; i < kRT; ++i)
-#pragma unroll
-    for (int c = 0; c < kNT; ++c) acc[i][c] = Quad{0, 0, 0, 0};
+  Quad acc = {0, 0, 0, 0};
   float inv_scale = 0.0f;
 
   for (int k0 = 0; k0 < p.kbytes; k0 += p.piece) {
@@ -93,12 +81,9 @@ __global__ __launch_bounds__(kDirectWaves* kWave, 4) void direct_kernel(const Di
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int b = 128 * (wave + W * (i + j)) + 64 * s;
-#pragma unroll
-          for (int t = 0; t < kRT; ++t) {
-            const uint32_t o = b + 16 * q < bytes ? woff[t] + k0 + b : kOutOfRange;
-            u[j].w[t][s] =
-                __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, (int)o, 0, 0));
-          }
+          const uint32_t o = b + 16 * q < bytes ? woff + k0 + b : kOutOfRange;
+          u[j].w[s] =
+              __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, (int)o, 0, 0));
         }
     };
     Unit a[kU], b[kU];
@@ -154,7 +139,7 @@ __global__ __launch_bounds__(kDirectWaves* kWave, 4) void direct_kernel(const Di
       load(a, 0);
       load(b, kU);
       __builtin_amdgcn_sched_barrier(0);
-      wait_stage<4 * kU * kRT>();  // the tokens are in; the weights stay in flight
+      wait_stage<4 * kU>();  // the tokens are in; the weights stay in flight
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -163,12 +148,7 @@ __global__ __launch_bounds__(kDirectWaves* kWave, 4) void direct_kernel(const Di
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int ch = 8 * (wave + W * i) + 4 * s + q;
-#pragma unroll
-        for (int c = 0; c < kNT; ++c) {
-          const u32x4 x = *(const u32x4*)(lds + xat[c] + 16 * (ch ^ sw[c]));
-#pragma unroll
-          for (int t = 0; t < kRT; ++t) acc[t][c] = Mma::mma(u.w[t][s], x, acc[t][c]);
-        }
+        acc = Mma::mma(u.w[s], *(const u32x4*)(xrow + 16 * (ch ^ sw)), acc);
       }
     };
     for (int i = 0; i < mine; i += 2 * kU) {
@@ -184,44 +164,31 @@ __global__ __launch_bounds__(kDirectWaves* kWave, 4) void direct_kernel(const Di
   }
 
   // join
-  constexpr int kTiles = kRT * kNT;
-#pragma unroll
-  for (int i = 0; i < kRT; ++i)
-#pragma unroll
-    for (int c = 0; c < kNT; ++c) asm volatile("" : "+v"(acc[i][c]));
+  asm volatile("" : "+v"(acc));
   __syncthreads();  // the sums take the tokens' place
   Quad* red = (Quad*)lds;
-#pragma unroll
-  for (int i = 0; i < kRT; ++i)
-#pragma unroll
-    for (int c = 0; c < kNT; ++c) red[(wave * kTiles + i * kNT + c) * 64 + lane] = acc[i][c];
+  red[wave * 64 + lane] = acc;
   __syncthreads();
   auto sum = [&](int o) {
     Quad v = red[o];
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += red[w * kTiles * 64 + o];
+    for (int w = 1; w < W; ++w) v += red[w * 64 + o];
     return v;
   };
   if constexpr (kQuant) epi.sx = sx;
-  for (int o = threadIdx.x; o < kTiles * 64 / (kPair ? 2 : 1); o += W * kWave) {
-    if constexpr (kPair && kRT == 1) {  // per 16 tokens 32 entries of gate rows, 32 of up rows
-      const int c = o >> 5, l = o & 31, m = 16 * c + (l & 15), n = n0 + 4 * (l >> 4);
-      if (m < T && n < p.N) epi(m, n, sum(64 * c + l), sum(64 * c + 32 + l));
-    } else {
-      const int l = o & 63, tile = o >> 6, c = tile % kNT, i = tile / kNT;
-      const int m = 16 * c + (l & 15), n = n0 + 16 * i + 4 * (l >> 4);
-      if (m < T && n < p.N) {
-        if constexpr (kPair)
-          epi(m, n, sum(o), sum(kNT * 64 + o));
-        else
-          epi(m, n, sum(o));
-      }
-    }
+  // four rows of a token a thread (pair form: of the gate tile and the up tile)
+  for (int o = threadIdx.x; o < (kPair ? 32 : 64); o += W * kWave) {
+    const int m = o & 15, n = n0 + 4 * (o >> 4);
+    if (m >= T || n >= p.N) continue;
+    if constexpr (kPair)
+      epi(m, n, sum(o), sum(32 + o));
+    else
+      epi(m, n, sum(o));
   }
 }
 
 inline bool direct_applies(long long T, long long N, long long row_bytes, bool pair) {
-  return T <= 64 && (pair ? N + 16 : 32) * row_bytes < (1LL << 31) - (1 << 20);
+  return T <= 16 && (pair ? N + 8 : 16) * row_bytes < (1LL << 31) - (1 << 20);
 }
 constexpr int kQuantRows = kDirectWaves;  // tokens that the quantising form takes
 
@@ -229,32 +196,22 @@ constexpr int kQuantRows = kDirectWaves;  // tokens that the quantising form tak
 template <typename Mma, bool kPair, bool kQuant, typename Epi>
 inline hipError_t launch_direct(DirectArgs p, const Epi& epi, hipStream_t s) {
   const int units = (p.kbytes + 127) >> 7;
-  p.piece = std::min((p.kbytes + 255) & ~255, kDirectLds / p.T & ~255);
-  auto go = [&](auto rt, auto nt, auto u) {
-    constexpr int RT = decltype(rt)::value, NT = decltype(nt)::value, U = decltype(u)::value;
-    constexpr int rows = kPair ? 8 * RT : 16 * RT;
-    // (the last load into LDS may reach past the tokens)
-    const size_t lds = std::max((size_t)p.T * p.piece + 1024, (size_t)kDirectWaves * RT * NT * 1024);
-    hipLaunchKernelGGL((direct_kernel<Mma, RT, NT, U, kPair, kQuant, Epi>),
-                       dim3((p.N + rows - 1) / rows), dim3(kDirectWaves * kWave), lds, s, p, epi);
+  const int blocks = (p.N + (kPair ? 7 : 15)) / (kPair ? 8 : 16);
+  const int most = blocks <= 256 ? kDirectLdsOne : kDirectLds;
+  p.piece = std::min((p.kbytes + 255) & ~255, most / p.T & ~255);
+  // (the last load into LDS may reach past the tokens)
+  const size_t lds = std::max((size_t)p.T * p.piece + 1024, (size_t)kDirectWaves * 1024);
+  auto go = [&](auto u) {
+    hipLaunchKernelGGL((direct_kernel<Mma, decltype(u)::value, kPair, kQuant, Epi>), dim3(blocks),
+                       dim3(kDirectWaves * kWave), lds, s, p, epi);
   };
   using std::integral_constant;
-  constexpr integral_constant<int, 1> one{};
-  constexpr integral_constant<int, 2> two{};
-  [[maybe_unused]] constexpr integral_constant<int, 4> four{};
-  if (p.T <= 16) {
-    if (units <= 16)
-      go(one, one, one);
-    else if (kQuant || units <= 32)
-      go(one, one, two);
-    else
-      go(one, one, integral_constant<int, kQuant ? 2 : 4>{});
-  } else if constexpr (!kQuant) {
-    if (p.T <= 32)
-      units <= 16 ? go(two, two, one) : go(two, two, two);
-    else
-      units <= 16 ? go(two, four, one) : go(two, four, two);
-  }
+  if (units <= 16)
+    go(integral_constant<int, 1>{});
+  else if (kQuant || units <= 32)
+    go(integral_constant<int, 2>{});
+  else
+    go(integral_constant<int, kQuant ? 2 : 4>{});
   return hipGetLastError();
 }
 

@@ -2,6 +2,7 @@
 // product's size, launch, and the join of split sums.
 #pragma once
 #include <algorithm>
+#include <utility>
 
 #include "launch.hpp"
 #include "mm_direct.hpp"
@@ -13,30 +14,47 @@ namespace mm {
 // sum over tokens).
 enum Layout { kInner, kOuterB, kOuterBoth };
 
-template <Layout kL, int bm, int bn, int wm, int wn, int stages, int groups = 1>
-using ShapeOf = std::conditional_t<kL == kOuterBoth && (bm == 192 || bm == 32), void,
-                                   Shape<bm, bn, wm, wn, stages, groups>>;
-
-// The tiled kernels, and what a product takes: 3 us and, for each 128 bytes (or
-// 64 rows) of k, the larger of `one` (latency of a stage: a block alone on a CU)
-// and `each` for every block a CU gets.  us, fitted to 130 products of 24 to
-// 4096 rows, 1000 to 12288 columns and k 1000 to 4096 on the whole chip.
+// The tiled kernels: what a product takes on the whole chip, in us, is
+//   fixed + block * n + stages * max(one, each * n)
+// for n blocks a CU and stages of 128 bytes (or 64 rows) of k; one: the latency
+// of a stage where a block is alone on its CU, each: its share of a full CU.
+// Fitted by kind of product to 140 random sizes each (1 to 8192 rows, 64 to 50304
+// columns, k 8 to 8192); on 80 others the choice took 1 % (bf16) and 2 % (int8)
+// longer than the fastest of 13 tiles on average, 33 % at most
+// (profiles/product_choice.txt).
 struct TileCost {
   int bm, bn;
-  float one[3], each[3];  // by Layout; 0: not built for it
+  struct {
+    float fixed, block, one, each;  // all 0: not built
+  } of[4];  // inner bf16, inner int8, outer B, both outer
   const char* name;
 };
-constexpr int kTileKernels = 9;
+constexpr int kTileKernels = 10;
 const TileCost kTileCosts[kTileKernels] = {
-    {256, 256, {1.35f, 1.75f, 1.75f}, {1.60f, 1.75f, 1.75f}, "tile 256x256"},
-    {192, 256, {1.15f, 1.45f, 0}, {1.30f, 1.45f, 0}, "tile 192x256"},
-    {128, 128, {0.62f, 0.97f, 0.97f}, {0.50f, 0.52f, 0.55f}, "tile 128x128"},
-    {128, 128, {0.60f, 0.76f, 0.76f}, {0.60f, 0.76f, 0.76f}, "tile 128x128 k2"},
-    {64, 128, {0.43f, 0.80f, 0}, {0.33f, 0.43f, 0}, "tile 64x128"},
-    {64, 64, {0.36f, 0.69f, 0.69f}, {0.21f, 0.30f, 0.30f}, "tile 64x64"},
-    {64, 64, {0, 0.37f, 0.37f}, {0, 0.52f, 0.52f}, "tile 64x64 k4"},
-    {32, 64, {0.24f, 0.33f, 0}, {0.165f, 0.31f, 0}, "tile 32x64"},
-    {32, 32, {0.15f, 0, 0}, {0.115f, 0, 0}, "tile 32x32 k2"},
+    {256, 256,
+     {{0.0f, 5.5f, 0.62f, 1.40f}, {0.0f, 9.6f, 1.67f, 1.94f}, {0.0f, 7.1f, 1.71f, 1.71f},
+      {0.0f, 8.1f, 1.25f, 1.75f}},
+     "tile 256x256"},
+    {192, 256,
+     {{0.0f, 4.4f, 0.14f, 1.25f}, {0.0f, 7.9f, 0.25f, 1.55f}, {0.8f, 2.5f, 1.65f, 1.65f}, {}},
+     "tile 192x256"},
+    {128, 128,
+     {{1.2f, 2.1f, 0.75f, 0.57f}, {2.0f, 3.1f, 0.71f, 0.65f}, {0.0f, 2.8f, 1.01f, 0.62f},
+      {1.6f, 3.2f, 0.95f, 0.59f}},
+     "tile 128x128"},
+    {128, 128, {{0.5f, 4.6f, 0.43f, 0.64f}, {0.1f, 6.5f, 0.51f, 0.64f}, {}, {}}, "tile 128x128 k2"},
+    {64, 128,
+     {{3.0f, 0.60f, 0.39f, 0.39f}, {2.9f, 1.7f, 0.08f, 0.39f}, {0.9f, 1.5f, 0.71f, 0.42f},
+      {1.9f, 1.8f, 0.70f, 0.45f}},
+     "tile 64x128"},
+    {64, 64,
+     {{3.1f, 0.11f, 0.28f, 0.25f}, {3.2f, 0.73f, 0.27f, 0.25f}, {0.9f, 1.2f, 0.57f, 0.25f},
+      {2.1f, 1.1f, 0.57f, 0.27f}},
+     "tile 64x64"},
+    {64, 64, {{}, {}, {1.9f, 2.5f, 0.02f, 0.37f}, {1.8f, 3.6f, 0.36f, 0.36f}}, "tile 64x64 k4"},
+    {32, 64, {{3.3f, 0.10f, 0.09f, 0.18f}, {3.4f, 0.51f, 0.18f, 0.17f}, {}, {}}, "tile 32x64"},
+    {32, 64, {{}, {}, {2.0f, 1.9f, 0.22f, 0.27f}, {}}, "tile 32x64 k4"},
+    {32, 32, {{3.1f, 0.73f, 0.05f, 0.09f}, {3.0f, 0.92f, 0.10f, 0.09f}, {}, {}}, "tile 32x32 k2"},
 };
 
 inline long long up(long long a, long long b) { return (a + b - 1) / b; }
@@ -48,23 +66,25 @@ struct Plan {
 };
 
 // M rows and N columns (of B, so 2 f of the pair form), `stages` of k.
-inline Plan plan_product(Layout l, long long M, long long N, int stages) {
+inline Plan plan_product(Layout l, bool i8, long long M, long long N, int stages) {
   constexpr int kCUs = 256;
+  const int kind = l == kInner ? i8 : l == kOuterB ? 2 : 3;
   Plan best = {0, 1, stages};
   float least = 1e30f;
   for (int t = 0; t < kTileKernels; ++t) {
-    const TileCost& c = kTileCosts[t];
-    if (c.one[l] == 0) continue;
-    const long long tiles = up(M, c.bm) * up(N, c.bn);
+    const auto& c = kTileCosts[t].of[kind];
+    if (c.one == 0) continue;
+    const long long tiles = up(M, kTileCosts[t].bm) * up(N, kTileCosts[t].bn);
     for (int k = 1; k <= (l == kOuterBoth ? 16 : 1); k *= 2) {
       if (k > 1 && stages / k < 8) break;
-      const int per = std::max((int)up(stages, k), 1), n = std::max((int)up(stages, per), 1);
-      const float us = per * std::max(c.one[l], c.each[l] * up(tiles * n, kCUs)) +
+      const int per = std::max((int)up(stages, k), 1), splits = std::max((int)up(stages, per), 1);
+      const float n = (float)up(tiles * splits, kCUs);
+      const float us = c.fixed + c.block * n + per * std::max(c.one, c.each * n) +
                        // a second launch, and the sums written and read (4 TB/s)
-                       (n > 1 ? 4.0f + 2.0e-6f * n * M * N : 0.0f);
+                       (splits > 1 ? 4.0f + 2.0e-6f * splits * M * N : 0.0f);
       if (us < least) {
         least = us;
-        best = {t, n, per};
+        best = {t, splits, per};
       }
     }
   }
@@ -73,7 +93,7 @@ inline Plan plan_product(Layout l, long long M, long long N, int stages) {
 
 // Workspace of a product over tokens (both operands outer).
 inline size_t partial_bytes(long long M, long long N, int stages) {
-  const Plan p = plan_product(kOuterBoth, M, N, stages);
+  const Plan p = plan_product(kOuterBoth, false, M, N, stages);
   return p.splits > 1 ? (size_t)p.splits * M * N * 4 : 0;
 }
 
@@ -81,60 +101,63 @@ inline size_t partial_bytes(long long M, long long N, int stages) {
 struct StorePartial {
   float* ws;
   long long M, N;
-  __device__ __forceinline__ void operator()(int m, int n, f32x4 v) const {
-    *(f32x4*)(ws + ((size_t)blockIdx.y * M + m) * N + n) = v;
+  template <typename V>
+  __device__ __forceinline__ void operator()(int m, int n, V v) const {
+    store_as(ws, 1, ((size_t)blockIdx.y * M + m) * N + n, v);
   }
 };
 
-// The splits' sums in their order, and the epilogue; four columns a thread.
+// The splits' sums in their order, and the epilogue; eight columns a thread.
 template <typename Epi>
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ ws, long long M,
                                                    long long N, int splits, const Epi epi) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, nq = N / 4;
-  if (i >= M * nq) return;
-  const int m = (int)(i / nq), n = 4 * (int)(i % nq);
-  const float* p = ws + (size_t)m * N + n;
-  f32x4 v = *(const f32x4*)p;
-  for (int s = 1; s < splits; ++s) v += *(const f32x4*)(p + (size_t)s * M * N);
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, per = N / 8;
+  if (i >= M * per) return;
+  const int m = (int)(i / per), n = 8 * (int)(i % per);
+  const size_t at = (size_t)m * N + n;
+  f32x8 v = row::load8<true>(ws, at);
+  for (int s = 1; s < splits; ++s) v += row::load8<true>(ws, at + (size_t)s * M * N);
   epi(m, n, v);
 }
 
-template <typename Mma, typename Sh, Layout kL, bool kPair, typename Epi>
-inline void launch_shape(Problem p, const Plan& plan, const Epi& epi, hipStream_t s) {
-  if constexpr (!std::is_void_v<Sh>) {
-    p.nm = (int)up(p.M, Sh::BM);
-    p.nn = (int)up(kPair ? 2LL * p.N : p.N, Sh::BN);
-    p.per_group = (int)up(plan.per, Sh::G);
-    hipLaunchKernelGGL((product_kernel<Mma, Sh, kL == kOuterBoth, kL != kInner, kPair, Epi>),
-                       dim3(p.nm * p.nn, plan.splits), dim3(Sh::kThreads), Sh::kLds, s, p, epi);
-  }
+template <typename Mma, Layout kL, bool kPair, typename Epi, int... kShape>
+inline void launch_shape(Problem p, const Plan& plan, const Epi& epi, hipStream_t s,
+                         std::integer_sequence<int, kShape...>) {
+  typedef Shape<kShape...> Sh;
+  p.nm = (int)up(p.M, Sh::BM);
+  p.nn = (int)up(kPair ? 2LL * p.N : p.N, Sh::BN);
+  p.per_group = (int)up(plan.per, Sh::G);
+  hipLaunchKernelGGL((product_kernel<Mma, Sh, kL == kOuterBoth, kL != kInner, kPair, Epi>),
+                     dim3(p.nm * p.nn, plan.splits), dim3(Sh::kThreads), Sh::kLds, s, p, epi);
 }
 
 template <typename Mma, Layout kL, bool kPair, typename Epi>
 inline void launch_tiles(const Problem& p, const Plan& plan, const Epi& epi, hipStream_t s) {
-  auto go = [&](auto* shape) {
-    launch_shape<Mma, std::remove_pointer_t<decltype(shape)>, kL, kPair>(p, plan, epi, s);
-  };
-  constexpr bool kOuter = kL != kInner, kSlim = kL != kOuterBoth;
-  switch (plan.tile) {
-    case 0: return go((ShapeOf<kL, 256, 256, 2, 4, 2>*)nullptr);
-    case 1: return go((ShapeOf<kL, 192, 256, 2, 4, 2>*)nullptr);
-    case 2: return go((ShapeOf<kL, 128, 128, 2, 2, 2>*)nullptr);
-    case 3: return go((ShapeOf<kL, 128, 128, 2, 2, 2, 2>*)nullptr);
-    case 4:
-      if constexpr (kSlim) return go((ShapeOf<kL, 64, 128, 1, 4, 3>*)nullptr);
+  auto go = [&](auto shape) { launch_shape<Mma, kL, kPair>(p, plan, epi, s, shape); };
+  using std::integer_sequence;
+  constexpr bool kIn = kL == kInner, kB = kL == kOuterB, kBoth = kL == kOuterBoth;
+  switch (plan.tile) {  // (as kTileCosts has them)
+    case 0: return go(integer_sequence<int, 256, 256, 2, 4, 2>{});
+    case 1:
+      if constexpr (!kBoth) go(integer_sequence<int, 192, 256, 2, 4, 2>{});
       return;
-    case 5: return go((ShapeOf<kL, 64, 64, 2, 2, 3>*)nullptr);
+    case 2: return go(integer_sequence<int, 128, 128, 2, 2, 2>{});
+    case 3:
+      if constexpr (kIn) go(integer_sequence<int, 128, 128, 2, 2, 2, 2>{});
+      return;
+    case 4: return go(integer_sequence<int, 64, 128, 1, 4, 3>{});
+    case 5: return go(integer_sequence<int, 64, 64, 2, 2, 3>{});
     case 6:
-      if constexpr (kOuter) return go((ShapeOf<kL, 64, 64, 2, 2, 2, 4>*)nullptr);
+      if constexpr (!kIn) go(integer_sequence<int, 64, 64, 2, 2, 2, 4>{});
       return;
     case 7:
-      if constexpr (kOuter)
-        return go((ShapeOf<kL, 32, 64, 2, 2, 3, 4>*)nullptr);
-      else
-        return go((ShapeOf<kL, 32, 64, 2, 2, 4>*)nullptr);
+      if constexpr (kIn) go(integer_sequence<int, 32, 64, 2, 2, 4>{});
+      return;
     case 8:
-      if constexpr (!kOuter) return go((ShapeOf<kL, 32, 32, 2, 1, 4, 2>*)nullptr);
+      if constexpr (kB) go(integer_sequence<int, 32, 64, 2, 2, 3, 4>{});
+      return;
+    case 9:
+      if constexpr (kIn) go(integer_sequence<int, 32, 32, 2, 1, 4, 2>{});
       return;
   }
 }
@@ -157,13 +180,13 @@ inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int 
       return launch_direct<Mma, kPair, false>({a.p, b.p, a.stride, b.stride, M, N, p.kbytes, 0},
                                               epi, s);
   }
-  const Plan plan = plan_product(kL, M, kPair ? 2LL * N : N, p.stages);
+  const Plan plan = plan_product(kL, std::is_same_v<Mma, I8>, M, kPair ? 2LL * N : N, p.stages);
   if constexpr (kL == kOuterBoth) {
     if (plan.splits > 1) {
       launch_tiles<Mma, kL, kPair>(p, plan, StorePartial{(float*)ws, M, N}, s);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
-      hipLaunchKernelGGL((join_kernel<Epi>), dim3((uint32_t)up((long long)M * (N / 4), 256)),
+      hipLaunchKernelGGL((join_kernel<Epi>), dim3((uint32_t)up((long long)M * (N / 8), 256)),
                          dim3(256), 0, s, (const float*)ws, (long long)M, (long long)N,
                          plan.splits, epi);
       return hipGetLastError();

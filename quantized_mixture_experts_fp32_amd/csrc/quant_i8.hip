@@ -38,45 +38,50 @@ __global__ __launch_bounds__(256) void quantize_i8_groups(const void* __restrict
   if (l == 0) scales[i] = s.scale;
 }
 
-// A block a row, which it holds in registers (kNC chunks of eight a thread), or
-// reads twice (kNC = 0).
-template <bool kF32, int kNC>
-__global__ __launch_bounds__(256) void quantize_i8_rows(const void* __restrict__ x, int K,
+// A row by W waves, which hold it in registers (kNC chunks of eight a lane), or
+// read it twice (kNC = 0); blocks of four waves.
+template <bool kF32, int kNC, int W>
+__global__ __launch_bounds__(256) void quantize_i8_rows(const void* __restrict__ x, int T, int K,
                                                         int8_t* __restrict__ codes,
                                                         float* __restrict__ scales) {
   __shared__ uint32_t red[4];
-  const size_t base = (size_t)blockIdx.x * K;
-  const int nch = K >> 3, tid = threadIdx.x;
+  const int wave = threadIdx.x >> 6, t = blockIdx.x * (4 / W) + wave / W;
+  const int first = threadIdx.x % (64 * W), nch = K >> 3;
+  if (t >= T) return;  // (a whole row's waves, and with W = 4 none)
+  const size_t base = (size_t)t * K;
   f32x8 v[kNC > 0 ? kNC : 1];
   uint32_t m = 0;
   if (kNC > 0) {
 #pragma unroll
     for (int i = 0; i < kNC; ++i) {
-      const int c = tid + 256 * i;
+      const int c = first + 64 * W * i;
       v[i] = 0.0f;
       if (c < nch) v[i] = load8<kF32>(x, base + 8 * c);
     }
 #pragma unroll
     for (int i = 0; i < kNC; ++i) m = max(m, top8(v[i]));
   } else {
-    for (int c = tid; c < nch; c += 256) m = max(m, top8(load8<kF32>(x, base + 8 * c)));
+    for (int c = first; c < nch; c += 64 * W) m = max(m, top8(load8<kF32>(x, base + 8 * c)));
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, kWave));
-  if ((tid & 63) == 0) red[tid >> 6] = m;
-  __syncthreads();
-  const Scaling s(max(max(red[0], red[1]), max(red[2], red[3])));
+  if (W > 1) {
+    if ((threadIdx.x & 63) == 0) red[wave] = m;
+    __syncthreads();
+    m = max(max(red[0], red[1]), max(red[2], red[3]));
+  }
+  const Scaling s(m);
   if (kNC > 0) {
 #pragma unroll
     for (int i = 0; i < kNC; ++i) {
-      const int c = tid + 256 * i;
+      const int c = first + 64 * W * i;
       if (c < nch) *(u32x2*)(codes + base + 8 * c) = codes8(v[i], s.inv);
     }
   } else {
-    for (int c = tid; c < nch; c += 256)
+    for (int c = first; c < nch; c += 64 * W)
       *(u32x2*)(codes + base + 8 * c) = codes8(load8<kF32>(x, base + 8 * c), s.inv);
   }
-  if (tid == 0) scales[blockIdx.x] = s.scale;
+  if (first == 0) scales[t] = s.scale;
 }
 
 // Codes back to values, eight a thread; G groups a row (128 each, or one).
@@ -104,20 +109,31 @@ hipError_t launch_quantize_i8(const void* x, int x_f32, int T, int K, int by_row
                        codes, scales);
     return hipGetLastError();
   }
-  auto go = [&](auto nc) {
-    constexpr int NC = decltype(nc)::value;
-    auto k = x_f32 ? quantize_i8_rows<true, NC> : quantize_i8_rows<false, NC>;
-    hipLaunchKernelGGL(k, dim3(T), dim3(256), 0, s, x, K, codes, scales);
+  auto go = [&](auto nc, auto w) {
+    constexpr int NC = decltype(nc)::value, W = decltype(w)::value;
+    auto k = x_f32 ? quantize_i8_rows<true, NC, W> : quantize_i8_rows<false, NC, W>;
+    hipLaunchKernelGGL(k, dim3((T + 4 / W - 1) / (4 / W)), dim3(256), 0, s, x, T, K, codes,
+                       scales);
   };
   using std::integral_constant;
-  if (K <= 2048)
-    go(integral_constant<int, 1>{});
+  // A wave a row where it can hold it: no barrier, and short rows leave no lanes
+  // idle (5597 x 336: .. us); four where there are few rows or they are long.
+  constexpr integral_constant<int, 1> one{};
+  constexpr integral_constant<int, 4> four{};
+  if (K <= 512)
+    go(one, one);
+  else if (K <= 1024)
+    go(integral_constant<int, 2>{}, one);
+  else if (K <= 2048 && T > 512)
+    go(four, one);
+  else if (K <= 2048)
+    go(one, four);
   else if (K <= 4096)
-    go(integral_constant<int, 2>{});
+    go(integral_constant<int, 2>{}, four);
   else if (K <= 8192)
-    go(integral_constant<int, 4>{});
+    go(four, four);
   else
-    go(integral_constant<int, 0>{});
+    go(integral_constant<int, 0>{}, four);
   return hipGetLastError();
 }
 

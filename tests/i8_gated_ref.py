@@ -109,7 +109,6 @@ def gated_ffn_bwd(dout, x, w, v, gate_up=None, dout_f32=False, x_rounded=False, 
         wa = w.abs().t().contiguous()
         more = ex @ wa
         eg, eu = eg + more[:, :f], eu + more[:, f:]
-        eg, eu = eg + BF * g.abs(), eu + BF * u.abs()  # kept as bf16 between two steps
     else:
         g, u = gate_up[:, :f], gate_up[:, f:]
         eg = eu = torch.zeros_like(g)

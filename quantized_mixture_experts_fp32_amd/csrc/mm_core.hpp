@@ -14,9 +14,12 @@
 //
 //   K-inner: row r takes 128 bytes, 16-byte chunk c at c ^ ((r >> 1) & 7): the
 //     16 rows a fragment reads fall on all 64 banks.
-//   K-outer: row k takes 2 BM bytes, 32-byte granule g at g ^ f(k), f(k) =
-//     k & 3 | (k >> 1) & 4; fragments come through the LDS transpose read, which
-//     turns four rows of 16 values into four values for each of 16 lanes.
+//   K-outer: row k takes 2 BM bytes.  A lane reads F = TM / 16 neighbouring
+//     values of eight rows of k and pairs them up in registers, so that it holds
+//     eight k of F fragments: fragment t is the tile's rows F r + t, r < 16 (the
+//     LDS transpose read gives rows 16 t + r, but at a quarter of the rate:
+//     8192^3 with both operands outer .. us, this way .. us).  Sixteen-byte chunk c
+//     lies at c ^ s(k), which keeps the four octets of k on different banks.
 #pragma once
 #include <type_traits>
 
@@ -55,10 +58,18 @@ __device__ __forceinline__ void wait_stage() {
   __builtin_amdgcn_s_waitcnt((vm & 15) | ((vm >> 4) << 14) | 0x70);
 }
 
+// Where row k of a K-outer stage has its chunks: a read takes 16, 32 or 64 lanes
+// at a time (8, 4 or 2 values each), so 1, 2 or 4 octets of k.
+template <int kRows, int kF>
+__device__ __forceinline__ int swizzle(int k) {
+  return kF >= 8 ? 0 : (((k >> 3) & (8 / kF - 1)) * 2 * kF) & (kRows / 8 - 1);
+}
+
 // Loader of one operand's stages.  kRows: rows (K-inner) or columns (K-outer)
 // of the tile; kPair: rows of two matrices, interleaved by 16.
 // kGroups: the stages are dealt to so many loaders in turn.
-template <bool kOuter, bool kPair, int kRows, int kWaves, int kGroups>
+// kF: fragments of a wave's rows.
+template <bool kOuter, bool kPair, int kRows, int kF, int kWaves, int kGroups>
 struct Loader {
   static constexpr int kLoads = kRows / 8 / kWaves;  // a wave's loads a stage
   static_assert(kRows % (8 * kWaves) == 0, "whole loads a wave");
@@ -78,8 +89,7 @@ struct Loader {
     const int r = row_of(j);
     if (!kOuter) return (lane & 7) ^ ((r >> 1) & 7);
     const int pos = ((w * kLoads + j) * 64 + lane) % (kRows / 8);
-    const int f = ((r & 3) | ((r >> 1) & 4)) & (kRows / 16 - 1);
-    return 2 * ((pos >> 1) ^ f) + (pos & 1);
+    return pos ^ swizzle<kRows, kF>(r);
   }
 
   // row0: the tile's first row (K-inner, of each matrix) or column (K-outer);
@@ -129,40 +139,50 @@ struct Loader {
   }
 };
 
-// Fragments of a stage: 16 rows from the tile's row 16 t on, k step ks (64
-// bytes of k).
-template <bool kOuter, int kRows, int kTiles>
+// A wave's fragments of a stage, k step ks (64 bytes, 32 rows of k): what is read
+// of LDS, and fragment t from it.
+template <bool kOuter, int kRows, int kF>
 struct Reader {
-  uint32_t at[kOuter ? kTiles : 2];
+  static constexpr int kReads = kOuter ? 8 : kF;
+  typedef uint32_t Part __attribute__((ext_vector_type(kOuter ? (kF < 8 ? kF / 2 : 4) : 4)));
+  struct Raw {
+    Part v[kReads];
+  };
+  static_assert(!kOuter || kF == 2 || kF == 4 || kF == 8, "whole reads");
+  uint32_t at[kOuter ? 1 : 2];
   __device__ __forceinline__ void init(int row0, int lane) {  // the wave's first row
     const int i = lane & 15, q = lane >> 4;
     if (kOuter) {
-      constexpr int kGran = kRows / 16;
-      const int k = 8 * q + (i >> 2), f = ((k & 3) | ((k >> 1) & 4)) & (kGran - 1);
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-        at[t] = k * (2 * kRows) + (((row0 / 16 + t) ^ f) << 5) + 8 * (i & 3);
+      const int b = 2 * row0 + 2 * kF * i;  // byte of a row; swizzled by chunks of 16
+      at[0] = 8 * q * (2 * kRows) + (b ^ (16 * swizzle<kRows, kF>(8 * q)));
     } else {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         at[s] = (row0 + i) * kStageBytes + (((4 * s + q) ^ ((i >> 1) & 7)) << 4);
     }
   }
-  __device__ __forceinline__ u32x4 get(const char* lds, int t, int ks) const {
-    if (kOuter) {
-      typedef __attribute__((address_space(3))) i16x4* P;
-      const char* b = lds + at[t] + ks * 32 * (2 * kRows);
-      const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(b));
-      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(b + 4 * (2 * kRows)));
-      const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      return __builtin_bit_cast(u32x4, v);
-    }
-    return *(const u32x4*)(lds + at[ks] + t * (16 * kStageBytes));
+  __device__ __forceinline__ void read(Raw& raw, const char* lds, int r, int ks) const {
+    raw.v[r] = kOuter ? *(const Part*)(lds + at[0] + (32 * ks + r) * (2 * kRows))
+                      : *(const Part*)(lds + at[kOuter ? 0 : ks] + r * (16 * kStageBytes));
   }
+  // dword p (k = 2 p, 2 p + 1) of fragment t of an outer operand
+  __device__ __forceinline__ uint32_t part(const Raw& raw, int t, int p) const {
+    return __builtin_amdgcn_perm(raw.v[2 * p + 1][t >> 1], raw.v[2 * p][t >> 1],
+                                 t & 1 ? 0x07060302u : 0x05040100u);
+  }
+  __device__ __forceinline__ u32x4 get(const Raw& raw, int t) const {
+    if constexpr (kOuter)
+      return u32x4{part(raw, t, 0), part(raw, t, 1), part(raw, t, 2), part(raw, t, 3)};
+    else
+      return raw.v[t];
+  }
+  // The wave's row that lane column c (of 16) of fragment t holds.
+  static __device__ __forceinline__ int row(int t, int c) { return kOuter ? kF * c + t : 16 * t + c; }
 };
 
 // The matrix instruction on 64 bytes of k.
 struct Bf16 {
+  typedef float Value;
   typedef f32x4 Acc;
   typedef f32x8 Acc8;
   static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
@@ -170,6 +190,7 @@ struct Bf16 {
   }
 };
 struct I8 {
+  typedef int32_t Value;
   typedef i32x4 Acc;
   typedef i32x8 Acc8;
   // two instructions of 32 bytes of k: both operands give them in the same order
@@ -262,8 +283,8 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
   const int block0 = blockIdx.y * Sh::G * p.per_group, stage0 = block0 + group;
   const int count = min(p.per_group, (p.stages - block0 + Sh::G - 1) / Sh::G);
 
-  Loader<kAOuter, false, Sh::BM, Sh::kWaves, Sh::G> la;
-  Loader<kBOuter, kPair, Sh::BN, Sh::kWaves, Sh::G> lb;
+  Loader<kAOuter, false, Sh::BM, MI, Sh::kWaves, Sh::G> la;
+  Loader<kBOuter, kPair, Sh::BN, NI, Sh::kWaves, Sh::G> lb;
   la.init(p.a, m0, kAOuter ? p.krows : p.kbytes, stage0, wave, lane);
   lb.init(p.b, kPair ? n0 / 2 : n0, kBOuter ? p.krows : p.kbytes, stage0, wave, lane);
   Reader<kAOuter, Sh::BM, MI> ra;
@@ -330,19 +351,23 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
     put = put + 1 == Sh::S ? 0 : put + 1;
   };
   struct Frags {
-    u32x4 a[MI], b[NI];
+    typename decltype(ra)::Raw a;
+    typename decltype(rb)::Raw b;
   } f0, f1;
-  auto read = [&](Frags& f, int i, int ks) {
+  constexpr int kReadsB = decltype(rb)::kReads, kReads = kReadsB + decltype(ra)::kReads;
+  auto read = [&](Frags& f, int r, int ks) {
     const char* s = ring + get * kStage;
-    if (i < NI)
-      f.b[i] = rb.get(s + kA, i, ks);
+    if (r < kReadsB)
+      rb.read(f.b, s + kA, r, ks);
     else
-      f.a[i - NI] = ra.get(s, i - NI, ks);
+      ra.read(f.a, s, r - kReadsB, ks);
   };
   // The products of one k step; between its rows the fragments of the next step
   // are asked for (in its first rows) and, `loads`, the next stage's loads: all
   // at once they would hold the wave up while the memory pipe takes them in.
-  constexpr int kReads = MI + NI, kHalf = kAOuter && kBOuter ? (MI + 3) / 4 : (MI + 1) / 2;
+  constexpr int kHalf = (MI + 1) / 2;
+  // An outer operand's fragments are made one row of products ahead.
+  u32x4 b[NI], a;
   auto multiply = [&](const Frags& f, Frags& next, int ks, auto loads) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -352,8 +377,25 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
       if (decltype(loads)::value)
 #pragma unroll
         for (int j = i * kLoads / MI; j < (i + 1) * kLoads / MI; ++j) ask(j);
+      if (!kAOuter) a = ra.get(f.a, i);
+      if (!kBOuter && i == 0)
 #pragma unroll
-      for (int j = 0; j < NI; ++j) acc[i][j] = Mma::mma(f.b[j], f.a[i], acc[i][j]);
+        for (int j = 0; j < NI; ++j) b[j] = rb.get(f.b, j);
+      u32x4 ahead;
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        acc[i][j] = Mma::mma(b[j], a, acc[i][j]);
+        if constexpr (kAOuter) {
+#pragma unroll
+          for (int q = j * 4 / NI; q < (j + 1) * 4 / NI; ++q)
+            ahead[q] = i + 1 < MI ? ra.part(f.a, i + 1, q) : ra.part(next.a, 0, q);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (kBOuter) {
+          if (i + 1 == MI) b[j] = rb.get(next.b, j);
+        }
+      }
+      if (kAOuter) a = ahead;
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -368,6 +410,9 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int r = 0; r < kReads; ++r) read(f0, r, 0);
+  a = ra.get(f0.a, 0);
+#pragma unroll
+  for (int j = 0; j < NI; ++j) b[j] = rb.get(f0.b, j);
   for (int kt = 0; kt < count; ++kt) {
     touch();
     multiply(f0, f1, 1, std::false_type{});
@@ -421,16 +466,28 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
   const int n = (kPair ? n0 / 2 : n0) + wn * kWidth + at;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
+    char* const to = turn + col * kRow;
+    if constexpr (kBOuter) {  // NI neighbouring columns, one of each fragment
+      typedef typename Mma::Value Row __attribute__((ext_vector_type(NI)));
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int c = kPair ? (j & 1) * kWidth + 8 * (j & ~1) : 16 * j;  // the tile's columns
-      *(typename Mma::Acc*)(turn + col * kRow + 4 * (c + 4 * q)) = acc[i][j];
+      for (int r = 0; r < 4; ++r) {
+        Row v;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) v[j] = acc[i][j][r];
+        *(Row*)(to + 4 * NI * (4 * q + r)) = v;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const int c = kPair ? (j & 1) * kWidth + 8 * (j & ~1) : 16 * j;  // the tile's columns
+        *(typename Mma::Acc*)(to + 4 * (c + 4 * q)) = acc[i][j];
+      }
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int r = 0; r < 16; r += kPass) {
-      const int m = m0 + wm * TM + 16 * i + r + row;
+      const int m = m0 + wm * TM + decltype(ra)::row(i, r + row);
       if (r + row < 16 && m < p.M && n < p.N) {
         const char* v = turn + (r + row) * kRow + 4 * at;
         if constexpr (kPair)

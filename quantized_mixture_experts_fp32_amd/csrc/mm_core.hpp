@@ -228,14 +228,15 @@ __device__ __forceinline__ void store_as(void* p, int f32, size_t i, V v) {
   }
 }
 
-// A configuration: tile, waves along m and n, stages in the ring, and groups of
-// waves that share the tile's k (each with a ring of its own, joined in LDS).
-template <int bm, int bn, int wm, int wn, int stages, int groups = 1>
+// A configuration: tile, waves along m and n, stages in the rings, groups of
+// waves that share the tile's k (each with rings of its own, joined in LDS), and
+// stages that B's ring has more than A's.
+template <int bm, int bn, int wm, int wn, int stages, int groups = 1, int more = 0>
 struct Shape {
-  static constexpr int BM = bm, BN = bn, WM = wm, WN = wn, S = stages, G = groups;
+  static constexpr int BM = bm, BN = bn, WM = wm, WN = wn, S = stages, G = groups, SB = S + more;
   static constexpr int kWaves = wm * wn, kThreads = 64 * kWaves * groups;  // waves: of a group
-  static constexpr int kRing = (bm + bn) * kStageBytes * stages;
-  static constexpr int kLds = groups * (kRing + 256 * kWaves);  // and a place for touched lines
+  static constexpr int kRing = (bm * S + bn * SB) * kStageBytes;
+  static constexpr int kLds = groups * kRing;
 };
 
 struct Problem {
@@ -268,7 +269,7 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
     const Problem p, const Epi epi) {
   extern __shared__ __align__(1024) char lds[];
   constexpr int TM = Sh::BM / Sh::WM, TN = Sh::BN / Sh::WN, MI = TM / 16, NI = TN / 16;
-  constexpr int kA = Sh::BM * kStageBytes, kStage = kA + Sh::BN * kStageBytes;
+  constexpr int kA = Sh::BM * kStageBytes, kB = Sh::BN * kStageBytes;
   const int lane = threadIdx.x & 63;
   const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = id / Sh::kWaves, wave = id % Sh::kWaves;
@@ -298,57 +299,26 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = typename Mma::Acc{0, 0, 0, 0};
 
-  // Lines that this lane touches ahead of their loads, so that they are in L2
-  // then.  The tiles that run on an XCD at a time share rows of A four at a time
-  // and columns of B eight at a time (tile_of), so a tile touches its share of
-  // each; half the waves see to A, half to B.  What comes back goes to a spare
-  // place in LDS.
-  // Two stages a ring leave a stage's loads too little time for HBM; with more,
-  // and in the largest tiles of inner operands, touches cost more than they give
-  // (1024 x 4096 x 4096 in tiles of 128 x 128: 57 -> 42 us; 4096 x 4096 x 4096,
-  // outer operands, tiles of 256 x 256: 138 -> 115 us, inner 106 -> 110 us).
-  constexpr bool kTouch = Sh::S == 2 && (kAOuter || kBOuter || Sh::kWaves == 4);
-  constexpr int kHalfWaves = Sh::kWaves / 2;
-  const bool for_a = wave < kHalfWaves, outer = for_a ? kAOuter : kBOuter;
-  const int parts = for_a ? (p.nn >= 4 ? 4 : p.nn >= 2 ? 2 : 1)
-                          : (p.nm >= 8 ? 8 : p.nm >= 4 ? 4 : p.nm >= 2 ? 2 : 1);
-  const Operand& to = for_a ? p.a : p.b;
-  const bool second = kPair && !for_a && (wave & 1);  // pair form: its waves take turns
-  const int mine = (for_a ? Sh::BM : Sh::BN) / parts / kHalfWaves;
-  const int line = ((for_a ? tn : tm) & (parts - 1)) * (mine * kHalfWaves) +
-                   (wave % kHalfWaves) * mine + lane;
-  const int first = for_a ? m0 : kPair ? n0 / 2 : n0;
-  const int trow = outer ? line / ((for_a ? Sh::BM : Sh::BN) / 64)
-                         : kPair && !for_a ? line / 2 : line;
-  const int tcol = outer ? 64 * (line % ((for_a ? Sh::BM : Sh::BN) / 64)) : 0;
-  const long long tstep = for_a ? la.step : lb.step;
-  uint32_t toff = (uint32_t)(trow * to.stride) + 2 * tcol;
-  if (lane >= mine || first + (outer ? tcol : trow) >= to.rows) toff = kOutOfRange;
-  // stages that can be touched whole; past them the lines are out of range
-  int tleft = (outer ? p.krows / kStageK : p.kbytes / kStageBytes) - stage0 - Sh::S * Sh::G;
-  const char* tbase = (second ? to.p2 : to.p) + (outer ? 2LL * first : first * to.stride) +
-                      (stage0 + Sh::S * Sh::G) * (tstep / Sh::G);
-  auto touch = [&]() {
-    if (!kTouch) return;
-    if (tleft <= 0) toff = kOutOfRange;
-    tleft -= Sh::G;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_of(tbase), (Lds)(lds + Sh::G * Sh::kRing + 256 * id),
-                                             4, (int)toff, 0, 0, 0);
-    tbase += tstep;
-  };
   constexpr int kLA = decltype(la)::kLoads, kLoads = kLA + decltype(lb)::kLoads;
-  int put = 0, get = 0;
-  auto ask = [&](int j) {  // past the last stage the loads are out of range
-    char* s = ring + put * kStage;
+  // The rings' next places: to load into, and to read.
+  struct Place {
+    int put = 0, get = 0;
+  } at_a, at_b;
+  auto after = [](int i, int stages) { return i + 1 == stages ? 0 : i + 1; };
+  char* const ring_b = ring + Sh::S * kA;
+  auto ask = [&](int j) {  // (past the last stage the loads are out of range)
     if (j < kLA)
-      la.load(j, s);
+      la.load(j, ring + at_a.put * kA);
     else
-      lb.load(j - kLA, s + kA);
+      lb.load(j - kLA, ring_b + at_b.put * kB);
   };
-  auto asked = [&]() {
+  auto asked_a = [&]() {
     la.next();
+    at_a.put = after(at_a.put, Sh::S);
+  };
+  auto asked_b = [&]() {
     lb.next();
-    put = put + 1 == Sh::S ? 0 : put + 1;
+    at_b.put = after(at_b.put, Sh::SB);
   };
   struct Frags {
     typename decltype(ra)::Raw a;
@@ -356,11 +326,10 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
   } f0, f1;
   constexpr int kReadsB = decltype(rb)::kReads, kReads = kReadsB + decltype(ra)::kReads;
   auto read = [&](Frags& f, int r, int ks) {
-    const char* s = ring + get * kStage;
     if (r < kReadsB)
-      rb.read(f.b, s + kA, r, ks);
+      rb.read(f.b, ring_b + at_b.get * kB, r, ks);
     else
-      ra.read(f.a, s, r - kReadsB, ks);
+      ra.read(f.a, ring + at_a.get * kA, r - kReadsB, ks);
   };
   // The products of one k step; between its rows the fragments of the next step
   // are asked for (in its first rows) and, `loads`, the next stage's loads: all
@@ -368,15 +337,15 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
   constexpr int kHalf = (MI + 1) / 2;
   // An outer operand's fragments are made one row of products ahead.
   u32x4 b[NI], a;
-  auto multiply = [&](const Frags& f, Frags& next, int ks, auto loads) {
+  auto multiply = [&](const Frags& f, Frags& next, int ks, auto from, auto to) {
+    constexpr int kFrom = decltype(from)::value, kMore = decltype(to)::value - kFrom;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       if (i < kHalf)
 #pragma unroll
         for (int r = i * kReads / kHalf; r < (i + 1) * kReads / kHalf; ++r) read(next, r, ks);
-      if (decltype(loads)::value)
 #pragma unroll
-        for (int j = i * kLoads / MI; j < (i + 1) * kLoads / MI; ++j) ask(j);
+      for (int j = i * kMore / MI; j < (i + 1) * kMore / MI; ++j) ask(kFrom + j);
       if (!kAOuter) a = ra.get(f.a, i);
       if (!kBOuter && i == 0)
 #pragma unroll
@@ -399,11 +368,17 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  using std::integral_constant;
+  constexpr bool kApart = Sh::SB > Sh::S;  // B's loads in the other half than A's
+  constexpr integral_constant<int, 0> kFirst{};
+  constexpr integral_constant<int, kLA> kBetween{};
+  constexpr integral_constant<int, kLoads> kLast{};
 #pragma unroll
   for (int s = 0; s < Sh::S; ++s) {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) ask(j);
-    asked();
+    asked_a();
+    asked_b();
   }
   wait_stage<(Sh::S - 1) * kLoads>();
   __builtin_amdgcn_s_barrier();
@@ -414,17 +389,27 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
 #pragma unroll
   for (int j = 0; j < NI; ++j) b[j] = rb.get(f0.b, j);
   for (int kt = 0; kt < count; ++kt) {
-    touch();
-    multiply(f0, f1, 1, std::false_type{});
+    if constexpr (kApart) {
+      multiply(f0, f1, 1, kBetween, kLast);
+      asked_b();
+    } else {
+      multiply(f0, f1, 1, kFirst, kFirst);
+    }
     // this wave's loads of the next stage are through (behind them are S - 2
-    // stages' loads, or a touch), and its reads of the one that the next loads
-    // overwrite; behind the barrier, every wave's
-    wait_stage<(Sh::S - 2) * kLoads + (kTouch ? 1 : 0)>();
+    // stages' loads, or B's loads of this half), and its reads of the one that
+    // the next loads overwrite; behind the barrier, every wave's
+    wait_stage<(Sh::S - 2) * kLoads + (kApart ? kLoads - kLA : 0)>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    get = get + 1 == Sh::S ? 0 : get + 1;
-    multiply(f1, f0, 0, std::true_type{});
-    asked();
+    at_a.get = after(at_a.get, Sh::S);
+    at_b.get = after(at_b.get, Sh::SB);
+    if constexpr (kApart) {
+      multiply(f1, f0, 0, kFirst, kBetween);
+    } else {
+      multiply(f1, f0, 0, kFirst, kLast);
+      asked_b();
+    }
+    asked_a();
   }
   // The loads past the end land before the block's LDS is given back, and the
   // sums are formed before the branches below.

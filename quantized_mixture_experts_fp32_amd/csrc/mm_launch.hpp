@@ -32,32 +32,33 @@ struct TileCost {
 constexpr int kTileKernels = 10;
 const TileCost kTileCosts[kTileKernels] = {
     {256, 256,
-     {{0.0f, 5.5f, 0.62f, 1.40f}, {0.0f, 9.6f, 1.67f, 1.94f}, {0.0f, 5.7f, 1.15f, 1.37f},
-      {0.0f, 9.3f, 1.22f, 1.35f}},
+     {{0.0f, 5.8f, 1.03f, 1.31f}, {0.0f, 9.5f, 1.66f, 1.96f}, {0.0f, 6.9f, 0.20f, 1.22f},
+      {0.0f, 9.0f, 0.46f, 1.18f}},
      "tile 256x256"},
     {192, 256,
-     {{0.0f, 4.4f, 0.14f, 1.25f}, {0.0f, 7.9f, 0.25f, 1.55f}, {0.0f, 4.7f, 1.12f, 1.14f}, {}},
+     {{0.0f, 4.6f, 1.15f, 1.15f}, {0.0f, 7.8f, 0.43f, 1.54f}, {0.0f, 6.1f, 0.23f, 0.94f}, {}},
      "tile 192x256"},
-    {128, 256, {{}, {}, {0.0f, 3.8f, 0.97f, 0.98f}, {0.0f, 6.6f, 0.87f, 0.89f}}, "tile 128x256"},
+    {128, 256, {{}, {}, {0.0f, 5.0f, 0.03f, 0.73f}, {0.0f, 6.3f, 0.79f, 0.80f}}, "tile 128x256"},
     {128, 128,
-     {{1.2f, 2.1f, 0.75f, 0.57f}, {2.0f, 3.1f, 0.71f, 0.65f}, {}, {3.0f, 2.6f, 0.65f, 0.53f}},
+     {{1.8f, 1.8f, 0.60f, 0.51f}, {2.2f, 3.0f, 0.62f, 0.60f}, {}, {2.3f, 2.8f, 0.59f, 0.51f}},
      "tile 128x128"},
     {128, 128,
-     {{0.5f, 4.6f, 0.43f, 0.64f}, {0.1f, 6.5f, 0.51f, 0.64f}, {}, {1.1f, 5.8f, 0.47f, 0.59f}},
+     {{0.1f, 4.7f, 0.27f, 0.54f}, {0.1f, 6.5f, 0.59f, 0.59f}, {0.0f, 5.4f, 0.44f, 0.46f},
+      {0.0f, 6.6f, 0.45f, 0.47f}},
      "tile 128x128 k2"},
     {64, 128,
-     {{3.0f, 0.60f, 0.39f, 0.39f}, {2.9f, 1.7f, 0.08f, 0.39f}, {2.5f, 1.1f, 0.38f, 0.37f},
-      {2.5f, 1.8f, 0.46f, 0.36f}},
+     {{2.9f, 0.53f, 0.39f, 0.39f}, {2.7f, 1.8f, 0.40f, 0.38f}, {2.7f, 0.94f, 0.37f, 0.36f},
+      {2.7f, 1.8f, 0.43f, 0.38f}},
      "tile 64x128"},
     {64, 64,
-     {{3.1f, 0.11f, 0.28f, 0.25f}, {3.2f, 0.73f, 0.27f, 0.25f}, {3.1f, 0.21f, 0.29f, 0.27f},
-      {3.0f, 0.81f, 0.37f, 0.27f}},
+     {{3.1f, 0.11f, 0.28f, 0.25f}, {3.1f, 0.74f, 0.27f, 0.25f}, {3.1f, 0.21f, 0.29f, 0.26f},
+      {2.8f, 0.89f, 0.36f, 0.27f}},
      "tile 64x64"},
     {32, 64,
-     {{3.3f, 0.10f, 0.09f, 0.18f}, {3.4f, 0.51f, 0.18f, 0.17f}, {3.3f, 0.18f, 0.24f, 0.20f}, {}},
+     {{3.2f, 0.12f, 0.16f, 0.18f}, {3.4f, 0.50f, 0.18f, 0.17f}, {3.4f, 0.09f, 0.24f, 0.21f}, {}},
      "tile 32x64"},
-    {32, 64, {{}, {}, {1.7f, 2.9f, 0.19f, 0.20f}, {}}, "tile 32x64 k4"},
-    {32, 32, {{3.1f, 0.73f, 0.05f, 0.09f}, {3.0f, 0.92f, 0.10f, 0.09f}, {}, {}}, "tile 32x32 k2"},
+    {32, 64, {{}, {}, {1.8f, 2.8f, 0.14f, 0.20f}, {}}, "tile 32x64 k4"},
+    {32, 32, {{2.9f, 0.75f, 0.10f, 0.10f}, {3.0f, 0.91f, 0.10f, 0.09f}, {}, {}}, "tile 32x32 k2"},
 };
 
 inline long long up(long long a, long long b) { return (a + b - 1) / b; }
@@ -140,19 +141,17 @@ inline void launch_tiles(const Problem& p, const Plan& plan, const Epi& epi, hip
   using std::integer_sequence;
   constexpr bool kIn = kL == kInner, kB = kL == kOuterB, kBoth = kL == kOuterBoth;
   switch (plan.tile) {  // (as kTileCosts has them)
-    case 0: return go(integer_sequence<int, 256, 256, 2, 4, 2>{});
+    case 0: return go(integer_sequence<int, 256, 256, 2, 4, 2, 1, 1>{});
     case 1:
-      if constexpr (!kBoth) go(integer_sequence<int, 192, 256, 2, 4, 2>{});
+      if constexpr (!kBoth) go(integer_sequence<int, 192, 256, 2, 4, 2, 1, 1>{});
       return;
     case 2:
-      if constexpr (!kIn) go(integer_sequence<int, 128, 256, 2, 4, 2>{});
+      if constexpr (!kIn) go(integer_sequence<int, 128, 256, 2, 4, 2, 1, 1>{});
       return;
     case 3:
-      if constexpr (!kB) go(integer_sequence<int, 128, 128, 2, 2, 2>{});
+      if constexpr (!kB) go(integer_sequence<int, 128, 128, 2, 2, 2, 1, 1>{});
       return;
-    case 4:
-      if constexpr (!kB) go(integer_sequence<int, 128, 128, 2, 2, 2, 2>{});
-      return;
+    case 4: return go(integer_sequence<int, 128, 128, 2, 2, 2, 2, 1>{});
     case 5: return go(integer_sequence<int, 64, 128, 1, 4, 3>{});
     case 6: return go(integer_sequence<int, 64, 64, 2, 2, 3>{});
     case 7:

@@ -680,8 +680,13 @@ int moe_rmsnorm_bwd_i8(const void *dout, int dout_dtype, const int8_t *codes,
  * T * K and T * N below 2^34.
  * ws / ws_bytes: at least moe_linear_i8_ws_bytes(T, N, K, x_scales != NULL),
  * 256-byte aligned, no contents carried between calls.
+ * moe_linear_i8_kernel: the kernel that these sizes run, for tests and
+ * profiles: "direct" (few tokens: weights straight to registers), "tile
+ * 128x256" (tokens x features of a block; "k2": waves that share k); "" where
+ * nothing runs.
  * ------------------------------------------------------------------- */
 size_t moe_linear_i8_ws_bytes(int T, int N, int K, int x_quantized);
+const char *moe_linear_i8_kernel(int T, int N, int K);
 int moe_linear_i8(const void *x, const float *x_scales, int T, int N, int K,
                   const int8_t *codes, const float *scales, const float *bias,
                   void *out, int out_dtype, void *ws, size_t ws_bytes,
@@ -706,7 +711,19 @@ int moe_linear_i8(const void *x, const float *x_scales, int T, int N, int K,
  * T * d below 2^34, T * f below 2^33.  ws / ws_bytes: at least the query's
  * bytes (dout_dtype, x_scales != NULL, gate_up != NULL), 256-byte aligned, no
  * contents carried between calls.
+ * moe_gated_ffn_kernel: the kernel that a product of these sizes runs, named as
+ * by moe_linear_i8_kernel; "split tile ..": k is split over blocks and a second
+ * kernel joins their sums.
  * ------------------------------------------------------------------- */
+enum {
+  MOE_GATED_GATE_UP = 0,   /* x Wgu^T and the activation */
+  MOE_GATED_DOWN = 1,      /* h Wd^T */
+  MOE_GATED_DH = 2,        /* dout Wd, and dg, du, h */
+  MOE_GATED_DX = 3,        /* [dg du] Wgu */
+  MOE_GATED_DW_GATE_UP = 4, /* [dg du]^T x */
+  MOE_GATED_DW_DOWN = 5    /* dout^T h */
+};
+const char *moe_gated_ffn_kernel(int product, int T, int d, int f);
 size_t moe_gated_ffn_ws_bytes(int T, int d, int f);
 int moe_gated_ffn(const void *x_bf16, const void *w_gate_up_bf16,
                   const void *w_down_bf16, int T, int d, int f, void *out,

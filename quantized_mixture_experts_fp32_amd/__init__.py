@@ -44,8 +44,9 @@ EXPORTS = ("moe_status_str", "moe_last_error", "moe_route_ws_bytes", "moe_route"
            "moe_rmsnorm_bwd_ws_bytes", "moe_rmsnorm_bwd", "moe_combine_residual",
            "moe_combine_residual_bwd_ws_bytes", "moe_combine_residual_bwd", "moe_dispatch",
            "moe_dispatch_bwd", "moe_combine_bwd", "moe_quantize_i8", "moe_dequantize_i8",
-           "moe_rmsnorm_i8", "moe_rmsnorm_bwd_i8", "moe_linear_i8_ws_bytes", "moe_linear_i8",
-           "moe_gated_ffn_ws_bytes", "moe_gated_ffn", "moe_gated_ffn_bwd_ws_bytes",
+           "moe_rmsnorm_i8", "moe_rmsnorm_bwd_i8", "moe_linear_i8_ws_bytes",
+           "moe_linear_i8_kernel", "moe_linear_i8", "moe_gated_ffn_ws_bytes",
+           "moe_gated_ffn_kernel", "moe_gated_ffn", "moe_gated_ffn_bwd_ws_bytes",
            "moe_gated_ffn_bwd")
 
 
@@ -135,6 +136,10 @@ def load_library():
     lib.moe_rmsnorm_i8.argtypes = [vp, vp, vp, i32, i32, f32, vp, i32, vp]
     lib.moe_rmsnorm_bwd_i8.argtypes = [vp, i32, vp, vp, vp, vp, i32, i32, f32, vp, i32, vp, vp,
                                        sz, vp]
+    lib.moe_linear_i8_kernel.argtypes = [i32] * 3
+    lib.moe_linear_i8_kernel.restype = ctypes.c_char_p
+    lib.moe_gated_ffn_kernel.argtypes = [i32] * 4
+    lib.moe_gated_ffn_kernel.restype = ctypes.c_char_p
     lib.moe_linear_i8_ws_bytes.argtypes, lib.moe_linear_i8_ws_bytes.restype = [i32] * 4, sz
     lib.moe_linear_i8.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp, i32, vp, sz, vp]
     lib.moe_gated_ffn_ws_bytes.argtypes, lib.moe_gated_ffn_ws_bytes.restype = [i32] * 3, sz
@@ -1057,6 +1062,11 @@ def moe_linear_i8_ws_bytes(T, N, K, x_quantized=False):
     return int(load_library().moe_linear_i8_ws_bytes(T, N, K, x_quantized))
 
 
+def moe_linear_i8_kernel(T, N, K):
+    """The kernel that moe_linear_i8 runs at these sizes ("" where nothing runs)."""
+    return load_library().moe_linear_i8_kernel(T, N, K).decode()
+
+
 @_on_device
 def moe_linear_i8(x, codes, scales, bias=None, out=None, out_dtype=MOE_OUT_BF16, ws=None,
                   x_scales=None):
@@ -1108,6 +1118,18 @@ def _gated_weights(fn, w_gate_up, w_down, d, like):
 
 def moe_gated_ffn_ws_bytes(T, d, f):
     return int(load_library().moe_gated_ffn_ws_bytes(T, d, f))
+
+
+GATED_PRODUCTS = ("gate_up", "down", "dh", "dx", "dw_gate_up", "dw_down")
+
+
+def moe_gated_ffn_kernel(product, T, d, f):
+    """The kernel that a product of the block (one of GATED_PRODUCTS) runs at these
+    sizes ("" where nothing runs)."""
+    if product not in GATED_PRODUCTS:
+        raise ValueError(f"moe_gated_ffn_kernel: product {product!r} is none of {GATED_PRODUCTS}")
+    at = GATED_PRODUCTS.index(product)
+    return load_library().moe_gated_ffn_kernel(at, T, d, f).decode()
 
 
 @_on_device

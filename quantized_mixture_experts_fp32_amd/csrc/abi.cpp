@@ -866,6 +866,12 @@ size_t moe_linear_i8_ws_bytes(int T, int N, int K, int x_quantized) {
   return moe::linear_i8_ws_bytes(T, N, K, !x_quantized);
 }
 
+const char* moe_linear_i8_kernel(int T, int N, int K) {
+  int status;
+  if (T == 0 || linear_i8_refusal(T, N, K, &status)) return "";
+  return moe::product_i8_name(T, N, K);
+}
+
 int moe_linear_i8(const void* x, const float* x_scales, int T, int N, int K, const int8_t* codes,
                   const float* scales, const float* bias, void* out, int out_dtype, void* ws,
                   size_t ws_bytes, void* stream) {
@@ -902,6 +908,12 @@ size_t moe_gated_ffn_ws_bytes(int T, int d, int f) {
   int status;
   if (T == 0 || gated_refusal(T, d, f, &status)) return 0;
   return moe::gated_ffn_ws_bytes(T, d, f);
+}
+
+const char* moe_gated_ffn_kernel(int product, int T, int d, int f) {
+  int status;
+  if (T == 0 || gated_refusal(T, d, f, &status)) return "";
+  return moe::gated_ffn_kernel(product, T, d, f);
 }
 
 int moe_gated_ffn(const void* x_bf16, const void* w_gate_up_bf16, const void* w_down_bf16, int T,

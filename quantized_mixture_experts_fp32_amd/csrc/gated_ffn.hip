@@ -12,6 +12,7 @@
 //   dx = [dg du] Wgu,  dWgu = [dg du]^T x,  dWd = dout^T h
 // dg, du and h are rounded to bf16, the matrix cores' operand type; all sums are
 // fp32 in a fixed order, and g and u that are computed again stay fp32.
+#include "moe_wq.h"
 #include "mm_launch.hpp"
 
 namespace moe {
@@ -101,6 +102,18 @@ Operand pairs(const uint16_t* w, int d, int f) {
 
 size_t gated_ffn_ws_bytes(int T, int d, int f) {
   return round_up(2 * (size_t)T * f);
+}
+
+const char* gated_ffn_kernel(int product, int T, int d, int f) {
+  switch (product) {
+    case MOE_GATED_GATE_UP: return product_name(kInner, false, T, f, d, 2LL * d, true);
+    case MOE_GATED_DOWN: return product_name(kInner, false, T, d, f, 2LL * f, false);
+    case MOE_GATED_DH: return product_name(kOuterB, false, T, f, d, 0, false);
+    case MOE_GATED_DX: return product_name(kOuterB, false, T, d, 2LL * f, 0, false);
+    case MOE_GATED_DW_GATE_UP: return product_name(kOuterBoth, false, 2LL * f, d, T, 0, false);
+    case MOE_GATED_DW_DOWN: return product_name(kOuterBoth, false, d, f, T, 0, false);
+  }
+  return "";
 }
 
 hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* w_gate_up, const uint16_t* w_down,

@@ -204,14 +204,22 @@ hipError_t launch_quantize_i8(const void* x, int x_f32, int T, int K, int by_row
 hipError_t launch_dequantize_i8(const int8_t* codes, const float* scales, int T, int K, int by_row,
                                 void* out, int out_f32, hipStream_t s);
 
-// Linear map in 8-bit integers (linear_i8.hip).  x_scales null: x is bf16 and
-// quantised by row into ws.
+// Linear map in 8-bit integers (quant_i8.hip).  x_scales null: x is bf16 and
+// quantised by row, into ws or (product_i8_quantizes) on its way into the product.
 size_t linear_i8_ws_bytes(int T, int N, int K, int x_bf16);
 hipError_t launch_linear_i8(const void* x, const float* x_scales, int T, int N, int K,
                             const int8_t* codes, const float* scales, const float* bias, void* out,
                             int out_f32, void* ws, hipStream_t s);
 
+// Its product (linear_i8.hip, libmoe_wq_i8.so).
+bool product_i8_quantizes(int T, int N, int K);
+const char* product_i8_name(int T, int N, int K);  // the chosen kernel's name
+hipError_t launch_product_i8(const void* x, const float* x_scales, int T, int N, int K,
+                             const int8_t* codes, const float* scales, const float* bias,
+                             void* out, int out_f32, hipStream_t s);
+
 // Gated feed-forward block and its gradient (gated_ffn.hip).
+const char* gated_ffn_kernel(int product, int T, int d, int f);  // (MOE_GATED_..)
 size_t gated_ffn_ws_bytes(int T, int d, int f);
 hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* w_gate_up, const uint16_t* w_down,
                             int T, int d, int f, void* out, int out_f32, uint16_t* gate_up,

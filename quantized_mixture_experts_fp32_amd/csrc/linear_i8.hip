@@ -3,6 +3,11 @@
 //   out[t][n] = sx[t] sw[n] sum_k qx[t][k] qw[n][k] + bias[n]
 // The sum is exact in int32 (K below 2^17); the scales' product, its product
 // with the sum and the bias are fp32, rounded once on store.
+//
+// A library of its own (libmoe_wq_i8.so), which libmoe_wq.so is linked to: its
+// matrix instruction, 16 x 16 x 64, multiplies twice as fast as the one of 16 x
+// 16 x 32, the widest that the check of libmoe_wq.so's waits knows (2501 x 4096 x
+// 4096: 65 -> 45 us); its own waits have a check of their own.
 #include "mm_launch.hpp"
 
 namespace moe {
@@ -29,33 +34,25 @@ struct ScaleStore {
   }
 };
 
-size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
-
 }  // namespace
 
-size_t linear_i8_ws_bytes(int T, int N, int K, int x_bf16) {
-  if (!x_bf16 || (T <= kQuantRows && direct_applies(T, N, K, false))) return 0;
-  return round_up((size_t)T * K) + round_up(4 * (size_t)T);
+hipError_t launch_product_i8(const void* x, const float* x_scales, int T, int N, int K,
+                             const int8_t* codes, const float* scales, const float* bias,
+                             void* out, int out_f32, hipStream_t s) {
+  const ScaleStore epi = {x_scales, scales, bias, out, N, out_f32};
+  if (!x_scales)
+    return launch_direct<I8, false, true>(
+        {(const char*)x, (const char*)codes, 2LL * K, K, T, N, K, 0}, epi, s);
+  const Operand a = {(const char*)x, nullptr, K, T}, b = {(const char*)codes, nullptr, K, N};
+  return launch_product<I8, kInner, false>(a, b, T, N, K, 1, epi, nullptr, s);
 }
 
-hipError_t launch_linear_i8(const void* x, const float* x_scales, int T, int N, int K,
-                            const int8_t* codes, const float* scales, const float* bias, void* out,
-                            int out_f32, void* ws, hipStream_t s) {
-  if (!x_scales && T <= kQuantRows && direct_applies(T, N, K, false))
-    return launch_direct<I8, false, true>(
-        {(const char*)x, (const char*)codes, 2LL * K, K, T, N, K, 0},
-        ScaleStore{nullptr, scales, bias, out, N, out_f32}, s);
-  if (!x_scales) {
-    int8_t* q = (int8_t*)ws;
-    float* sx = (float*)((char*)ws + round_up((size_t)T * K));
-    const hipError_t e = launch_quantize_i8(x, 0, T, K, 1, q, sx, s);
-    if (e != hipSuccess) return e;
-    x = q;
-    x_scales = sx;
-  }
-  const Operand a = {(const char*)x, nullptr, K, T}, b = {(const char*)codes, nullptr, K, N};
-  return launch_product<I8, kInner, false>(
-      a, b, T, N, K, 1, ScaleStore{x_scales, scales, bias, out, N, out_f32}, nullptr, s);
+const char* product_i8_name(int T, int N, int K) {
+  return product_name(kInner, true, T, N, K, K, false);
+}
+
+bool product_i8_quantizes(int T, int N, int K) {
+  return T <= kQuantRows && direct_applies(T, N, K, false);
 }
 
 }  // namespace moe

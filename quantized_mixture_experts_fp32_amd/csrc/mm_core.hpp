@@ -193,11 +193,9 @@ struct I8 {
   typedef int32_t Value;
   typedef i32x4 Acc;
   typedef i32x8 Acc8;
-  // two instructions of 32 bytes of k: both operands give them in the same order
-  static __device__ __forceinline__ i32x4 mma(u32x4 a, u32x4 b, i32x4 c) {
-    const u64x2 x = __builtin_bit_cast(u64x2, a), y = __builtin_bit_cast(u64x2, b);
-    c = __builtin_amdgcn_mfma_i32_16x16x32_i8((long)x[0], (long)y[0], c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_i32_16x16x32_i8((long)x[1], (long)y[1], c, 0, 0, 0);
+  static __device__ __forceinline__ Acc mma(u32x4 a, u32x4 b, Acc c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                                 __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
   }
 };
 

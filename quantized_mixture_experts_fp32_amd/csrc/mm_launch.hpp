@@ -18,47 +18,51 @@ enum Layout { kInner, kOuterB, kOuterBoth };
 //   fixed + block * n + stages * max(one, each * n)
 // for n blocks a CU and stages of 128 bytes (or 64 rows) of k; one: the latency
 // of a stage where a block is alone on its CU, each: its share of a full CU.
-// Fitted by kind of product to 140 random sizes each (1 to 8192 rows, 64 to 50304
-// columns, k 8 to 8192); on 80 others the choice took 1 % (bf16) and 2 % (int8)
-// longer than the fastest of 13 tiles on average, 33 % at most
+// Fitted by kind of product to 140 to 180 random sizes each (1 to 8192 rows, 64
+// to 50304 columns, k 8 to 8192); on 55 others of each kind the choice took 0.3 %
+// (outer B) to 1.3 % (inner bf16) longer than the fastest of 13 tiles on average,
+// 18 % at most; with both outer 4 % and 33 %, before k is split over blocks
 // (profiles/product_choice.txt).
 struct TileCost {
   int bm, bn;
   struct {
     float fixed, block, one, each;  // all 0: not built
   } of[4];  // inner bf16, inner int8, outer B, both outer
-  const char* name;
+  const char* name;  // behind the prefix of one whose k is split over blocks
 };
+constexpr int kSplitPrefix = 6;  // "split "
 constexpr int kTileKernels = 10;
 const TileCost kTileCosts[kTileKernels] = {
     {256, 256,
-     {{0.0f, 5.8f, 1.03f, 1.31f}, {0.0f, 9.5f, 1.66f, 1.96f}, {0.0f, 6.9f, 0.20f, 1.22f},
+     {{0.0f, 5.8f, 1.03f, 1.31f}, {0.0f, 8.5f, 1.17f, 1.22f}, {0.0f, 6.9f, 0.20f, 1.22f},
       {0.0f, 9.0f, 0.46f, 1.18f}},
-     "tile 256x256"},
+     "split tile 256x256"},
     {192, 256,
-     {{0.0f, 4.6f, 1.15f, 1.15f}, {0.0f, 7.8f, 0.43f, 1.54f}, {0.0f, 6.1f, 0.23f, 0.94f}, {}},
-     "tile 192x256"},
-    {128, 256, {{}, {}, {0.0f, 5.0f, 0.03f, 0.73f}, {0.0f, 6.3f, 0.79f, 0.80f}}, "tile 128x256"},
+     {{0.0f, 4.6f, 1.15f, 1.15f}, {0.0f, 7.1f, 0.32f, 1.08f}, {0.0f, 6.1f, 0.23f, 0.94f}, {}},
+     "split tile 192x256"},
+    {128, 256,
+     {{}, {0.0f, 5.7f, 0.89f, 0.90f}, {0.0f, 5.0f, 0.03f, 0.73f}, {0.0f, 6.3f, 0.79f, 0.80f}},
+     "split tile 128x256"},
     {128, 128,
-     {{1.8f, 1.8f, 0.60f, 0.51f}, {2.2f, 3.0f, 0.62f, 0.60f}, {}, {2.3f, 2.8f, 0.59f, 0.51f}},
-     "tile 128x128"},
+     {{1.8f, 1.8f, 0.60f, 0.51f}, {0.9f, 3.5f, 0.56f, 0.53f}, {}, {2.3f, 2.8f, 0.59f, 0.51f}},
+     "split tile 128x128"},
     {128, 128,
-     {{0.1f, 4.7f, 0.27f, 0.54f}, {0.1f, 6.5f, 0.59f, 0.59f}, {0.0f, 5.4f, 0.44f, 0.46f},
+     {{0.1f, 4.7f, 0.27f, 0.54f}, {0.0f, 5.6f, 0.49f, 0.52f}, {0.0f, 5.4f, 0.44f, 0.46f},
       {0.0f, 6.6f, 0.45f, 0.47f}},
-     "tile 128x128 k2"},
+     "split tile 128x128 k2"},
     {64, 128,
-     {{2.9f, 0.53f, 0.39f, 0.39f}, {2.7f, 1.8f, 0.40f, 0.38f}, {2.7f, 0.94f, 0.37f, 0.36f},
+     {{2.9f, 0.53f, 0.39f, 0.39f}, {2.3f, 1.7f, 0.08f, 0.38f}, {2.7f, 0.94f, 0.37f, 0.36f},
       {2.7f, 1.8f, 0.43f, 0.38f}},
-     "tile 64x128"},
+     "split tile 64x128"},
     {64, 64,
-     {{3.1f, 0.11f, 0.28f, 0.25f}, {3.1f, 0.74f, 0.27f, 0.25f}, {3.1f, 0.21f, 0.29f, 0.26f},
+     {{3.1f, 0.11f, 0.28f, 0.25f}, {2.9f, 0.70f, 0.25f, 0.25f}, {3.1f, 0.21f, 0.29f, 0.26f},
       {2.8f, 0.89f, 0.36f, 0.27f}},
-     "tile 64x64"},
+     "split tile 64x64"},
     {32, 64,
-     {{3.2f, 0.12f, 0.16f, 0.18f}, {3.4f, 0.50f, 0.18f, 0.17f}, {3.4f, 0.09f, 0.24f, 0.21f}, {}},
-     "tile 32x64"},
-    {32, 64, {{}, {}, {1.8f, 2.8f, 0.14f, 0.20f}, {}}, "tile 32x64 k4"},
-    {32, 32, {{2.9f, 0.75f, 0.10f, 0.10f}, {3.0f, 0.91f, 0.10f, 0.09f}, {}, {}}, "tile 32x32 k2"},
+     {{3.2f, 0.12f, 0.16f, 0.18f}, {3.1f, 0.47f, 0.15f, 0.17f}, {3.4f, 0.09f, 0.24f, 0.21f}, {}},
+     "split tile 32x64"},
+    {32, 64, {{}, {}, {1.8f, 2.8f, 0.14f, 0.20f}, {}}, "split tile 32x64 k4"},
+    {32, 32, {{2.9f, 0.75f, 0.10f, 0.10f}, {2.8f, 0.91f, 0.10f, 0.09f}, {}, {}}, "split tile 32x32 k2"},
 };
 
 inline long long up(long long a, long long b) { return (a + b - 1) / b; }
@@ -93,6 +97,14 @@ inline Plan plan_product(Layout l, bool i8, long long M, long long N, int stages
     }
   }
   return best;
+}
+
+// The kernel that a product runs: "direct", a tile's name, "split ..".
+inline const char* product_name(Layout l, bool i8, long long M, long long N, long long k,
+                                long long b_stride, bool pair) {
+  if (l == kInner && direct_applies(M, N, b_stride, pair)) return "direct";
+  const Plan p = plan_product(l, i8, M, pair ? 2 * N : N, (int)up(k * (i8 ? 1 : 2), kStageBytes));
+  return kTileCosts[p.tile].name + (p.splits > 1 ? 0 : kSplitPrefix);
 }
 
 // Workspace of a product over tokens (both operands outer).
@@ -146,7 +158,8 @@ inline void launch_tiles(const Problem& p, const Plan& plan, const Epi& epi, hip
       if constexpr (!kBoth) go(integer_sequence<int, 192, 256, 2, 4, 2, 1, 1>{});
       return;
     case 2:
-      if constexpr (!kIn) go(integer_sequence<int, 128, 256, 2, 4, 2, 1, 1>{});
+      if constexpr (!kIn || std::is_same_v<Mma, I8>)
+        go(integer_sequence<int, 128, 256, 2, 4, 2, 1, 1>{});
       return;
     case 3:
       if constexpr (!kB) go(integer_sequence<int, 128, 128, 2, 2, 2, 1, 1>{});

@@ -147,4 +147,25 @@ hipError_t launch_dequantize_i8(const int8_t* codes, const float* scales, int T,
   return hipGetLastError();
 }
 
+static size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
+
+size_t linear_i8_ws_bytes(int T, int N, int K, int x_bf16) {
+  if (!x_bf16 || product_i8_quantizes(T, N, K)) return 0;
+  return round_up((size_t)T * K) + round_up(4 * (size_t)T);
+}
+
+hipError_t launch_linear_i8(const void* x, const float* x_scales, int T, int N, int K,
+                            const int8_t* codes, const float* scales, const float* bias, void* out,
+                            int out_f32, void* ws, hipStream_t s) {
+  if (!x_scales && !product_i8_quantizes(T, N, K)) {
+    int8_t* q = (int8_t*)ws;
+    float* sx = (float*)((char*)ws + round_up((size_t)T * K));
+    const hipError_t e = launch_quantize_i8(x, 0, T, K, 1, q, sx, s);
+    if (e != hipSuccess) return e;
+    x = q;
+    x_scales = sx;
+  }
+  return launch_product_i8(x, x_scales, T, N, K, codes, scales, bias, out, out_f32, s);
+}
+
 }  // namespace moe

@@ -11,6 +11,7 @@ import torch
 
 import i8_gated_ref as ref
 import quantized_mixture_experts_fp32_amd as moe
+from i8_gated_sizes import GATED, LINEAR
 
 FAKE = ctypes.c_void_p(0x10000)
 ODD = ctypes.c_void_p(0x10002)
@@ -222,3 +223,33 @@ def test_layer_refuses_two_adds():
     layer.d, layer.wr = 128, torch.zeros(8, 128)
     with pytest.raises(ValueError, match="shared and add"):
         layer.forward_block(torch.zeros(4, 128), add=torch.zeros(4, 128), shared=object())
+
+
+# ------------------------------------------------------------ the kernels' names
+@pytest.mark.parametrize("product,name", [(p, n) for p in GATED for n in GATED[p]])
+def test_kernel_of_the_block(lib, product, name):
+    assert moe.moe_gated_ffn_kernel(product, *GATED[product][name]) == name
+
+
+@pytest.mark.parametrize("name", LINEAR)
+def test_kernel_of_the_linear_map(lib, name):
+    assert moe.moe_linear_i8_kernel(*LINEAR[name]) == name
+
+
+def test_no_other_kernel_is_chosen(lib):
+    """Over many sizes, every choice is one that a GPU test reaches."""
+    rng = np.random.default_rng(5)
+    for T, d, f in np.exp2(rng.uniform(0, [14, 13, 13], (3000, 3))).astype(int).tolist():
+        d, f = -(-d // 8) * 8, -(-f // 8) * 8
+        for p in GATED:
+            assert moe.moe_gated_ffn_kernel(p, T, d, f) in GATED[p], (p, T, d, f)
+        assert moe.moe_linear_i8_kernel(T, 4 * d, 2 * f) in LINEAR, (T, d, f)
+
+
+def test_no_kernel(lib):
+    assert moe.moe_linear_i8_kernel(0, 64, 64) == "" == moe.moe_linear_i8_kernel(4, 64, 8)
+    assert moe.moe_gated_ffn_kernel("dx", 0, 64, 64) == ""
+    assert moe.moe_gated_ffn_kernel("dx", 4, 64, 12) == ""
+    assert lib.moe_gated_ffn_kernel(6, 4, 64, 64) == b"" == lib.moe_gated_ffn_kernel(-1, 4, 64, 64)
+    with pytest.raises(ValueError, match="none of"):
+        moe.moe_gated_ffn_kernel("up", 4, 64, 64)

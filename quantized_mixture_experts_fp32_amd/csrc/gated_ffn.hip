@@ -53,16 +53,29 @@ struct Store {
 };
 
 // dh -> dg, du and h.
+template <bool kGuF32>
 struct GatedBwdStore {
   const void* gate_up;
-  int gu_f32;
   uint16_t* dgu;
   uint16_t* h;
   int f;
-  __device__ __forceinline__ void operator()(int m, int n, f32x8 dh) const {
+  struct Ahead {
+    static constexpr int kRegs = kGuF32 ? 16 : 8;
+    row::Raw8<kGuF32> g, u;
+  };
+  struct Columns {};
+  __device__ __forceinline__ Columns columns(int) const { return {}; }
+  __device__ __forceinline__ Ahead ahead(int m, int n) const {
     const size_t at = (size_t)m * (2 * f) + n;
-    const f32x8 g = load_as<f32x8>(gate_up, gu_f32, at);
-    const f32x8 u = load_as<f32x8>(gate_up, gu_f32, at + f);
+    Ahead a;
+    a.g.load(gate_up, at);
+    a.u.load(gate_up, at + f);
+    return a;
+  }
+  __device__ __forceinline__ void operator()(int m, int n, f32x8 dh, Columns,
+                                             const Ahead& kept) const {
+    const size_t at = (size_t)m * (2 * f) + n;
+    const f32x8 g = kept.g.get(), u = kept.u.get();
     f32x8 dg, du, hv;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -164,8 +177,6 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
   void* part = place(at.part);
   const uint16_t* x = (const uint16_t*)a.x;
   const uint16_t* dout = (const uint16_t*)a.dout;
-  const void* gate_up = a.gate_up;
-  const int gu_f32 = !gate_up;
   hipError_t e = hipSuccess;
   if (T > 0) {
     if (a.do_f32) {
@@ -175,20 +186,24 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
       if ((e = hipGetLastError()) != hipSuccess) return e;
       dout = place(at.dout);
     }
-    if (a.x_scales && (!gate_up || a.dw_gate_up)) {
+    if (a.x_scales && (!a.gate_up || a.dw_gate_up)) {
       e = launch_dequantize_i8((const int8_t*)a.x, a.x_scales, T, d, 0, place(at.x), 0, s);
       if (e != hipSuccess) return e;
       x = place(at.x);
     }
-    if (!gate_up) {
+    if (!a.gate_up) {
       e = launch_product<Bf16, kInner, true>(
           rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d, 2,
           GatedStore{nullptr, place(at.gate_up), 1, f}, part, s);
       if (e != hipSuccess) return e;
-      gate_up = place(at.gate_up);
     }
-    e = launch_product<Bf16, kOuterB, false>(rows(dout, d, T), rows(a.w_down, f, f), T, f, d,
-                                                 2, GatedBwdStore{gate_up, gu_f32, dgu, h, f}, part, s);
+    const Operand m = rows(dout, d, T), w = rows(a.w_down, f, f);
+    if (a.gate_up)
+      e = launch_product<Bf16, kOuterB, false>(
+          m, w, T, f, d, 2, GatedBwdStore<false>{a.gate_up, dgu, h, f}, nullptr, s);
+    else
+      e = launch_product<Bf16, kOuterB, false>(
+          m, w, T, f, d, 2, GatedBwdStore<true>{place(at.gate_up), dgu, h, f}, nullptr, s);
     if (e != hipSuccess) return e;
     if (a.dx) {
       e = launch_product<Bf16, kOuterB, false>(rows(dgu, 2 * f, T), rows(a.w_gate_up, d, d), T,

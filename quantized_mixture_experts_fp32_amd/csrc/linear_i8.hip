@@ -21,15 +21,33 @@ struct ScaleStore {
   void* out;
   long long N;
   int f32;
-  template <typename I>
-  __device__ __forceinline__ void operator()(int m, int n, I a) const {
-    typedef std::conditional_t<sizeof(I) == 32, f32x8, f32x4> V;
-    const float s = sx[m];
-    const V w = load_as<V>(sw, 1, n);
+  struct Columns {
+    f32x8 w, b;
+  };
+  struct Ahead {
+    static constexpr int kRegs = 1;
+    float s;
+  };
+  __device__ __forceinline__ Columns columns(int n) const { return {load_as<f32x8>(sw, 1, n), bias_at<f32x8>(n)}; }
+  __device__ __forceinline__ Ahead ahead(int m, int) const { return {sx[m]}; }
+  __device__ __forceinline__ void operator()(int m, int n, i32x8 a, const Columns& c,
+                                             const Ahead& r) const {
+    put(m, n, a, r.s, c.w, c.b);
+  }
+  // (the kernel for few tokens: four columns, read in place)
+  __device__ __forceinline__ void operator()(int m, int n, i32x4 a) const {
+    put(m, n, a, sx[m], load_as<f32x4>(sw, 1, n), bias_at<f32x4>(n));
+  }
+  template <typename V>
+  __device__ __forceinline__ V bias_at(int n) const {
+    return bias ? load_as<V>(bias, 1, n) : V(0.0f);
+  }
+  template <typename I, typename V>
+  __device__ __forceinline__ void put(int m, int n, I a, float s, V w, V b) const {
     V v;
 #pragma unroll
     for (int r = 0; r < (int)(sizeof(I) / 4); ++r) v[r] = (float)a[r] * (s * w[r]);
-    if (bias) v += load_as<V>(bias, 1, n);
+    if (bias) v += b;
     store_as(out, f32, (size_t)m * N + n, v);
   }
 };

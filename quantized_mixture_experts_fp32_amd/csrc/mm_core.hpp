@@ -65,14 +65,21 @@ __device__ __forceinline__ int swizzle(int k) {
   return kF >= 8 ? 0 : (((k >> 3) & (8 / kF - 1)) * 2 * kF) & (kRows / 8 - 1);
 }
 
+// Rows of a K-inner tile that its waves load in whole instructions, eight rows
+// each; those past the tile are out of range and cost no traffic.
+constexpr int whole_loads(int rows, int waves) {
+  return (rows + 8 * waves - 1) / (8 * waves) * (8 * waves);
+}
+
 // Loader of one operand's stages.  kRows: rows (K-inner) or columns (K-outer)
 // of the tile; kPair: rows of two matrices, interleaved by 16.
 // kGroups: the stages are dealt to so many loaders in turn.
 // kF: fragments of a wave's rows.
 template <bool kOuter, bool kPair, int kRows, int kF, int kWaves, int kGroups>
 struct Loader {
-  static constexpr int kLoads = kRows / 8 / kWaves;  // a wave's loads a stage
-  static_assert(kRows % (8 * kWaves) == 0, "whole loads a wave");
+  static constexpr int kPlaces = whole_loads(kRows, kWaves);  // rows in LDS
+  static constexpr int kLoads = kPlaces / 8 / kWaves;         // a wave's loads a stage
+  static_assert(!kOuter || kRows == kPlaces, "whole loads a wave");
   uint32_t off[kLoads];    // bytes from the stage's base
   const char* base;        // of the next stage
   const char* base2;       // of the second matrix (pair form)
@@ -111,7 +118,7 @@ struct Loader {
       const int r = row_of(j), c = chunk_of(j);
       const int row = kPair ? (r >> 5) * 16 + (r & 15) : r;
       off[j] = (uint32_t)(row * o.stride) + 16 * c;
-      if (row0 + (kOuter ? 8 * c : row) >= o.rows) off[j] = kOutOfRange;
+      if (row0 + (kOuter ? 8 * c : row) >= o.rows || r >= kRows) off[j] = kOutOfRange;
     }
     if (full <= 0) last();
   }
@@ -233,7 +240,8 @@ template <int bm, int bn, int wm, int wn, int stages, int groups = 1, int more =
 struct Shape {
   static constexpr int BM = bm, BN = bn, WM = wm, WN = wn, S = stages, G = groups, SB = S + more;
   static constexpr int kWaves = wm * wn, kThreads = 64 * kWaves * groups;  // waves: of a group
-  static constexpr int kRing = (bm * S + bn * SB) * kStageBytes;
+  static constexpr int kA = whole_loads(bm, kWaves) * kStageBytes, kB = bn * kStageBytes;
+  static constexpr int kRing = kA * S + kB * SB;
   static constexpr int kLds = groups * kRing;
 };
 
@@ -260,14 +268,39 @@ __device__ __forceinline__ void tile_of(int id, int nm, int nn, int& tm, int& tn
   tn = i / rows;
 }
 
+// What an epilogue reads from memory is asked for before the rows are turned
+// around: Epi::Columns by columns(n), once, and Epi::Ahead by ahead(m, n), for a
+// piece of a row; nothing where it has no such types.
+template <typename Epi, typename = void>
+struct ReadAhead {
+  struct Type {};
+  struct Columns {};
+  static __device__ __forceinline__ Type get(const Epi&, int, int) { return {}; }
+  static __device__ __forceinline__ Columns columns(const Epi&, int) { return {}; }
+  static constexpr int kDepth = 0;
+};
+template <typename Epi>
+struct ReadAhead<Epi, std::void_t<typename Epi::Ahead>> {
+  typedef typename Epi::Ahead Type;
+  typedef typename Epi::Columns Columns;
+  static __device__ __forceinline__ Type get(const Epi& epi, int m, int n) {
+    return epi.ahead(m, n);
+  }
+  static __device__ __forceinline__ Columns columns(const Epi& epi, int n) {
+    return epi.columns(n);
+  }
+  static constexpr int kDepth = 64 / Type::kRegs;  // pieces in flight, in 64 registers
+};
+
 // Epi: operator()(m, n, v) for eight consecutive n (N is a multiple of 8; the
 // direct kernel: four), or in the pair form operator()(m, n, first, second).
+// With Epi::Ahead: operator()(m, n, v, columns(n), ahead(m, n)).
 template <typename Mma, typename Sh, bool kAOuter, bool kBOuter, bool kPair, typename Epi>
 __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kernel(
     const Problem p, const Epi epi) {
   extern __shared__ __align__(1024) char lds[];
   constexpr int TM = Sh::BM / Sh::WM, TN = Sh::BN / Sh::WN, MI = TM / 16, NI = TN / 16;
-  constexpr int kA = Sh::BM * kStageBytes, kB = Sh::BN * kStageBytes;
+  constexpr int kA = Sh::kA, kB = Sh::kB;
   const int lane = threadIdx.x & 63;
   const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = id / Sh::kWaves, wave = id % Sh::kWaves;
@@ -409,6 +442,27 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
     }
     asked_a();
   }
+  typedef typename Mma::Acc8 Acc8;
+  constexpr int kRow = TN * 4 + 16, kWidth = kPair ? TN / 2 : TN;  // features of the wave
+  constexpr int kLanes = kWidth / 8, kPass = 64 / kLanes < 16 ? 64 / kLanes : 16;  // rows at a time
+  constexpr int kPasses = (16 + kPass - 1) / kPass, kRounds = MI * kPasses;
+  const int row = lane / kLanes, at = 8 * (lane % kLanes);
+  const int n = (kPair ? n0 / 2 : n0) + wn * kWidth + at;
+  auto row_of = [&](int round) {
+    return m0 + wm * TM +
+           decltype(ra)::row(round / kPasses, round % kPasses * kPass + row);
+  };
+  // what the epilogue reads of the first rounds
+  typedef ReadAhead<Epi> Early;
+  constexpr int kDepth = Early::kDepth < kRounds ? Early::kDepth : kRounds;
+  typename Early::Type early[kDepth ? kDepth : 1];
+  auto fetch = [&](int round) {  // (rows and columns past the end read the last)
+    early[round % (kDepth ? kDepth : 1)] =
+        Early::get(epi, min(row_of(round), p.M - 1), min(n, p.N - 8));
+  };
+#pragma unroll
+  for (int r = 0; r < kDepth; ++r) fetch(r);
+  const typename Early::Columns columns = Early::columns(epi, min(n, p.N - 8));
   // The loads past the end land before the block's LDS is given back, and the
   // sums are formed before the branches below.
   wait_stage<0>();
@@ -440,13 +494,8 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
   // each wave turns its rows around in LDS, 16 at a time, and writes 128 bytes of
   // a row together (64 with TN = 32).
   __syncthreads();  // the last stage has been read (or, of a group, the sums)
-  typedef typename Mma::Acc8 Acc8;
-  constexpr int kRow = TN * 4 + 16, kWidth = kPair ? TN / 2 : TN;  // features of the wave
-  constexpr int kLanes = kWidth / 8, kPass = 64 / kLanes < 16 ? 64 / kLanes : 16;  // rows at a time
   char* const turn = lds + (Sh::G - 1) * (Sh::kWaves * MI * NI * 1024) + wave * (16 * kRow);
   const int col = lane & 15, q = lane >> 4;
-  const int row = lane / kLanes, at = 8 * (lane % kLanes);
-  const int n = (kPair ? n0 / 2 : n0) + wn * kWidth + at;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     char* const to = turn + col * kRow;
@@ -469,15 +518,18 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int r = 0; r < 16; r += kPass) {
-      const int m = m0 + wm * TM + decltype(ra)::row(i, r + row);
-      if (r + row < 16 && m < p.M && n < p.N) {
-        const char* v = turn + (r + row) * kRow + 4 * at;
-        if constexpr (kPair)
+    for (int r = 0; r < kPasses; ++r) {
+      const int round = i * kPasses + r, at_row = r * kPass + row, m = row_of(round);
+      if (at_row < 16 && m < p.M && n < p.N) {
+        const char* v = turn + at_row * kRow + 4 * at;
+        if constexpr (kDepth > 0)
+          epi(m, n, *(const Acc8*)v, columns, early[round % kDepth]);
+        else if constexpr (kPair)
           epi(m, n, *(const Acc8*)v, *(const Acc8*)(v + 4 * kWidth));
         else
           epi(m, n, *(const Acc8*)v);
       }
+      if (kDepth && round + kDepth < kRounds) fetch(round + kDepth);
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();

@@ -31,14 +31,14 @@ struct TileCost {
   const char* name;  // behind the prefix of one whose k is split over blocks
 };
 constexpr int kSplitPrefix = 6;  // "split "
-constexpr int kTileKernels = 10;
+constexpr int kTileKernels = 11;
 const TileCost kTileCosts[kTileKernels] = {
     {256, 256,
      {{0.0f, 5.8f, 1.03f, 1.31f}, {0.0f, 8.5f, 1.17f, 1.22f}, {0.0f, 6.9f, 0.20f, 1.22f},
       {0.0f, 9.0f, 0.46f, 1.18f}},
      "split tile 256x256"},
     {192, 256,
-     {{0.0f, 4.6f, 1.15f, 1.15f}, {0.0f, 7.1f, 0.32f, 1.08f}, {0.0f, 6.1f, 0.23f, 0.94f}, {}},
+     {{0.0f, 5.0f, 0.70f, 1.13f}, {0.0f, 7.1f, 0.32f, 1.08f}, {0.0f, 6.1f, 0.23f, 0.94f}, {}},
      "split tile 192x256"},
     {128, 256,
      {{}, {0.0f, 5.7f, 0.89f, 0.90f}, {0.0f, 5.0f, 0.03f, 0.73f}, {0.0f, 6.3f, 0.79f, 0.80f}},
@@ -63,6 +63,9 @@ const TileCost kTileCosts[kTileKernels] = {
      "split tile 32x64"},
     {32, 64, {{}, {}, {1.8f, 2.8f, 0.14f, 0.20f}, {}}, "split tile 32x64 k4"},
     {32, 32, {{2.9f, 0.75f, 0.10f, 0.10f}, {2.8f, 0.91f, 0.10f, 0.09f}, {}, {}}, "split tile 32x32 k2"},
+    {160, 256,
+     {{0.0f, 4.6f, 0.25f, 1.03f}, {0.0f, 6.6f, 0.95f, 0.96f}, {0.0f, 5.7f, 0.80f, 0.80f}, {}},
+     "split tile 160x256"},
 };
 
 inline long long up(long long a, long long b) { return (a + b - 1) / b; }
@@ -175,6 +178,9 @@ inline void launch_tiles(const Problem& p, const Plan& plan, const Epi& epi, hip
       return;
     case 9:
       if constexpr (kIn) go(integer_sequence<int, 32, 32, 2, 1, 4, 2>{});
+      return;
+    case 10:
+      if constexpr (!kBoth) go(integer_sequence<int, 160, 256, 2, 4, 2, 1, 1>{});
       return;
   }
 }

@@ -706,14 +706,18 @@ int moe_linear_i8(const void *x, const float *x_scales, int T, int N, int K,
  *   x: bf16 [T][d], or (x_scales not NULL) codes of moe_quantize_i8 with
  *     group_size 128, restored and rounded to bf16.
  *   gate_up: as the forward call left it, or NULL: computed again from x.
- * dg, du and h are rounded to bf16 between the products.
+ * dg, du and h are rounded to bf16 between the products.  The sizes and the
+ * outputs that are asked for choose the kernels, and so the order of the fp32
+ * sums: the same call gives the same bits, one for fewer outputs may not.
  * Both require d % 8 == 0, f % 8 == 0, d and f at most 65536, T below 2^23,
  * T * d below 2^34, T * f below 2^33.  ws / ws_bytes: at least the query's
  * bytes (dout_dtype, x_scales != NULL, gate_up != NULL), 256-byte aligned, no
  * contents carried between calls.
  * moe_gated_ffn_kernel: the kernel that a product of these sizes runs, named as
  * by moe_linear_i8_kernel; "split tile ..": k is split over blocks and a second
- * kernel joins their sums.
+ * kernel joins their sums.  all != 0: in a gradient call that asks for all three
+ * outputs (GATE_UP and DH: with gate_up NULL); "joint 32x64 64x64": with others in
+ * one launch, the tile of the first product and that of the others.
  * ------------------------------------------------------------------- */
 enum {
   MOE_GATED_GATE_UP = 0,   /* x Wgu^T and the activation */
@@ -723,7 +727,7 @@ enum {
   MOE_GATED_DW_GATE_UP = 4, /* [dg du]^T x */
   MOE_GATED_DW_DOWN = 5    /* dout^T h */
 };
-const char *moe_gated_ffn_kernel(int product, int T, int d, int f);
+const char *moe_gated_ffn_kernel(int product, int T, int d, int f, int all);
 size_t moe_gated_ffn_ws_bytes(int T, int d, int f);
 int moe_gated_ffn(const void *x_bf16, const void *w_gate_up_bf16,
                   const void *w_down_bf16, int T, int d, int f, void *out,

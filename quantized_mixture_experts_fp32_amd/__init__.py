@@ -138,7 +138,7 @@ def load_library():
                                        sz, vp]
     lib.moe_linear_i8_kernel.argtypes = [i32] * 3
     lib.moe_linear_i8_kernel.restype = ctypes.c_char_p
-    lib.moe_gated_ffn_kernel.argtypes = [i32] * 4
+    lib.moe_gated_ffn_kernel.argtypes = [i32] * 5
     lib.moe_gated_ffn_kernel.restype = ctypes.c_char_p
     lib.moe_linear_i8_ws_bytes.argtypes, lib.moe_linear_i8_ws_bytes.restype = [i32] * 4, sz
     lib.moe_linear_i8.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp, i32, vp, sz, vp]
@@ -1123,13 +1123,14 @@ def moe_gated_ffn_ws_bytes(T, d, f):
 GATED_PRODUCTS = ("gate_up", "down", "dh", "dx", "dw_gate_up", "dw_down")
 
 
-def moe_gated_ffn_kernel(product, T, d, f):
+def moe_gated_ffn_kernel(product, T, d, f, all=False):
     """The kernel that a product of the block (one of GATED_PRODUCTS) runs at these
-    sizes ("" where nothing runs)."""
+    sizes ("" where nothing runs): by itself, or (all) in a moe_gated_ffn_bwd that
+    asks for every gradient, and for gate_up and dh computes them again."""
     if product not in GATED_PRODUCTS:
         raise ValueError(f"moe_gated_ffn_kernel: product {product!r} is none of {GATED_PRODUCTS}")
     at = GATED_PRODUCTS.index(product)
-    return load_library().moe_gated_ffn_kernel(at, T, d, f).decode()
+    return load_library().moe_gated_ffn_kernel(at, T, d, f, all).decode()
 
 
 @_on_device

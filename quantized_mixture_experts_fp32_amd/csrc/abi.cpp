@@ -910,10 +910,10 @@ size_t moe_gated_ffn_ws_bytes(int T, int d, int f) {
   return moe::gated_ffn_ws_bytes(T, d, f);
 }
 
-const char* moe_gated_ffn_kernel(int product, int T, int d, int f) {
+const char* moe_gated_ffn_kernel(int product, int T, int d, int f, int all) {
   int status;
-  if (T == 0 || gated_refusal(T, d, f, &status)) return "";
-  return moe::gated_ffn_kernel(product, T, d, f);
+  if (T == 0 || product < 0 || gated_refusal(T, d, f, &status)) return "";
+  return moe::gated_ffn_kernel(product, T, d, f, all != 0);
 }
 
 int moe_gated_ffn(const void* x_bf16, const void* w_gate_up_bf16, const void* w_down_bf16, int T,

@@ -90,6 +90,17 @@ struct GatedBwdStore {
   }
 };
 
+// dh -> dg, du and h where dh and the pre-activations come from one launch; eight
+// values a thread.
+__global__ __launch_bounds__(256) void gated_bwd_kernel(const float* __restrict__ dh, int T,
+                                                        const GatedBwdStore<true> epi) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int per = epi.f / 8;
+  if (i >= (long long)T * per) return;
+  const int m = (int)(i / per), n = 8 * (int)(i % per);
+  epi(m, n, load_as<f32x8>(dh, 1, 8 * (size_t)i), {}, epi.ahead(m, n));
+}
+
 // fp32 rows to bf16, eight values a thread.
 __global__ __launch_bounds__(256) void to_bf16_kernel(const float* __restrict__ x,
                                                       long long chunks,
@@ -117,18 +128,6 @@ size_t gated_ffn_ws_bytes(int T, int d, int f) {
   return round_up(2 * (size_t)T * f);
 }
 
-const char* gated_ffn_kernel(int product, int T, int d, int f) {
-  switch (product) {
-    case MOE_GATED_GATE_UP: return product_name(kInner, false, T, f, d, 2LL * d, true);
-    case MOE_GATED_DOWN: return product_name(kInner, false, T, d, f, 2LL * f, false);
-    case MOE_GATED_DH: return product_name(kOuterB, false, T, f, d, 0, false);
-    case MOE_GATED_DX: return product_name(kOuterB, false, T, d, 2LL * f, 0, false);
-    case MOE_GATED_DW_GATE_UP: return product_name(kOuterBoth, false, 2LL * f, d, T, 0, false);
-    case MOE_GATED_DW_DOWN: return product_name(kOuterBoth, false, d, f, T, 0, false);
-  }
-  return "";
-}
-
 hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* w_gate_up, const uint16_t* w_down,
                             int T, int d, int f, void* out, int out_f32, uint16_t* gate_up,
                             void* ws, hipStream_t s) {
@@ -142,9 +141,32 @@ hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* w_gate_up, const 
 
 namespace {
 
+template <int kTile>
+using Tile = std::integral_constant<int, kTile>;
+
+// The gradient's launches of several products.  dx and both weights' gradients:
+const JointTiles kGradients[] = {{7, 6, "joint 32x64 64x64"},   {6, 5, "joint 64x64 64x128"},
+                                 {5, 6, "joint 64x128 64x64"},  {5, 5, "joint 64x128 64x128"},
+                                 {4, 4, "joint 128x128 k2"},    {2, 2, "joint 128x256"},
+                                 {0, 0, "joint 256x256"}};
+int plan_gradients(int T, int d, int f, bool dx, bool dw_gate_up, bool dw_down) {
+  const JointItem items[] = {{kOuterB, dx ? T : 0, d, stages_of(2 * f)},
+                             {kOuterBoth, dw_gate_up ? 2LL * f : 0, d, stages_of(T)},
+                             {kOuterBoth, dw_down ? d : 0, f, stages_of(T)}};
+  return plan_joint(kGradients, items, 0.0f);
+}
+// ... and the pre-activations computed again beside dh, which then goes to memory
+// and through a kernel of its own (4.5 TB/s).
+const JointTiles kRecompute[] = {{7, 7, "joint 32x64"}, {6, 6, "joint 64x64"},
+                                 {5, 5, "joint 64x128"}};
+int plan_recompute(int T, int d, int f) {
+  const JointItem items[] = {{kInner, T, 2LL * f, stages_of(d)}, {kOuterB, T, f, stages_of(d)}};
+  return plan_joint(kRecompute, items, 20.0f / 4.5e6f * T * f);
+}
+
 // Workspace of the gradient, in bytes from its start.
 struct BwdSpace {
-  size_t dgu, h, gate_up, x, dout, part, bytes;
+  size_t dgu, h, gate_up, x, dout, dh, part, bytes;
   BwdSpace(int T, int d, int f, int do_f32, int x_i8, int kept) {
     size_t at = 0;
     auto take = [&](bool wanted, size_t values, size_t size = 2) {
@@ -157,6 +179,7 @@ struct BwdSpace {
     gate_up = take(!kept, (size_t)T * 2 * f, 4);  // fp32: not rounded on the way
     x = take(x_i8, (size_t)T * d);
     dout = take(do_f32, (size_t)T * d);
+    dh = take(!kept && T > 0 && plan_recompute(T, d, f) >= 0, (size_t)T * f, 4);
     part = at;
     bytes = at + std::max(partial_bytes(2LL * f, d, stages_of(T)),
                           partial_bytes(d, f, stages_of(T)));
@@ -164,6 +187,25 @@ struct BwdSpace {
 };
 
 }  // namespace
+
+const char* gated_ffn_kernel(int product, int T, int d, int f, bool all) {
+  if (all && product <= MOE_GATED_DH) {
+    const int c = plan_recompute(T, d, f);
+    if (product != MOE_GATED_DOWN && c >= 0) return kRecompute[c].name;
+  } else if (all) {
+    const int c = plan_gradients(T, d, f, true, true, true);
+    if (c >= 0) return kGradients[c].name;
+  }
+  switch (product) {
+    case MOE_GATED_GATE_UP: return product_name(kInner, false, T, f, d, 2LL * d, true);
+    case MOE_GATED_DOWN: return product_name(kInner, false, T, d, f, 2LL * f, false);
+    case MOE_GATED_DH: return product_name(kOuterB, false, T, f, d, 0, false);
+    case MOE_GATED_DX: return product_name(kOuterB, false, T, d, 2LL * f, 0, false);
+    case MOE_GATED_DW_GATE_UP: return product_name(kOuterBoth, false, 2LL * f, d, T, 0, false);
+    case MOE_GATED_DW_DOWN: return product_name(kOuterBoth, false, d, f, T, 0, false);
+  }
+  return "";
+}
 
 size_t gated_ffn_bwd_ws_bytes(int T, int d, int f, int do_f32, int x_i8, int kept) {
   return BwdSpace(T, d, f, do_f32, x_i8, kept).bytes;
@@ -191,20 +233,69 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
       if (e != hipSuccess) return e;
       x = place(at.x);
     }
-    if (!a.gate_up) {
+    const Operand m = rows(dout, d, T), w = rows(a.w_down, f, f);
+    const int again = a.gate_up ? -1 : plan_recompute(T, d, f);
+    if (again >= 0) {
+      auto go = [&](auto tile) {
+        typedef typename TileShape<decltype(tile)::value>::Type Sh;
+        const auto gu = part_of<Sh, kInner, true>(rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d,
+                                                  GatedStore{nullptr, place(at.gate_up), 1, f});
+        const auto dh = part_of<Sh, kOuterB, false>(m, w, T, f, d, Store{place(at.dh), f, 1});
+        auto none = dh;
+        none.blocks = 0;
+        return launch_joint(gu, dh, none, s);
+      };
+      switch (again) {  // (as kRecompute has them)
+        case 0: e = go(Tile<7>{}); break;
+        case 1: e = go(Tile<6>{}); break;
+        case 2: e = go(Tile<5>{}); break;
+      }
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL(gated_bwd_kernel, dim3((uint32_t)up((long long)T * (f / 8), 256)),
+                         dim3(256), 0, s, (const float*)place(at.dh), T,
+                         GatedBwdStore<true>{place(at.gate_up), dgu, h, f});
+      e = hipGetLastError();
+    } else if (!a.gate_up) {
       e = launch_product<Bf16, kInner, true>(
           rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d, 2,
           GatedStore{nullptr, place(at.gate_up), 1, f}, part, s);
       if (e != hipSuccess) return e;
     }
-    const Operand m = rows(dout, d, T), w = rows(a.w_down, f, f);
-    if (a.gate_up)
+    if (again >= 0) {
+      // (done)
+    } else if (a.gate_up)
       e = launch_product<Bf16, kOuterB, false>(
           m, w, T, f, d, 2, GatedBwdStore<false>{a.gate_up, dgu, h, f}, nullptr, s);
     else
       e = launch_product<Bf16, kOuterB, false>(
           m, w, T, f, d, 2, GatedBwdStore<true>{place(at.gate_up), dgu, h, f}, nullptr, s);
     if (e != hipSuccess) return e;
+    const int joint = plan_gradients(T, d, f, a.dx, a.dw_gate_up, a.dw_down);
+    if (joint >= 0) {
+      auto go = [&](auto tile_x, auto tile_w) {
+        typedef typename TileShape<decltype(tile_x)::value>::Type ShX;
+        typedef typename TileShape<decltype(tile_w)::value>::Type ShW;
+        auto dx = part_of<ShX, kOuterB, false>(rows(dgu, 2 * f, T), rows(a.w_gate_up, d, d), T, d,
+                                               2 * f, Store{a.dx, d, 0});
+        auto wu = part_of<ShW, kOuterBoth, false>(rows(dgu, 2 * f, 2 * f), rows(x, d, d), 2 * f, d,
+                                                  T, Store{a.dw_gate_up, d, a.dw_f32});
+        auto wd = part_of<ShW, kOuterBoth, false>(rows(dout, d, d), rows(h, f, f), d, f, T,
+                                                  Store{a.dw_down, f, a.dw_f32});
+        if (!a.dx) dx.blocks = 0;
+        if (!a.dw_gate_up) wu.blocks = 0;
+        if (!a.dw_down) wd.blocks = 0;
+        return launch_joint(dx, wu, wd, s);
+      };
+      switch (joint) {  // (as kGradients has them)
+        case 0: return go(Tile<7>{}, Tile<6>{});
+        case 1: return go(Tile<6>{}, Tile<5>{});
+        case 2: return go(Tile<5>{}, Tile<6>{});
+        case 3: return go(Tile<5>{}, Tile<5>{});
+        case 4: return go(Tile<4>{}, Tile<4>{});
+        case 5: return go(Tile<2>{}, Tile<2>{});
+        case 6: return go(Tile<0>{}, Tile<0>{});
+      }
+    }
     if (a.dx) {
       e = launch_product<Bf16, kOuterB, false>(rows(dgu, 2 * f, T), rows(a.w_gate_up, d, d), T,
                                                    d, 2 * f, 2, Store{a.dx, d, 0}, part, s);

@@ -219,7 +219,7 @@ hipError_t launch_product_i8(const void* x, const float* x_scales, int T, int N,
                              void* out, int out_f32, hipStream_t s);
 
 // Gated feed-forward block and its gradient (gated_ffn.hip).
-const char* gated_ffn_kernel(int product, int T, int d, int f);  // (MOE_GATED_..)
+const char* gated_ffn_kernel(int product, int T, int d, int f, bool all);  // (MOE_GATED_..)
 size_t gated_ffn_ws_bytes(int T, int d, int f);
 hipError_t launch_gated_ffn(const uint16_t* x, const uint16_t* w_gate_up, const uint16_t* w_down,
                             int T, int d, int f, void* out, int out_f32, uint16_t* gate_up,

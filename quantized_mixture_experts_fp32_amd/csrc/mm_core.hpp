@@ -295,24 +295,24 @@ struct ReadAhead<Epi, std::void_t<typename Epi::Ahead>> {
 // Epi: operator()(m, n, v) for eight consecutive n (N is a multiple of 8; the
 // direct kernel: four), or in the pair form operator()(m, n, first, second).
 // With Epi::Ahead: operator()(m, n, v, columns(n), ahead(m, n)).
+// id: the block's among the tiles' blocks; part: its share of k.
 template <typename Mma, typename Sh, bool kAOuter, bool kBOuter, bool kPair, typename Epi>
-__global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kernel(
-    const Problem p, const Epi epi) {
-  extern __shared__ __align__(1024) char lds[];
+__device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, char* lds, int id,
+                                              int part) {
   constexpr int TM = Sh::BM / Sh::WM, TN = Sh::BN / Sh::WN, MI = TM / 16, NI = TN / 16;
   constexpr int kA = Sh::kA, kB = Sh::kB;
   const int lane = threadIdx.x & 63;
-  const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int group = id / Sh::kWaves, wave = id % Sh::kWaves;
+  const int any = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = any / Sh::kWaves, wave = any % Sh::kWaves;
   const int wm = wave / Sh::WN, wn = wave % Sh::WN;
   char* const ring = lds + group * Sh::kRing;
   int tm, tn;
-  tile_of(blockIdx.x, p.nm, p.nn, tm, tn);
+  tile_of(id, p.nm, p.nn, tm, tn);
   const int m0 = tm * Sh::BM, n0 = tn * Sh::BN;
   // The groups take the block's stages in turn, so that together they read long
   // pieces of a row (the groups' ranges side by side in k: .. of HBM's rate);
   // past the end of k stages are zeros.
-  const int block0 = blockIdx.y * Sh::G * p.per_group, stage0 = block0 + group;
+  const int block0 = part * Sh::G * p.per_group, stage0 = block0 + group;
   const int count = min(p.per_group, (p.stages - block0 + Sh::G - 1) / Sh::G);
 
   Loader<kAOuter, false, Sh::BM, MI, Sh::kWaves, Sh::G> la;
@@ -534,6 +534,43 @@ __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kern
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+template <typename Mma, typename Sh, bool kAOuter, bool kBOuter, bool kPair, typename Epi>
+__global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kernel(
+    const Problem p, const Epi epi) {
+  extern __shared__ __align__(1024) char lds[];
+  product_block<Mma, Sh, kAOuter, kBOuter, kPair>(p, epi, lds, blockIdx.x, blockIdx.y);
+}
+
+// Products that do not wait for each other, in one launch: one of the first kind
+// and up to two of the second, whose blocks follow.
+template <typename Shape_, bool kAOuter, bool kBOuter, bool kPair, typename Epi_>
+struct Part {
+  typedef Shape_ Sh;
+  typedef Epi_ Epi;
+  Problem p;
+  Epi epi;
+  int blocks;  // a multiple of 8, so that a tile's XCD is the one it has alone
+  __device__ __forceinline__ void run(char* lds, int id) const {
+    if (id < p.nm * p.nn) product_block<Bf16, Sh, kAOuter, kBOuter, kPair>(p, epi, lds, id, 0);
+  }
+};
+
+template <typename First, typename Second>
+__global__ __launch_bounds__(First::Sh::kThreads, First::Sh::kThreads / 256) void joint_kernel(
+    const First a, const Second b, const Second c, int shift) {
+  static_assert(First::Sh::kThreads == Second::Sh::kThreads, "blocks of one size");
+  extern __shared__ __align__(1024) char lds[];
+  int id = blockIdx.x + shift;
+  if (id >= (int)gridDim.x) id -= gridDim.x;
+  const int after = id - a.blocks;
+  if (after < 0)
+    a.run(lds, id);
+  else if (after < b.blocks)
+    b.run(lds, after);
+  else
+    c.run(lds, after - b.blocks);
 }
 
 }  // namespace mm

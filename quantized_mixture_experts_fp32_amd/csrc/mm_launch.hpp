@@ -74,14 +74,14 @@ struct Plan {
   int tile;    // of kTileCosts
   int splits;  // blocks that share a tile's k (both operands outer: k is long)
   int per;     // stages a block
+  float us;    // what it takes
 };
 
 // M rows and N columns (of B, so 2 f of the pair form), `stages` of k.
 inline Plan plan_product(Layout l, bool i8, long long M, long long N, int stages) {
   constexpr int kCUs = 256;
   const int kind = l == kInner ? i8 : l == kOuterB ? 2 : 3;
-  Plan best = {0, 1, stages};
-  float least = 1e30f;
+  Plan best = {0, 1, stages, 1e30f};
   for (int t = 0; t < kTileKernels; ++t) {
     const auto& c = kTileCosts[t].of[kind];
     if (c.one == 0) continue;
@@ -93,10 +93,7 @@ inline Plan plan_product(Layout l, bool i8, long long M, long long N, int stages
       const float us = c.fixed + c.block * n + per * std::max(c.one, c.each * n) +
                        // a second launch, and the sums written and read (4 TB/s)
                        (splits > 1 ? 4.0f + 2.0e-6f * splits * M * N : 0.0f);
-      if (us < least) {
-        least = us;
-        best = {t, splits, per};
-      }
+      if (us < best.us) best = {t, splits, per, us};
     }
   }
   return best;
@@ -185,11 +182,8 @@ inline void launch_tiles(const Problem& p, const Plan& plan, const Epi& epi, hip
   }
 }
 
-// C = A B^T with the epilogue; k values a row.  ws: partial_bytes of it (both
-// operands outer).
-template <typename Mma, Layout kL, bool kPair, typename Epi>
-inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int N, int k,
-                                 int elem_bytes, const Epi& epi, void* ws, hipStream_t s) {
+inline Problem problem_of(const Operand& a, const Operand& b, int M, int N, int k,
+                          int elem_bytes) {
   Problem p{};
   p.a = a;
   p.b = b;
@@ -198,6 +192,15 @@ inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int 
   p.kbytes = k * elem_bytes;
   p.krows = k;
   p.stages = (int)up((long long)k * elem_bytes, kStageBytes);
+  return p;
+}
+
+// C = A B^T with the epilogue; k values a row.  ws: partial_bytes of it (both
+// operands outer).
+template <typename Mma, Layout kL, bool kPair, typename Epi>
+inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int N, int k,
+                                 int elem_bytes, const Epi& epi, void* ws, hipStream_t s) {
+  const Problem p = problem_of(a, b, M, N, k, elem_bytes);
   if constexpr (kL == kInner) {
     if (direct_applies(M, N, b.stride, kPair))
       return launch_direct<Mma, kPair, false>({a.p, b.p, a.stride, b.stride, M, N, p.kbytes, 0},
@@ -216,6 +219,90 @@ inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int 
     }
   }
   launch_tiles<Mma, kL, kPair>(p, plan, epi, s);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------ several products a launch
+// Products that do not wait for each other share a launch where that is faster:
+// the blocks of one run where another leaves CUs idle, and a launch is saved.
+// The first product has one tile, the others have another; both by cost:
+//   max(longest, work) + 0.2 min(longest, work)
+// with the longest block's time alone on a CU, and all blocks' shares of a full
+// CU over the 256 CUs; one by one they take the sum of their plans.
+struct JointTiles {
+  int first, second;  // of kTileCosts
+  const char* name;
+};
+struct JointItem {
+  Layout l;
+  long long M, N;  // N: of the tile grid; M = 0: not wanted
+  int stages;
+};
+
+// Which of n choices of tiles, or -1: one by one.  extra: us that a joint launch
+// costs beside it.
+template <int kChoices, int kItems>
+inline int plan_joint(const JointTiles (&choices)[kChoices], const JointItem (&items)[kItems],
+                      float extra) {
+  float apart = 0.0f, best_us = 1e30f;
+  int best = -1, wanted = 0;
+  for (const JointItem& it : items) {
+    if (!it.M) continue;
+    ++wanted;
+    apart += plan_product(it.l, false, it.M, it.N, it.stages).us;
+  }
+  if (wanted < 2) return -1;
+  for (int c = 0; c < kChoices; ++c) {
+    float longest = 0.0f, work = 0.0f, fixed = 0.0f;
+    for (int i = 0; i < kItems; ++i) {
+      const JointItem& it = items[i];
+      if (!it.M) continue;
+      const TileCost& t = kTileCosts[i ? choices[c].second : choices[c].first];
+      const auto& us = t.of[it.l == kInner ? 0 : it.l == kOuterB ? 2 : 3];
+      const float blocks = (float)(up(it.M, t.bm) * up(it.N, t.bn));
+      fixed = std::max(fixed, us.fixed);
+      longest = std::max(longest, us.block + it.stages * std::max(us.one, us.each));
+      work += blocks * (us.block + it.stages * us.each) / 256;
+    }
+    const float us = fixed + extra + std::max(longest, work) + 0.2f * std::min(longest, work);
+    if (us < best_us) {
+      best_us = us;
+      best = c;
+    }
+  }
+  return best_us < apart ? best : -1;
+}
+
+// (as kTileCosts has them)
+template <int kTile>
+struct TileShape;
+template <> struct TileShape<0> { typedef Shape<256, 256, 2, 4, 2, 1, 1> Type; };
+template <> struct TileShape<2> { typedef Shape<128, 256, 2, 4, 2, 1, 1> Type; };
+template <> struct TileShape<4> { typedef Shape<128, 128, 2, 2, 2, 2, 1> Type; };
+template <> struct TileShape<5> { typedef Shape<64, 128, 1, 4, 3> Type; };
+template <> struct TileShape<6> { typedef Shape<64, 64, 2, 2, 3> Type; };
+template <> struct TileShape<7> { typedef Shape<32, 64, 2, 2, 4> Type; };
+
+// A product as a part of a launch.
+template <typename Sh, Layout kL, bool kPair, typename Epi>
+inline auto part_of(const Operand& a, const Operand& b, int M, int N, int k, const Epi& epi) {
+  Part<Sh, kL == kOuterBoth, kL != kInner, kPair, Epi> part{problem_of(a, b, M, N, k, 2), epi, 0};
+  Problem& p = part.p;
+  p.nm = (int)up(M, Sh::BM);
+  p.nn = (int)up(kPair ? 2LL * N : N, Sh::BN);
+  p.per_group = p.stages;
+  part.blocks = (p.nm * p.nn + 7) & ~7;
+  return part;
+}
+
+// (a part with blocks = 0 is left out)
+template <typename First, typename Second>
+inline hipError_t launch_joint(const First& a, const Second& b, const Second& c, hipStream_t s) {
+  constexpr int kLds = std::max(First::Sh::kLds, Second::Sh::kLds);
+  hipLaunchKernelGGL((joint_kernel<First, Second>), dim3(a.blocks + b.blocks + c.blocks),
+                     dim3(First::Sh::kThreads), kLds, s, a, b, c,
+                     // the longest sums first
+                     a.p.stages < b.p.stages && b.blocks ? a.blocks : 0);
   return hipGetLastError();
 }
 

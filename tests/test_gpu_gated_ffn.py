@@ -87,10 +87,14 @@ def test_gradient(T, d, f, source):
     for name, a, b, e in zip(got._fields, got, want, bounds):
         ref.check(name, a, b, e)
     part = moe.moe_gated_ffn_bwd(behind(dout), x, w, v, dw_dtype=code, need_dw=False, **kw)
-    assert part.dw_gate_up is None and torch.equal(part.dx, dx)
+    # (what is asked for chooses the kernels, so the order of the sums may differ; the
+    # bounds hold for any order)
+    assert part.dw_gate_up is None and part.dw_down is None
+    ref.check("dx alone", part.dx, want[0], bounds[0])
     part = moe.moe_gated_ffn_bwd(behind(dout), x, w, v, dw_dtype=code, need_dx=False, **kw)
     assert part.dx is None
-    assert torch.equal(part.dw_gate_up, dw) and torch.equal(part.dw_down, dv)
+    ref.check("dw_gate_up alone", part.dw_gate_up, want[1], bounds[1])
+    ref.check("dw_down alone", part.dw_down, want[2], bounds[2])
 
 
 def test_no_tokens():

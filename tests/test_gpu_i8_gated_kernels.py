@@ -5,7 +5,7 @@ import torch
 
 import i8_gated_ref as ref
 import quantized_mixture_experts_fp32_amd as moe
-from i8_gated_sizes import GATED, LINEAR
+from i8_gated_sizes import GATED, JOINT, LINEAR
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -26,6 +26,24 @@ def linear(T, N, K, seed=0):
     return (x, *moe.moe_quantize_i8(w, group=0), torch.randn(N, generator=g, device=DEV))
 
 
+def one_gradient(p, kept, name):
+    """One output of the gradient's C entry, by itself."""
+    lib = moe.load_library()
+    T, d = p["x"].shape
+    f = p["v"].shape[1]
+    shape = {"dx": (T, d), "dw_gate_up": (2 * f, d), "dw_down": (d, f)}
+    out = torch.full(shape[name], 7.0, dtype=BF16, device=DEV)
+    ws = torch.empty(lib.moe_gated_ffn_bwd_ws_bytes(T, d, f, 0, 0, 1), dtype=torch.uint8,
+                     device=DEV)
+    at = [out.data_ptr() if n == name else None for n in shape]
+    rc = lib.moe_gated_ffn_bwd(p["dout"].data_ptr(), 0, p["x"].data_ptr(), None, kept.data_ptr(),
+                               p["w"].data_ptr(), p["v"].data_ptr(), T, d, f, *at, 0,
+                               ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == moe.MOE_OK
+    torch.cuda.synchronize()
+    return out
+
+
 @pytest.mark.parametrize("product,name", [(p, n) for p in GATED for n in GATED[p]])
 def test_kernel_of_the_block(product, name):
     T, d, f = GATED[product][name]
@@ -39,12 +57,38 @@ def test_kernel_of_the_block(product, name):
     ref.check("gate_up", kept, gu, egu)
     if product in ("gate_up", "down"):
         return
-    got = moe.moe_gated_ffn_bwd(p["dout"], p["x"], p["w"], p["v"], gate_up=kept)
     grads, bounds = ref.gated_ffn_bwd(q["dout"], q["x"], q["w"], q["v"], kept.to(F64))
-    for n, a, b, e in zip(got._fields, got, grads, bounds):
+    names = ("dx", "dw_gate_up", "dw_down")
+    for n, b, e in zip(names, grads, bounds):
+        if product in ("dh", n):
+            got = one_gradient(p, kept, n)
+            ref.check(n, got, b, e)
+            assert torch.equal(got, one_gradient(p, kept, n))
+
+
+@pytest.mark.parametrize("part,name", [(p, n) for p in JOINT for n in JOINT[p]])
+def test_products_of_one_launch(part, name):
+    T, d, f = JOINT[part][name]
+    print(f"gated {part} {name} T={T} d={d} f={f}", flush=True)
+    got = moe.moe_gated_ffn_kernel("dx" if part == "gradients" else "dh", T, d, f, all=True)
+    assert got == name or (name == "apart" and not got.startswith("joint"))
+    p = block(T, d, f)
+    q = {n: t.to(F64) for n, t in p.items()}
+    kept = moe.moe_gated_ffn(p["x"], p["w"], p["v"], save=True)[1]
+    kw = dict(gate_up=kept) if part == "gradients" else {}
+    got = moe.moe_gated_ffn_bwd(p["dout"], p["x"], p["w"], p["v"], **kw)
+    want, bounds = ref.gated_ffn_bwd(q["dout"], q["x"], q["w"], q["v"],
+                                     kept.to(F64) if kw else None)
+    for n, a, b, e in zip(got._fields, got, want, bounds):
         ref.check(n, a, b, e)
-    again = moe.moe_gated_ffn_bwd(p["dout"], p["x"], p["w"], p["v"], gate_up=kept)
+    again = moe.moe_gated_ffn_bwd(p["dout"], p["x"], p["w"], p["v"], **kw)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
+    part = moe.moe_gated_ffn_bwd(p["dout"], p["x"], p["w"], p["v"], need_dx=False, **kw)
+    for n, a, b, e in zip(got._fields[1:], part[1:], want[1:], bounds[1:]):
+        ref.check(n, a, b, e)
+    if kw:
+        n = "dw_down"
+        ref.check(n, one_gradient(p, kept, n), want[2], bounds[2])
 
 
 @pytest.mark.parametrize("name", LINEAR)

@@ -11,7 +11,7 @@ import torch
 
 import i8_gated_ref as ref
 import quantized_mixture_experts_fp32_amd as moe
-from i8_gated_sizes import GATED, LINEAR
+from i8_gated_sizes import GATED, JOINT, LINEAR
 
 FAKE = ctypes.c_void_p(0x10000)
 ODD = ctypes.c_void_p(0x10002)
@@ -243,6 +243,9 @@ def test_no_other_kernel_is_chosen(lib):
         d, f = -(-d // 8) * 8, -(-f // 8) * 8
         for p in GATED:
             assert moe.moe_gated_ffn_kernel(p, T, d, f) in GATED[p], (p, T, d, f)
+        for p, joint in (("dx", "gradients"), ("dh", "recompute")):
+            name = moe.moe_gated_ffn_kernel(p, T, d, f, all=True)
+            assert name in JOINT[joint] or not name.startswith("joint"), (p, T, d, f)
         assert moe.moe_linear_i8_kernel(T, 4 * d, 2 * f) in LINEAR, (T, d, f)
 
 
@@ -250,6 +253,7 @@ def test_no_kernel(lib):
     assert moe.moe_linear_i8_kernel(0, 64, 64) == "" == moe.moe_linear_i8_kernel(4, 64, 8)
     assert moe.moe_gated_ffn_kernel("dx", 0, 64, 64) == ""
     assert moe.moe_gated_ffn_kernel("dx", 4, 64, 12) == ""
-    assert lib.moe_gated_ffn_kernel(6, 4, 64, 64) == b"" == lib.moe_gated_ffn_kernel(-1, 4, 64, 64)
+    assert lib.moe_gated_ffn_kernel(6, 4, 64, 64, 0) == b""
+    assert lib.moe_gated_ffn_kernel(-1, 4, 64, 64, 1) == b""
     with pytest.raises(ValueError, match="none of"):
         moe.moe_gated_ffn_kernel("up", 4, 64, 64)

@@ -64,17 +64,6 @@ __global__ __launch_bounds__(kDirectWaves* kWave, 4) void direct_kernel(const Di
   for (int k0 = 0; k0 < p.kbytes; k0 += p.piece) {
     const int bytes = min(p.piece, p.kbytes - k0), units = (bytes + 127) >> 7;
     if (k0) __syncthreads();  // every wave has read the last piece
-    // tokens to LDS: asked for ahead of the weights
-    if constexpr (!kQuant) {
-      const int per = p.piece >> 4, n = T * per;  // chunks
-      const __amdgpu_buffer_rsrc_t xr = rsrc_of(p.x + k0);
-      for (int i = wave * kWave; i < n; i += W * kWave) {
-        const int t = (i + lane) / per, c = (i + lane) - t * per, at = 16 * (c ^ (t & 15));
-        const uint32_t o = t < T && at < bytes ? (uint32_t)(t * p.xstride) + at : kOutOfRange;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (Lds)(lds + 16 * i), 16, (int)o, 0, 0, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
     auto load = [&](Unit (&u)[kU], int i) {  // (units past the last are out of range)
 #pragma unroll
       for (int j = 0; j < kU; ++j)
@@ -87,6 +76,21 @@ __global__ __launch_bounds__(kDirectWaves* kWave, 4) void direct_kernel(const Di
         }
     };
     Unit a[kU], b[kU];
+    if constexpr (!kQuant) {
+      load(a, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // tokens to LDS: asked for ahead of the weights
+    if constexpr (!kQuant) {
+      const int per = p.piece >> 4, n = T * per;  // chunks
+      const __amdgpu_buffer_rsrc_t xr = rsrc_of(p.x + k0);
+      for (int i = wave * kWave; i < n; i += W * kWave) {
+        const int t = (i + lane) / per, c = (i + lane) - t * per, at = 16 * (c ^ (t & 15));
+        const uint32_t o = t < T && at < bytes ? (uint32_t)(t * p.xstride) + at : kOutOfRange;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (Lds)(lds + 16 * i), 16, (int)o, 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if constexpr (kQuant) {
       // a row is one wave's; all of it is read once for its largest value
       const int nch = p.kbytes >> 3;
@@ -136,10 +140,9 @@ __global__ __launch_bounds__(kDirectWaves* kWave, 4) void direct_kernel(const Di
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
     } else {
-      load(a, 0);
       load(b, kU);
       __builtin_amdgcn_sched_barrier(0);
-      wait_stage<4 * kU>();  // the tokens are in; the weights stay in flight
+      wait_stage<2 * kU>();  // the tokens are in; the weights stay in flight
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
     }

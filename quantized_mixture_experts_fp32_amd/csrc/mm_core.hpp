@@ -18,8 +18,16 @@
 //     values of eight rows of k and pairs them up in registers, so that it holds
 //     eight k of F fragments: fragment t is the tile's rows F r + t, r < 16 (the
 //     LDS transpose read gives rows 16 t + r, but at a quarter of the rate:
-//     8192^3 with both operands outer .. us, this way .. us).  Sixteen-byte chunk c
+//     8192^3 with both operands outer 888 us, this way 828 us).  Sixteen-byte chunk c
 //     lies at c ^ s(k), which keeps the four octets of k on different banks.
+//
+// Bound by the matrix cores where a launch fills the chip and k is long: bf16, the
+// gated block's two products of 8192 tokens of 8192 values through 4096 features
+// 1172 us, 1.41 PFLOP/s (the library's product 8192^3 713 us, 1.54, on the same
+// card; its instructions alone 575 us); int8 8192^3 420 us, 2.6 POP/s (the
+// library's 491).  Short k is bound by what a block does before and after its
+// stages, 4 to 8 us of a 256 x 256 tile.  Tried without gain: deeper rings, a
+// raised wave priority, 32 x 32 instructions (slower).
 #pragma once
 #include <type_traits>
 
@@ -310,8 +318,7 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
   tile_of(id, p.nm, p.nn, tm, tn);
   const int m0 = tm * Sh::BM, n0 = tn * Sh::BN;
   // The groups take the block's stages in turn, so that together they read long
-  // pieces of a row (the groups' ranges side by side in k: .. of HBM's rate);
-  // past the end of k stages are zeros.
+  // pieces of a row; past the end of k stages are zeros.
   const int block0 = part * Sh::G * p.per_group, stage0 = block0 + group;
   const int count = min(p.per_group, (p.stages - block0 + Sh::G - 1) / Sh::G);
 

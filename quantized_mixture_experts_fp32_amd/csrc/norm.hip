@@ -12,7 +12,8 @@
 // registers, and has the next row's three arrays in flight during the sums of
 // this one: 8191 rows of 4096 (bf16) take 55 us with the column sums, 4.9 TB/s,
 // the rate of a large copy (76 us without the prefetch).  Forward, 8192 rows of
-// 4096 (bf16) 27 us, 4.9 TB/s; 16 rows 2.5 us, a launch.
+// 4096 (bf16) 27 us, 4.9 TB/s; 16 rows 2.5 us, a launch.  From an 8-bit checkpoint
+// (kRowI8) 8192 rows of 4096 take 20 us (5.0 TB/s), their gradient 44 to 52 us.
 #include "launch.hpp"
 #include "rowops.hpp"
 

@@ -7,7 +7,10 @@
 // three fp32 steps.  A group below 2^-119 is stored as zeros (127 / m stays
 // finite), one with an infinity or NaN restores as NaN.
 //
-// HBM-bound: x is read once and the codes are written once.
+// HBM-bound: x is read once and the codes are written once.  8192 x 4096 (bf16):
+// 22.7 us in groups (4.5 TB/s), 20.4 us by row (4.9 TB/s), restored in 18.7 us (5.4
+// TB/s; a large copy: 5.1); 8192 x 4096 (fp32) 30 us (5.6 TB/s, partly from the
+// last cache); 16 rows 2.9 us, a launch.
 #include "i8.hpp"
 #include "launch.hpp"
 
@@ -116,16 +119,16 @@ hipError_t launch_quantize_i8(const void* x, int x_f32, int T, int K, int by_row
                        scales);
   };
   using std::integral_constant;
-  // A wave a row where it can hold it: no barrier, and short rows leave no lanes
-  // idle (5597 x 336: .. us); four where there are few rows or they are long.
+  // A wave a row up to 1024 values: no barrier, and short rows leave no lanes idle
+  // (5597 x 336 4.2 us, four waves 6.0; 8192 x 1024 8.3 and 10.0); four waves for
+  // longer ones (8192 x 2048 13.0 us, one wave 15.2), which beyond 8192 values are
+  // read twice (8192 x 16384 109 us).
   constexpr integral_constant<int, 1> one{};
   constexpr integral_constant<int, 4> four{};
   if (K <= 512)
     go(one, one);
   else if (K <= 1024)
     go(integral_constant<int, 2>{}, one);
-  else if (K <= 2048 && T > 512)
-    go(four, one);
   else if (K <= 2048)
     go(one, four);
   else if (K <= 4096)

@@ -4,8 +4,8 @@
 # with clang through hipcc, both under AddressSanitizer and
 # UndefinedBehaviorSanitizer with recovery off, then runs the CPU tests that
 # exercise them: the oracle pins against the instrumented oracle, and the
-# ABI validation and the expert cache slot planner against the instrumented
-# library.  Usage: tests/sanitize_host.sh [output dir]
+# ABI validation (of the 8-bit rows and the gated block too) and the expert cache
+# slot planner against the instrumented library.  Usage: tests/sanitize_host.sh [output dir]
 set -euo pipefail
 R=$(cd "$(dirname "$0")/.." && pwd)
 OUT=${1:-/tmp/moe_sanitize}
@@ -16,19 +16,23 @@ SAN="-fsanitize=address,undefined -fno-sanitize-recover=all -fno-omit-frame-poin
 gcc -O1 -g -std=c11 -fPIC -shared -fopenmp -ffp-contract=off $SAN \
     -o "$OUT/liboracle.so" "$R/oracle/oracle.c" -lm
 
-SRCS="abi.cpp route.hip permute.hip quant.hip ffn.hip ffn_decode.hip ffn_bitplane.hip \
-      ffn_prefill.hip combine.hip alloc.hip cache.hip cache.cpp noalloc.hip retile.hip"
-ARGS=()
-for s in $SRCS; do ARGS+=("$R/quantized_mixture_experts_fp32_amd/csrc/$s"); done
-"$HIPCC" --offload-arch=gfx950 -O1 -g -std=c++17 -fPIC -shared \
+sources() {  # of the build's own lists
+  (cd "$R" && python3 -c "
+from quantized_mixture_experts_fp32_amd import build
+print(' '.join('quantized_mixture_experts_fp32_amd/csrc/' + s for s in build.$1))")
+}
+FLAGS="--offload-arch=gfx950 -O1 -g -std=c++17 -fPIC -shared \
     -Xclang -target-feature -Xclang -packed-fp32-ops -mllvm -amdgpu-mfma-vgpr-form=1 \
     -Xarch_host -fsanitize=address -Xarch_host -fsanitize=undefined \
-    -Xarch_host -fno-sanitize-recover=all -Xarch_host -fno-omit-frame-pointer \
-    -I "$R/include" -o "$OUT/libmoe_wq.so" "${ARGS[@]}"
+    -Xarch_host -fno-sanitize-recover=all -Xarch_host -fno-omit-frame-pointer"
+cd "$R"
+"$HIPCC" $FLAGS -I "$R/include" -Wl,-soname,libmoe_wq_i8.so -o "$OUT/libmoe_wq_i8.so" \
+    $(sources SOURCES_I8)
+"$HIPCC" $FLAGS -I "$R/include" -o "$OUT/libmoe_wq.so" $(sources SOURCES) \
+    -L"$OUT" -l:libmoe_wq_i8.so -Wl,-rpath,'$ORIGIN'
 
 export ASAN_OPTIONS=detect_leaks=0:abort_on_error=1
 export UBSAN_OPTIONS=print_stacktrace=1:halt_on_error=1
-cd "$R"
 LD_PRELOAD=$(gcc -print-file-name=libasan.so) python3 -c "
 import sys, oracle, pytest
 oracle.LIB = sys.argv[1]
@@ -40,5 +44,6 @@ import sys, pytest
 import quantized_mixture_experts_fp32_amd as moe
 moe.LIB_PATH = sys.argv[1]
 sys.exit(pytest.main(['-q', '-p', 'no:cacheprovider', '-m', 'not gpu',
-                      'tests/test_abi_host.py', 'tests/test_cache_plan.py']))" "$OUT/libmoe_wq.so"
+                      'tests/test_abi_host.py', 'tests/test_cache_plan.py',
+                      'tests/test_i8_gated_host.py']))" "$OUT/libmoe_wq.so"
 echo "sanitized host run: clean"

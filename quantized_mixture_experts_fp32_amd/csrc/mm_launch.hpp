@@ -19,9 +19,8 @@ enum Layout { kInner, kOuterB, kOuterBoth };
 // for n blocks a CU and stages of 128 bytes (or 64 rows) of k; one: the latency
 // of a stage where a block is alone on its CU, each: its share of a full CU.
 // Fitted by kind of product to 140 to 180 random sizes each (1 to 8192 rows, 64
-// to 50304 columns, k 8 to 8192); on 55 others of each kind the choice took 0.3 %
-// (outer B) to 1.3 % (inner bf16) longer than the fastest of 13 tiles on average,
-// 18 % at most; with both outer 4 % and 33 %, before k is split over blocks
+// to 50304 columns, k 8 to 8192); on 70 others of each kind the choice took 0.2 to
+// 0.7 % longer than the fastest tile on average, 13 % at most
 // (profiles/product_choice.txt).
 struct TileCost {
   int bm, bn;
@@ -34,37 +33,37 @@ constexpr int kSplitPrefix = 6;  // "split "
 constexpr int kTileKernels = 11;
 const TileCost kTileCosts[kTileKernels] = {
     {256, 256,
-     {{0.0f, 5.8f, 1.03f, 1.31f}, {0.0f, 8.5f, 1.17f, 1.22f}, {0.0f, 6.9f, 0.20f, 1.22f},
+     {{0.0f, 7.0f, 1.48f, 1.43f}, {0.0f, 8.5f, 1.17f, 1.22f}, {0.0f, 6.9f, 0.20f, 1.22f},
       {0.0f, 9.0f, 0.46f, 1.18f}},
      "split tile 256x256"},
     {192, 256,
-     {{0.0f, 5.0f, 0.70f, 1.13f}, {0.0f, 7.1f, 0.32f, 1.08f}, {0.0f, 6.1f, 0.23f, 0.94f}, {}},
+     {{0.0f, 6.5f, 1.21f, 1.17f}, {0.0f, 7.1f, 0.32f, 1.08f}, {0.0f, 6.1f, 0.23f, 0.94f}, {}},
      "split tile 192x256"},
     {128, 256,
      {{}, {0.0f, 5.7f, 0.89f, 0.90f}, {0.0f, 5.0f, 0.03f, 0.73f}, {0.0f, 6.3f, 0.79f, 0.80f}},
      "split tile 128x256"},
     {128, 128,
-     {{1.8f, 1.8f, 0.60f, 0.51f}, {0.9f, 3.5f, 0.56f, 0.53f}, {}, {2.3f, 2.8f, 0.59f, 0.51f}},
+     {{2.6f, 1.5f, 0.63f, 0.51f}, {0.9f, 3.5f, 0.56f, 0.53f}, {}, {2.3f, 2.8f, 0.59f, 0.51f}},
      "split tile 128x128"},
     {128, 128,
-     {{0.1f, 4.7f, 0.27f, 0.54f}, {0.0f, 5.6f, 0.49f, 0.52f}, {0.0f, 5.4f, 0.44f, 0.46f},
+     {{1.6f, 4.0f, 0.27f, 0.56f}, {0.0f, 5.6f, 0.49f, 0.52f}, {0.0f, 5.4f, 0.44f, 0.46f},
       {0.0f, 6.6f, 0.45f, 0.47f}},
      "split tile 128x128 k2"},
     {64, 128,
-     {{2.9f, 0.53f, 0.39f, 0.39f}, {2.3f, 1.7f, 0.08f, 0.38f}, {2.7f, 0.94f, 0.37f, 0.36f},
+     {{3.2f, 0.78f, 0.38f, 0.37f}, {2.3f, 1.7f, 0.08f, 0.38f}, {2.7f, 0.94f, 0.37f, 0.36f},
       {2.7f, 1.8f, 0.43f, 0.38f}},
      "split tile 64x128"},
     {64, 64,
-     {{3.1f, 0.11f, 0.28f, 0.25f}, {2.9f, 0.70f, 0.25f, 0.25f}, {3.1f, 0.21f, 0.29f, 0.26f},
+     {{3.2f, 0.36f, 0.26f, 0.24f}, {2.9f, 0.70f, 0.25f, 0.25f}, {3.1f, 0.21f, 0.29f, 0.26f},
       {2.8f, 0.89f, 0.36f, 0.27f}},
      "split tile 64x64"},
     {32, 64,
-     {{3.2f, 0.12f, 0.16f, 0.18f}, {3.1f, 0.47f, 0.15f, 0.17f}, {3.4f, 0.09f, 0.24f, 0.21f}, {}},
+     {{3.1f, 0.34f, 0.19f, 0.17f}, {3.1f, 0.47f, 0.15f, 0.17f}, {3.4f, 0.09f, 0.24f, 0.21f}, {}},
      "split tile 32x64"},
     {32, 64, {{}, {}, {1.8f, 2.8f, 0.14f, 0.20f}, {}}, "split tile 32x64 k4"},
-    {32, 32, {{2.9f, 0.75f, 0.10f, 0.10f}, {2.8f, 0.91f, 0.10f, 0.09f}, {}, {}}, "split tile 32x32 k2"},
+    {32, 32, {{2.6f, 0.85f, 0.12f, 0.10f}, {2.8f, 0.91f, 0.10f, 0.09f}, {}, {}}, "split tile 32x32 k2"},
     {160, 256,
-     {{0.0f, 4.6f, 0.25f, 1.03f}, {0.0f, 6.6f, 0.95f, 0.96f}, {0.0f, 5.7f, 0.80f, 0.80f}, {}},
+     {{0.0f, 5.9f, 1.09f, 1.05f}, {0.0f, 6.6f, 0.95f, 0.96f}, {0.0f, 5.7f, 0.80f, 0.80f}, {}},
      "split tile 160x256"},
 };
 

@@ -153,10 +153,11 @@ template <int kTile>
 using Tile = std::integral_constant<int, kTile>;
 
 // The gradient's launches of several products.  dx and both weights' gradients:
-const JointTiles kGradients[] = {{7, 6, "joint 32x64 64x64"},   {6, 5, "joint 64x64 64x128"},
-                                 {5, 6, "joint 64x128 64x64"},  {5, 5, "joint 64x128 64x128"},
-                                 {4, 4, "joint 128x128 k2"},    {2, 2, "joint 128x256"},
-                                 {0, 0, "joint 256x256"}};
+const JointTiles kGradients[] = {
+    {7, 6, 0.2f, "joint 32x64 64x64"},  {6, 5, 0.2f, "joint 64x64 64x128"},
+    {5, 6, 0.2f, "joint 64x128 64x64"}, {5, 5, 0.2f, "joint 64x128 64x128"},
+    {4, 4, 0.2f, "joint 128x128 k2"},   {2, 2, 0.2f, "joint 128x256"},
+    {0, 0, 0.2f, "joint 256x256"},      {8, 11, 0.5f, "joint 32x64 k4 128x128"}};
 int plan_gradients(int T, int d, int f, bool dx, bool dw_gate_up, bool dw_down) {
   const JointItem items[] = {{kOuterB, dx ? T : 0, d, stages_of(2 * f)},
                              {kOuterBoth, dw_gate_up ? 2LL * f : 0, d, stages_of(T)},
@@ -165,8 +166,10 @@ int plan_gradients(int T, int d, int f, bool dx, bool dw_gate_up, bool dw_down) 
 }
 // ... and the pre-activations computed again beside dh, which then goes to memory
 // and through a kernel of its own (4.5 TB/s).
-const JointTiles kRecompute[] = {{7, 7, "joint 32x64"}, {6, 6, "joint 64x64"},
-                                 {5, 5, "joint 64x128"}};
+const JointTiles kRecompute[] = {{7, 7, 0.2f, "joint 32x64"},
+                                 {6, 6, 0.2f, "joint 64x64"},
+                                 {5, 5, 0.2f, "joint 64x128"},
+                                 {8, 8, 0.5f, "joint 32x64 k4"}};
 int plan_recompute(int T, int d, int f) {
   const JointItem items[] = {{kInner, T, 2LL * f, stages_of(d)}, {kOuterB, T, f, stages_of(d)}};
   return plan_joint(kRecompute, items, 20.0f / 4.5e6f * T * f);
@@ -257,6 +260,7 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
         case 0: e = go(Tile<7>{}); break;
         case 1: e = go(Tile<6>{}); break;
         case 2: e = go(Tile<5>{}); break;
+        case 3: e = go(Tile<8>{}); break;
       }
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL(gated_bwd_kernel, dim3((uint32_t)up((long long)T * (f / 8), 256)),
@@ -302,6 +306,7 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
         case 4: return go(Tile<4>{}, Tile<4>{});
         case 5: return go(Tile<2>{}, Tile<2>{});
         case 6: return go(Tile<0>{}, Tile<0>{});
+        case 7: return go(Tile<8>{}, Tile<11>{});
       }
     }
     if (a.dx) {

@@ -30,8 +30,8 @@ struct TileCost {
   const char* name;  // behind the prefix of one whose k is split over blocks
 };
 constexpr int kSplitPrefix = 6;  // "split "
-constexpr int kTileKernels = 11;
-const TileCost kTileCosts[kTileKernels] = {
+constexpr int kTileKernels = 11;  // and one behind them for launches of several products
+const TileCost kTileCosts[kTileKernels + 1] = {
     {256, 256,
      {{0.0f, 7.0f, 1.48f, 1.43f}, {0.0f, 8.5f, 1.17f, 1.22f}, {0.0f, 6.9f, 0.20f, 1.22f},
       {0.0f, 9.0f, 0.46f, 1.18f}},
@@ -58,13 +58,16 @@ const TileCost kTileCosts[kTileKernels] = {
       {2.8f, 0.89f, 0.36f, 0.27f}},
      "split tile 64x64"},
     {32, 64,
-     {{3.1f, 0.34f, 0.19f, 0.17f}, {3.1f, 0.47f, 0.15f, 0.17f}, {3.4f, 0.09f, 0.24f, 0.21f}, {}},
+     {{3.1f, 0.34f, 0.19f, 0.17f}, {3.1f, 0.47f, 0.15f, 0.17f}, {2.8f, 0.46f, 0.26f, 0.20f}, {}},
      "split tile 32x64"},
-    {32, 64, {{}, {}, {1.8f, 2.8f, 0.14f, 0.20f}, {}}, "split tile 32x64 k4"},
+    {32, 64,
+     {{1.7f, 2.8f, 0.02f, 0.17f}, {}, {0.8f, 3.7f, 0.17f, 0.18f}, {}},
+     "split tile 32x64 k4"},
     {32, 32, {{2.6f, 0.85f, 0.12f, 0.10f}, {2.8f, 0.91f, 0.10f, 0.09f}, {}, {}}, "split tile 32x32 k2"},
     {160, 256,
      {{0.0f, 5.9f, 1.09f, 1.05f}, {0.0f, 6.6f, 0.95f, 0.96f}, {0.0f, 5.7f, 0.80f, 0.80f}, {}},
      "split tile 160x256"},
+    {128, 128, {{}, {}, {}, {1.5f, 3.1f, 0.75f, 0.61f}}, "split tile 128x128 w16"},
 };
 
 inline long long up(long long a, long long b) { return (a + b - 1) / b; }
@@ -170,7 +173,8 @@ inline void launch_tiles(const Problem& p, const Plan& plan, const Epi& epi, hip
       if constexpr (!kBoth) go(integer_sequence<int, 32, 64, 2, 2, 4>{});
       return;
     case 8:
-      if constexpr (kB) go(integer_sequence<int, 32, 64, 2, 2, 3, 4>{});
+      if constexpr (kB || (kIn && std::is_same_v<Mma, Bf16>))
+        go(integer_sequence<int, 32, 64, 2, 2, 3, 4>{});
       return;
     case 9:
       if constexpr (kIn) go(integer_sequence<int, 32, 32, 2, 1, 4, 2>{});
@@ -225,9 +229,12 @@ inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int 
 // Products that do not wait for each other share a launch where that is faster:
 // the blocks of one run where another leaves CUs idle, and a launch is saved.
 // The first product has one tile, the others have another; both by cost:
-//   max(longest, work) + 0.2 min(longest, work)
+//   max(longest, work) + overlap * min(longest, work)
 // with the longest block's time alone on a CU, and all blocks' shares of a full
-// CU over the 256 CUs; one by one they take the sum of their plans.  Over 80
+// CU over the 256 CUs; overlap 0.2, or 0.5 where a block has its CU to itself and
+// is there for few blocks with a long k (tokens 1, d 896, f 1952: 27.6 us with tiles
+// of four waves, 21.3 with 16; 131, 2048, 1024: 26.4 and 29.3); one by one they take
+// the sum of their plans.  Over 80
 // random sizes of a gradient (1 to 8192 tokens, 128 to 4096 values) the choice took
 // 1.6 % longer than the best and 26 % less than one by one; 5000 tokens of 2560
 // through 2560 features 350 us together and 385 us one by one, 4096 of 4096 through
@@ -235,6 +242,7 @@ inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int 
 // (profiles/product_choice.txt).
 struct JointTiles {
   int first, second;  // of kTileCosts
+  float overlap;
   const char* name;
 };
 struct JointItem {
@@ -268,7 +276,8 @@ inline int plan_joint(const JointTiles (&choices)[kChoices], const JointItem (&i
       longest = std::max(longest, us.block + it.stages * std::max(us.one, us.each));
       work += blocks * (us.block + it.stages * us.each) / 256;
     }
-    const float us = fixed + extra + std::max(longest, work) + 0.2f * std::min(longest, work);
+    const float us = fixed + extra + std::max(longest, work) +
+                     choices[c].overlap * std::min(longest, work);
     if (us < best_us) {
       best_us = us;
       best = c;
@@ -286,6 +295,8 @@ template <> struct TileShape<4> { typedef Shape<128, 128, 2, 2, 2, 2, 1> Type; }
 template <> struct TileShape<5> { typedef Shape<64, 128, 1, 4, 3> Type; };
 template <> struct TileShape<6> { typedef Shape<64, 64, 2, 2, 3> Type; };
 template <> struct TileShape<7> { typedef Shape<32, 64, 2, 2, 4> Type; };
+template <> struct TileShape<8> { typedef Shape<32, 64, 2, 2, 3, 4> Type; };
+template <> struct TileShape<11> { typedef Shape<128, 128, 4, 4, 2> Type; };
 
 // A product as a part of a launch.
 template <typename Sh, Layout kL, bool kPair, typename Epi>

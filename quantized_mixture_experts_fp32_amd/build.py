@@ -2,8 +2,10 @@
 to (libmoe_wq_i8.so, 8-bit products) in-tree with hipcc."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -20,27 +22,44 @@ SOURCES_I8 = ["linear_i8.hip"]
 # MFMA accumulators are allocated in ordinary VGPRs (not AGPRs): the kernels
 # rescale and convert accumulators with VALU instructions, which would
 # otherwise need a move to and from the AGPR file for every element.
-FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-Wall", "-Wno-unused-result", "-Xclang", "-target-feature",
          "-Xclang", "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form=1",
          "-I", os.path.join(ROOT, "include")]
 
 
-def _link(lib, sources, verbose, *more):
-    tmp = lib + ".tmp"
-    cmd = [HIPCC] + FLAGS + ["-o", tmp] + [os.path.join(CSRC, s) for s in sources] + list(more)
+def _run(what, cmd):
     r = subprocess.run(cmd, cwd=CSRC, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{os.path.basename(lib)} build failed:\n" + r.stdout + r.stderr)
-    if verbose:
-        print(r.stderr)
+        raise RuntimeError(f"{what} failed:\n" + r.stdout + r.stderr)
+    return r.stderr
+
+
+def _link(lib, objects, *more):
+    tmp = lib + ".tmp"
+    _run(f"{os.path.basename(lib)} link",
+         [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objects, *more])
     os.replace(tmp, lib)
-    return lib
 
 
 def build(verbose: bool = False) -> str:
-    _link(LIB_I8, SOURCES_I8, verbose, "-Wl,-soname,libmoe_wq_i8.so")
-    return _link(LIB, SOURCES, verbose, LIB_I8, "-Wl,-rpath,$ORIGIN")
+    sources = SOURCES + SOURCES_I8
+    with tempfile.TemporaryDirectory() as objects:
+        out = [os.path.join(objects, s + ".o") for s in sources]
+
+        def compile_one(s, o):
+            return _run(f"{s} build", [HIPCC, *FLAGS, "-c", os.path.join(CSRC, s), "-o", o])
+
+        jobs = int(os.environ.get("MAX_JOBS", 0)) or min(8, os.cpu_count() or 1)
+        with concurrent.futures.ThreadPoolExecutor(jobs) as pool:
+            for said in pool.map(compile_one, sources, out):
+                if verbose:
+                    print(said)
+        n = len(SOURCES)
+        _link(LIB_I8, out[n:], "-Wl,-soname," + os.path.basename(LIB_I8))
+        # found beside the library, here and wherever both are copied
+        _link(LIB, out[:n], LIB_I8, "-Wl,-rpath,$ORIGIN")
+    return LIB
 
 
 if __name__ == "__main__":

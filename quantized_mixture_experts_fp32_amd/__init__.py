@@ -679,9 +679,8 @@ def _out_f32(fn, name, t, shape, like):
 
 
 def _workspace(fn, ws, need, like):
-    import torch
-    if ws is None:
-        return like.new_empty((need,), dtype=torch.uint8) if need else None
+    if ws is None:  # (of like's type: the shortest call)
+        return like.new_empty(-(-need // like.element_size())) if need else None
     if not ws.is_contiguous() or ws.device != like.device:
         raise ValueError(f"{fn}: ws must be contiguous and on {like.device}")
     return ws

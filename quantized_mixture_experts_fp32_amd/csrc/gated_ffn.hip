@@ -267,20 +267,17 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
                          dim3(256), 0, s, (const float*)place(at.dh), T,
                          GatedBwdStore<true>{place(at.gate_up), dgu, h, f});
       e = hipGetLastError();
-    } else if (!a.gate_up) {
-      e = launch_product<Bf16, kInner, true>(
-          rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d, 2,
-          GatedStore{nullptr, place(at.gate_up), 1, f}, part, s);
-      if (e != hipSuccess) return e;
-    }
-    if (again >= 0) {
-      // (done)
-    } else if (a.gate_up)
+    } else if (a.gate_up) {
       e = launch_product<Bf16, kOuterB, false>(
           m, w, T, f, d, 2, GatedBwdStore<false>{a.gate_up, dgu, h, f}, nullptr, s);
-    else
+    } else {
+      e = launch_product<Bf16, kInner, true>(
+          rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d, 2,
+          GatedStore{nullptr, place(at.gate_up), 1, f}, nullptr, s);
+      if (e != hipSuccess) return e;
       e = launch_product<Bf16, kOuterB, false>(
           m, w, T, f, d, 2, GatedBwdStore<true>{place(at.gate_up), dgu, h, f}, nullptr, s);
+    }
     if (e != hipSuccess) return e;
     const int joint = plan_gradients(T, d, f, a.dx, a.dw_gate_up, a.dw_down);
     if (joint >= 0) {
@@ -311,7 +308,7 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
     }
     if (a.dx) {
       e = launch_product<Bf16, kOuterB, false>(rows(dgu, 2 * f, T), rows(a.w_gate_up, d, d), T,
-                                                   d, 2 * f, 2, Store{a.dx, d, 0}, part, s);
+                                               d, 2 * f, 2, Store{a.dx, d, 0}, nullptr, s);
       if (e != hipSuccess) return e;
     }
   }

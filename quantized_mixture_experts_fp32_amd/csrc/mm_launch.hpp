@@ -234,12 +234,11 @@ inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int 
 // CU over the 256 CUs; overlap 0.2, or 0.5 where a block has its CU to itself and
 // is there for few blocks with a long k (tokens 1, d 896, f 1952: 27.6 us with tiles
 // of four waves, 21.3 with 16; 131, 2048, 1024: 26.4 and 29.3); one by one they take
-// the sum of their plans.  Over 80
-// random sizes of a gradient (1 to 8192 tokens, 128 to 4096 values) the choice took
-// 1.6 % longer than the best and 26 % less than one by one; 5000 tokens of 2560
-// through 2560 features 350 us together and 385 us one by one, 4096 of 4096 through
-// 2048, which 256 blocks a product fill evenly, 382 and 369 us
-// (profiles/product_choice.txt).
+// the sum of their plans.  Over 80 random sizes of a gradient (1 to 8192 tokens,
+// 128 to 4096 values) the choice took 1.6 % longer than the best and 26 % less than
+// one by one; 5000 tokens of 2560 through 2560 features 350 us together and 385 us
+// one by one, 4096 of 4096 through 2048, which 256 blocks a product fill evenly, 382
+// and 369 us (profiles/product_choice.txt).
 struct JointTiles {
   int first, second;  // of kTileCosts
   float overlap;

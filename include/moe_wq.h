@@ -717,7 +717,8 @@ int moe_linear_i8(const void *x, const float *x_scales, int T, int N, int K,
  * by moe_linear_i8_kernel; "split tile ..": k is split over blocks and a second
  * kernel joins their sums.  all != 0: in a gradient call that asks for all three
  * outputs (GATE_UP and DH: with gate_up NULL); "joint 32x64 64x64": with others in
- * one launch, the tile of the first product and that of the others.
+ * one launch, the tile of the first product and that of the others; "fused
+ * 128x128": GATE_UP and DH of a tile in one block.
  * ------------------------------------------------------------------- */
 enum {
   MOE_GATED_GATE_UP = 0,   /* x Wgu^T and the activation */

@@ -298,6 +298,14 @@ struct ReadAhead<Epi, std::void_t<typename Epi::Ahead>> {
   static constexpr int kDepth = 64 / Type::kRegs;  // pieces in flight, in 64 registers
 };
 
+// Epilogues that keep values of a thread from one product of a block to the next
+// take the round's number last (Epi::kRounds of them): a thread has the same rows
+// and columns in every product of the same waves and tile.
+template <typename Epi, typename = void>
+struct ByRound : std::false_type {};
+template <typename Epi>
+struct ByRound<Epi, std::void_t<decltype(Epi::kRounds)>> : std::true_type {};
+
 // Epi: operator()(m, n, v) for eight consecutive n (N is a multiple of 8; the
 // direct kernel: four), or in the pair form operator()(m, n, first, second).
 // With Epi::Ahead: operator()(m, n, v, columns(n), ahead(m, n)).
@@ -527,7 +535,11 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
       const int round = i * kPasses + r, at_row = r * kPass + row, m = row_of(round);
       if (at_row < 16 && m < p.M && n < p.N) {
         const char* v = turn + at_row * kRow + 4 * at;
-        if constexpr (kDepth > 0)
+        if constexpr (ByRound<Epi>::value && kPair)
+          epi(m, n, *(const Acc8*)v, *(const Acc8*)(v + 4 * kWidth), round);
+        else if constexpr (ByRound<Epi>::value)
+          epi(m, n, *(const Acc8*)v, round);
+        else if constexpr (kDepth > 0)
           epi(m, n, *(const Acc8*)v, columns, early[round % kDepth]);
         else if constexpr (kPair)
           epi(m, n, *(const Acc8*)v, *(const Acc8*)(v + 4 * kWidth));

@@ -250,11 +250,11 @@ struct JointItem {
   int stages;
 };
 
-// Which of n choices of tiles, or -1: one by one.  extra: us that a joint launch
-// costs beside it.
+// Which of the choices of tiles, or -1: one by one; *took: the time.  extra: us
+// that a joint launch costs beside it.
 template <int kChoices, int kItems>
 inline int plan_joint(const JointTiles (&choices)[kChoices], const JointItem (&items)[kItems],
-                      float extra) {
+                      float extra, float* took) {
   float apart = 0.0f, best_us = 1e30f;
   int best = -1, wanted = 0;
   for (const JointItem& it : items) {
@@ -262,6 +262,7 @@ inline int plan_joint(const JointTiles (&choices)[kChoices], const JointItem (&i
     ++wanted;
     apart += plan_product(it.l, false, it.M, it.N, it.stages).us;
   }
+  *took = apart;
   if (wanted < 2) return -1;
   for (int c = 0; c < kChoices; ++c) {
     float longest = 0.0f, work = 0.0f, fixed = 0.0f;
@@ -282,7 +283,9 @@ inline int plan_joint(const JointTiles (&choices)[kChoices], const JointItem (&i
       best = c;
     }
   }
-  return best_us < apart ? best : -1;
+  if (best_us >= apart) return -1;
+  *took = best_us;
+  return best;
 }
 
 // (as kTileCosts has them)

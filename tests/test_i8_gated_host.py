@@ -245,7 +245,8 @@ def test_no_other_kernel_is_chosen(lib):
             assert moe.moe_gated_ffn_kernel(p, T, d, f) in GATED[p], (p, T, d, f)
         for p, joint in (("dx", "gradients"), ("dh", "recompute")):
             name = moe.moe_gated_ffn_kernel(p, T, d, f, all=True)
-            assert name in JOINT[joint] or not name.startswith("joint"), (p, T, d, f)
+            assert name in JOINT[joint] or not name.startswith(("joint", "fused")), (
+                p, T, d, f)
         assert moe.moe_linear_i8_kernel(T, 4 * d, 2 * f) in LINEAR, (T, d, f)
 
 

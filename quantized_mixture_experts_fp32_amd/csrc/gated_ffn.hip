@@ -16,10 +16,10 @@
 // Bound by the matrix cores for prompts and training, by the weights' bytes and the
 // launches' latency for few tokens.  bf16: 2501 tokens of 4096 through 2048 features
 // 110 us (1.15 PFLOP/s), 4096 tokens 159 us (1.30); the gradient of 4096 tokens 369
-// to 382 us (1.1), of which the product with the activation's gradient takes a
-// quarter: its epilogue moves 84 MB that no other block's products hide.  131 tokens
-// of 2048 through 1024, pre-activations computed again, 29 us in three launches
-// (five, product by product: 46 us).
+// us (1.1), of which the product with the activation's gradient takes a quarter: its
+// epilogue moves 84 MB that no other block's products hide.  Pre-activations
+// computed again: 131 tokens of 2048 through 1024 29 us in three launches (five,
+// product by product: 46 us), 4093 tokens from a checkpoint 161 us.
 #include "moe_wq.h"
 #include "mm_launch.hpp"
 

@@ -191,3 +191,88 @@ def test_two_graphs_of_one_workspace():
             graphs[i].replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
+
+
+@pytest.mark.parametrize("source", ["saved", "recompute", "checkpoint"])
+def test_offsets_beyond_32_bits(source):
+    """More than 2^31 values of x, h, gate_up and their gradients: only the last
+    rows hold anything, so an offset that wrapped would leave them wrong or the
+    others not zero."""
+    T, d, f, n = (1 << 21) + 77, 1032, 1032, 96
+    print(f"gated T={T} d={d} f={f} {source}", flush=True)
+    tail = block(n, d, f)
+    full = lambda t: torch.zeros(T, d, dtype=BF16, device=DEV).index_copy_(  # noqa: E731
+        0, torch.arange(T - n, T, device=DEV), t)
+    x, dout, w, v = full(tail["x"]), full(tail["dout"]), tail["w"], tail["v"]
+    q = {k: t.to(F64) for k, t in tail.items()}
+    out, kept = moe.moe_gated_ffn(x, w, v, save=True)
+    want, bound, gu, egu = ref.gated_ffn(q["x"], q["w"], q["v"])
+    ref.check("out", out[-n:], want, bound)
+    ref.check("gate_up", kept[-n:], gu, egu)
+    assert not out[:-n].any() and not kept[:-n].any()
+    del out
+    kw, x64, gu64 = {}, q["x"], None
+    if source == "saved":
+        kw["gate_up"], gu64 = kept, kept[-n:].to(F64)
+    else:
+        del kept
+    if source == "checkpoint":
+        x, kw["x_scales"] = moe.moe_quantize_i8(x)
+        x64 = ref.restore(x[-n:], kw["x_scales"][-n:])
+    got = moe.moe_gated_ffn_bwd(dout, x, w, v, **kw)
+    want, bounds = ref.gated_ffn_bwd(q["dout"], x64, q["w"], q["v"], gu64,
+                                     x_rounded=source == "checkpoint")
+    # (the weights' sums run over all tokens: as many more roundings, of zeros)
+    for name, a, b, e in zip(got._fields, got, want, bounds):
+        ref.check(name, a[-n:] if name == "dx" else a, b, e)
+    assert not got.dx[:-n].any()
+
+
+def test_linear_offsets_beyond_32_bits():
+    T, N, K, n = (1 << 20) + 33, 2056, 64, 70
+    print(f"linear_i8 T={T} N={N} K={K}", flush=True)
+    tail, codes, scales, _ = linear(n, N, K)
+    x = torch.zeros(T, K, dtype=BF16, device=DEV)
+    x[-n:] = tail
+    xq, xs = moe.moe_quantize_i8(tail, group=0)
+    want, e = ref.linear_i8(xq, xs, codes, scales, None)
+    got = moe.moe_linear_i8(x, codes, scales, out_dtype=moe.MOE_OUT_F32)
+    ref.check("out", got[-n:], want, ref.stored(want, e, True))
+    assert not got[:-n].any()
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_weights_beyond_32_bits(T):
+    """The largest weights that the call takes, zeros but for the first and last
+    features."""
+    d = f = 65536
+    print(f"gated T={T} d={d} f={f}", flush=True)
+    g = torch.Generator(DEV).manual_seed(T)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF16)  # noqa: E731
+    live = torch.cat((torch.arange(0, 8, device=DEV), torch.arange(f - 8, f, device=DEV)))
+    both = torch.cat((live, f + live))  # rows of w_gate_up
+    w = torch.zeros(2 * f, d, dtype=BF16, device=DEV)
+    w[both] = n(32, d) * 2 * d ** -0.5
+    v = torch.zeros(d, f, dtype=BF16, device=DEV)
+    v[live] = n(16, f)
+    x, dout = n(T, d), n(T, d)
+    out, kept = moe.moe_gated_ffn(x, w, v, save=True)
+    # the features that hold something, as a block of 16 features and 16 outputs
+    xs, ws = x.to(F64), w[both].to(F64)
+    vs = v[live][:, live].to(F64)
+    want, bound, gu, egu = ref.gated_ffn(xs, ws, vs)
+    ref.check("gate_up", kept[:, both], gu, egu)
+    ref.check("out", out[:, live], want, bound)
+    rest = torch.ones(d, dtype=torch.bool, device=DEV)
+    rest[live] = False
+    assert not out[:, rest].any() and not kept[:, :f][:, rest].any()
+    got = moe.moe_gated_ffn_bwd(dout, x, w, v, gate_up=kept)
+    # dout meets v's live rows only; dh of a feature that holds nothing gives no dx
+    # and, as its g and u are 0, no weight gradient
+    ds = dout[:, live].to(F64)
+    grads, bounds = ref.gated_ffn_bwd(ds, xs, ws, vs, kept[:, both].to(F64))
+    ref.check("dx", got.dx, grads[0], bounds[0])
+    ref.check("dw_gate_up", got.dw_gate_up[both], grads[1], bounds[1])
+    assert not got.dw_gate_up[8:f - 8].any() and not got.dw_gate_up[f + 8:2 * f - 8].any()
+    ref.check("dw_down", got.dw_down[live][:, live], grads[2], bounds[2])
+    assert not got.dw_down[:, rest].any()

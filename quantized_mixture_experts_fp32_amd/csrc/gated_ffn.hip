@@ -12,10 +12,9 @@
 //   dx = [dg du] Wgu,  dWgu = [dg du]^T x,  dWd = dout^T h
 // dg, du and h are rounded to bf16, the matrix cores' operand type, and so are a
 // restored checkpoint of x and an fp32 dout, which are operands too: results are
-// 2.4e-3 (bf16's own rounding is 1.7e-3) from 64 bits, from a checkpoint 3.4e-3; a
-// second product with what x's rounding leaves would take a quarter of the time
-// more.  All sums are fp32 in a fixed order, and g and u that are computed again
-// stay fp32.
+// 2.4e-3 (bf16's own rounding is 1.7e-3) from 64 bits, from a checkpoint 3.4e-3;
+// products with what x's rounding leaves would double the two largest of the five.
+// All sums are fp32 in a fixed order, and g and u that are computed again stay fp32.
 //
 // Bound by the matrix cores for prompts and training, by the weights' bytes and the
 // launches' latency for few tokens.  bf16: 2501 tokens of 4096 through 2048 features

@@ -1424,8 +1424,9 @@ class MoeLayer(_StepBuffers):
             if residual.is_cuda and stream.device != residual.device:
                 raise ValueError(f"forward_block: stream of {stream.device}, residual on "
                                  f"{residual.device}")
+            weights = () if shared is None else (shared.w_gate_up, shared.w_down)
             with _launch_on(stream, (residual, gain, add, post_gain, gate, next_gain, out,
-                                     next_out)):
+                                     next_out, *weights)):
                 return self.forward_block(residual, gain, eps, add, post_gain, gate, gate_mode,
                                           res_scale, next_gain, out, next_out, path,
                                           shared=shared)

@@ -199,8 +199,13 @@ __global__ __launch_bounds__(kDirectWaves* kWave, 4) void direct_kernel(const Di
   }
 }
 
+inline long long direct_blocks(long long N, bool pair) {
+  return (N + (pair ? 7 : 15)) / (pair ? 8 : 16);
+}
+// (a launch has fewer than 2^32 threads, 32 a feature here: N of 2^27 goes to a tile)
 inline bool direct_applies(long long T, long long N, long long row_bytes, bool pair) {
-  return T <= 16 && (pair ? N + 8 : 16) * row_bytes < (1LL << 31) - (1 << 20);
+  return T <= 16 && (pair ? N + 8 : 16) * row_bytes < (1LL << 31) - (1 << 20) &&
+         direct_blocks(N, pair) * (kDirectWaves * kWave) < 1LL << 32;
 }
 constexpr int kQuantRows = kDirectWaves;  // tokens that the quantising form takes
 
@@ -208,7 +213,7 @@ constexpr int kQuantRows = kDirectWaves;  // tokens that the quantising form tak
 template <typename Mma, bool kPair, bool kQuant, typename Epi>
 inline hipError_t launch_direct(DirectArgs p, const Epi& epi, hipStream_t s) {
   const int units = (p.kbytes + 127) >> 7;
-  const int blocks = (p.N + (kPair ? 7 : 15)) / (kPair ? 8 : 16);
+  const int blocks = (int)direct_blocks(p.N, kPair);
   const int most = blocks <= 256 ? kDirectLdsOne : kDirectLds;
   p.piece = std::min((p.kbytes + 255) & ~255, most / p.T & ~255);
   // (the last load into LDS may reach past the tokens)

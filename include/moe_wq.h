@@ -669,13 +669,15 @@ int moe_rmsnorm_bwd_i8(const void *dout, int dout_dtype, const int8_t *codes,
 /* ---------------------------------------------------------------------
  * moe_linear_i8 -- y = x W^T + bias with both operands in 8-bit integers, a
  * scale for each token and each feature.
- *   out[t][n] = sx[t] * sw[n] * sum_k qx[t][k] * qw[n][k] + bias[n]
+ *   out[t][n] = (sum_k qx[t][k] * qw[n][k] * sw[n]) * sx[t] + bias[n]
  * codes int8 [N][K] and scales fp32 [N] as moe_quantize_i8 returns them for the
  * rows of W with group_size 0; bias fp32 [N] or NULL; out [T][N] of out_dtype.
  * x: int8 codes [T][K] with x_scales fp32 [T], or (x_scales NULL) bf16 [T][K],
  * which the call quantizes by token first, as moe_quantize_i8 does.  The sum is
- * exact (int32); the scaling and the bias are fp32, rounded once on store.  A
- * token whose row holds an infinity or NaN gives a row of NaN.
+ * exact (int32); the scaling, in the order of the formula, and the bias are fp32,
+ * rounded once on store: as far apart as the two scales may be, no step loses
+ * bits to fp32's range before the result does (sw must be below 2^97).  A token
+ * whose row holds an infinity or NaN gives a row of NaN.
  * Requires K % 16 == 0, N % 8 == 0, K below 2^17, T below 2^23, N below 2^28,
  * T * K and T * N below 2^34.
  * ws / ws_bytes: at least moe_linear_i8_ws_bytes(T, N, K, x_scales != NULL),

@@ -1,8 +1,10 @@
 // Linear map in 8-bit integers: codes of the activations (a scale for each
 // token) times codes of the weights (a scale for each feature).
-//   out[t][n] = sx[t] sw[n] sum_k qx[t][k] qw[n][k] + bias[n]
-// The sum is exact in int32 (K below 2^17); the scales' product, its product
-// with the sum and the bias are fp32, rounded once on store.
+//   out[t][n] = (sum_k qx[t][k] qw[n][k] * sw[n]) * sx[t] + bias[n]
+// The sum is exact in int32 (K below 2^17); its products with sw and then sx and
+// the bias are fp32, rounded once on store.  In this order no step leaves fp32's
+// normal range before the result does (a sum is 0 or at least 1, and a scale of
+// the quantiser at least 2^-126; sw below 2^97).
 //
 // A library of its own (libmoe_wq_i8.so), which libmoe_wq.so is linked to: its
 // matrix instruction, 16 x 16 x 64, multiplies twice as fast as the one of 16 x
@@ -52,7 +54,7 @@ struct ScaleStore {
   __device__ __forceinline__ void put(int m, int n, I a, float s, V w, V b) const {
     V v;
 #pragma unroll
-    for (int r = 0; r < (int)(sizeof(I) / 4); ++r) v[r] = (float)a[r] * (s * w[r]);
+    for (int r = 0; r < (int)(sizeof(I) / 4); ++r) v[r] = (float)a[r] * w[r] * s;
     if (bias) v += b;
     store_as(out, f32, (size_t)m * N + n, v);
   }

@@ -714,7 +714,8 @@ int moe_linear_i8(const void *x, const float *x_scales, int T, int N, int K,
  * Both require d % 8 == 0, f % 8 == 0, d and f at most 65536, T below 2^23,
  * T * d below 2^34, T * f below 2^33.  ws / ws_bytes: at least the query's
  * bytes (dout_dtype, x_scales != NULL, gate_up != NULL), 256-byte aligned, no
- * contents carried between calls.
+ * contents carried between calls.  What is returned for T tokens serves fewer of
+ * them too.
  * moe_gated_ffn_kernel: the kernel that a product of these sizes runs, named as
  * by moe_linear_i8_kernel; "split tile ..": k is split over blocks and a second
  * kernel joins their sums.  all != 0: in a gradient call that asks for all three

@@ -1165,8 +1165,12 @@ def moe_gated_ffn(x, w_gate_up, w_down, out=None, out_dtype=MOE_OUT_BF16, save=F
 GatedFfnGrads = collections.namedtuple("GatedFfnGrads", "dx dw_gate_up dw_down")
 
 
+# (kept by size: the query goes through the choices of fewer tokens too, 2 to 150 us up
+# to 16384 tokens)
+@functools.lru_cache(4096)
 def moe_gated_ffn_bwd_ws_bytes(T, d, f, dout_dtype=MOE_OUT_BF16, x_quantized=False,
                                gate_up_kept=False):
+    """Bytes of workspace for T or fewer tokens."""
     return int(load_library().moe_gated_ffn_bwd_ws_bytes(T, d, f, dout_dtype, x_quantized,
                                                          gate_up_kept))
 
@@ -1206,8 +1210,8 @@ def moe_gated_ffn_bwd(dout, x, w_gate_up, w_down, x_scales=None, gate_up=None,
         dw_down = _out_rows(fn, "dw_down", dw_down, (d, f), dw_dtype, dout)
     lib = _lib or load_library()
     code = _code(dout)
-    ws = _workspace(fn, ws, lib.moe_gated_ffn_bwd_ws_bytes(T, d, f, code, x_scales is not None,
-                                                           gate_up is not None), dout)
+    ws = _workspace(fn, ws, moe_gated_ffn_bwd_ws_bytes(T, d, f, code, x_scales is not None,
+                                                       gate_up is not None), dout)
     rc = lib.moe_gated_ffn_bwd(dout.data_ptr(), code, x.data_ptr(), _addr(x_scales),
                                _addr(gate_up), w_gate_up.data_ptr(), w_down.data_ptr(), T, d, f,
                                _addr(dx), _addr(dw_gate_up), _addr(dw_down), dw_dtype,

@@ -943,8 +943,8 @@ size_t moe_gated_ffn_bwd_ws_bytes(int T, int d, int f, int dout_dtype, int x_qua
                                   int gate_up_kept) {
   int status;
   if (gated_refusal(T, d, f, &status)) return 0;
-  return moe::gated_ffn_bwd_ws_bytes(T, d, f, dout_dtype == MOE_OUT_F32, x_quantized != 0,
-                                     gate_up_kept != 0);
+  return moe::gated_ffn_bwd_ws_most(T, d, f, dout_dtype == MOE_OUT_F32, x_quantized != 0,
+                                    gate_up_kept != 0);
 }
 
 int moe_gated_ffn_bwd(const void* dout, int dout_dtype, const void* x, const float* x_scales,

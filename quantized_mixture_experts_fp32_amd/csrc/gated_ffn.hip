@@ -256,10 +256,15 @@ int plan_recompute(int T, int d, int f) {
   return best;
 }
 
-// Workspace of the gradient, in bytes from its start.
+// Bytes of split sums of the weights' gradients.
+size_t sums_bytes(int d, int f, int stages) {
+  return std::max(partial_bytes(2LL * f, d, stages), partial_bytes(d, f, stages));
+}
+
+// Workspace of the gradient, in bytes from its start; again: plan_recompute's.
 struct BwdSpace {
-  size_t dgu, h, gate_up, x, dout, dh, part, bytes;
-  BwdSpace(int T, int d, int f, int do_f32, int x_i8, int kept) {
+  size_t dgu, h, gate_up, x, dout, dh, part;
+  BwdSpace(int T, int d, int f, int do_f32, int x_i8, int kept, int again) {
     size_t at = 0;
     auto take = [&](bool wanted, size_t values, size_t size = 2) {
       const size_t p = at;
@@ -268,15 +273,12 @@ struct BwdSpace {
     };
     dgu = take(true, (size_t)T * 2 * f);
     h = take(true, (size_t)T * f);
-    const int again = kept || T == 0 ? -1 : plan_recompute(T, d, f);
     // fp32: not rounded on the way
     gate_up = take(!kept && again < kJointChoices, (size_t)T * 2 * f, 4);
     x = take(x_i8, (size_t)T * d);
     dout = take(do_f32, (size_t)T * d);
-    dh = take(again >= 0 && again < kJointChoices, (size_t)T * f, 4);
-    part = at;
-    bytes = at + std::max(partial_bytes(2LL * f, d, stages_of(T)),
-                          partial_bytes(d, f, stages_of(T)));
+    dh = take(!kept && again >= 0 && again < kJointChoices, (size_t)T * f, 4);
+    part = at;  // (the last)
   }
 };
 
@@ -303,12 +305,35 @@ const char* gated_ffn_kernel(int product, int T, int d, int f, bool all) {
 }
 
 size_t gated_ffn_bwd_ws_bytes(int T, int d, int f, int do_f32, int x_i8, int kept) {
-  return BwdSpace(T, d, f, do_f32, x_i8, kept).bytes;
+  const int again = kept || T == 0 ? -1 : plan_recompute(T, d, f);
+  return BwdSpace(T, d, f, do_f32, x_i8, kept, again).part + sums_bytes(d, f, stages_of(T));
+}
+
+size_t gated_ffn_bwd_ws_most(int T, int d, int f, int do_f32, int x_i8, int kept) {
+  size_t most = 0, sums = 0;
+  auto bytes = [&](int t, int again) { return BwdSpace(t, d, f, do_f32, x_i8, kept, again).part; };
+  // Every tile's rows are a multiple of 32, so over 32 tokens only the costs of what
+  // goes to memory grow: the choice goes from a joint launch, which takes the most, to
+  // one by one and to a fused kernel, which takes nothing more.
+  for (int t = T, step = 1; t > 0 && bytes(t, 0) > most; t -= step) {
+    const int first = (t - 1) / 32 * 32 + 1, again = kept ? -1 : plan_recompute(t, d, f);
+    most = std::max(most, bytes(t, again));
+    if (t == T || t % 32 == 0) {
+      const int least = kept ? -1 : plan_recompute(first, d, f);
+      step = bytes(t, least) > bytes(t, again) ? 1 : t - first + 1;
+    }
+  }
+  const size_t one = 4 * (size_t)(2 * f) * d;  // a split's sums, at most
+  // (so many splits at most of n stages, and of fewer)
+  for (int n = stages_of(T); splits_most(n) > 1 && splits_most(n) * one > sums; --n)
+    sums = std::max(sums, sums_bytes(d, f, n));
+  return most + sums;
 }
 
 hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) {
   const int T = a.T, d = a.d, f = a.f;
-  const BwdSpace at(T, d, f, a.do_f32, a.x_scales != nullptr, a.gate_up != nullptr);
+  const int again = a.gate_up || T == 0 ? -1 : plan_recompute(T, d, f);
+  const BwdSpace at(T, d, f, a.do_f32, a.x_scales != nullptr, a.gate_up != nullptr, again);
   auto place = [&](size_t p) { return (uint16_t*)((char*)ws + p); };
   uint16_t *dgu = place(at.dgu), *h = place(at.h);
   void* part = place(at.part);
@@ -329,7 +354,6 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
       x = place(at.x);
     }
     const Operand m = rows(dout, d, T), w = rows(a.w_down, f, f);
-    const int again = a.gate_up ? -1 : plan_recompute(T, d, f);
     if (again >= kJointChoices) {
       auto go = [&](auto shape_g, auto shape_h) {
         typedef decltype(shape_g) G;

@@ -238,7 +238,10 @@ struct GatedBwdArgs {
   void* dw_down;
   int dw_f32;
 };
+// What a call takes, and the most that one of so many or fewer tokens takes (the
+// kernels that T tokens choose may take less than those of fewer).
 size_t gated_ffn_bwd_ws_bytes(int T, int d, int f, int do_f32, int x_i8, int kept);
+size_t gated_ffn_bwd_ws_most(int T, int d, int f, int do_f32, int x_i8, int kept);
 hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s);
 
 // Canonical -> streaming code layouts (retile.hip).

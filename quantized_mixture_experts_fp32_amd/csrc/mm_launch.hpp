@@ -79,6 +79,9 @@ struct Plan {
   float us;    // what it takes
 };
 
+// Blocks that may share so many stages of k: 16, of eight stages each or more.
+inline int splits_most(int stages) { return std::min(16, std::max(1, stages / 8)); }
+
 // M rows and N columns (of B, so 2 f of the pair form), `stages` of k.
 inline Plan plan_product(Layout l, bool i8, long long M, long long N, int stages) {
   constexpr int kCUs = 256;
@@ -88,8 +91,7 @@ inline Plan plan_product(Layout l, bool i8, long long M, long long N, int stages
     const auto& c = kTileCosts[t].of[kind];
     if (c.one == 0) continue;
     const long long tiles = up(M, kTileCosts[t].bm) * up(N, kTileCosts[t].bn);
-    for (int k = 1; k <= (l == kOuterBoth ? 16 : 1); k *= 2) {
-      if (k > 1 && stages / k < 8) break;
+    for (int k = 1; k <= (l == kOuterBoth ? splits_most(stages) : 1); k *= 2) {
       const int per = std::max((int)up(stages, k), 1), splits = std::max((int)up(stages, per), 1);
       const float n = (float)up(tiles * splits, kCUs);
       const float us = c.fixed + c.block * n + per * std::max(c.one, c.each * n) +

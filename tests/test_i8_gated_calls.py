@@ -1,6 +1,8 @@
 """CPU tests of the shared expert's calls around their kernels: what is recorded
-on a side stream, and which kernel takes the largest sizes."""
+on a side stream, which kernel takes the largest sizes, and what a workspace
+holds."""
 import contextlib
+import ctypes
 import os
 import re
 
@@ -80,3 +82,39 @@ def test_every_size_can_be_launched(lib, K):
     # (the few-token kernel forms up to 8 tokens' codes by itself, the tiles do not)
     assert moe.moe_linear_i8_ws_bytes(1, (1 << 27) - 16, K) == 0
     assert moe.moe_linear_i8_ws_bytes(1, 1 << 27, K) >= K + 4
+
+
+# ------------------------------------------------------------- the workspaces
+def needed(lib, T, d, f, do_f32, x_i8, kept):
+    """What the gradient asks for, from its refusal of a workspace of no bytes."""
+    p = ctypes.c_void_p(0x10000)
+    rc = lib.moe_gated_ffn_bwd(p, int(do_f32), p, p if x_i8 else None, p if kept else None, p, p,
+                               T, d, f, p, p, p, 0, p, 0, None)
+    if rc == moe.MOE_OK or rc != moe.MOE_ERR_WORKSPACE:
+        raise AssertionError(rc)
+    return int(re.search(rb"< (\d+) bytes", lib.moe_last_error())[1])
+
+
+@pytest.mark.parametrize("form", [(0, 0, 0), (0, 0, 1), (1, 1, 0)])
+@pytest.mark.parametrize("d,f", [(2048, 1024), (256, 1824), (264, 2288), (4096, 136), (72, 136),
+                                 (2224, 152)])
+def test_a_workspace_serves_smaller_batches(lib, d, f, form):
+    """A workspace for T tokens is large enough for fewer of them, whichever
+    kernels these choose."""
+    last = 0
+    step = lambda T: 1 if T < 300 else 37 if T < 3000 else 173  # noqa: E731
+    T = 1
+    while T < 17000:
+        at = moe.moe_gated_ffn_bwd_ws_bytes(T, d, f, *form)
+        assert at >= last and at >= needed(lib, T, d, f, *form), (T, last, at)
+        last, T = at, T + step(T)
+
+
+def test_a_workspace_is_not_larger_than_needed(lib):
+    """The largest need of so many or fewer tokens: here found one by one."""
+    for T in (4, 131, 512, 700, 1024, 2600):
+        most = max(needed(lib, t, 2048, 1024, 0, 0, 0) for t in range(1, T + 1))
+        assert moe.moe_gated_ffn_bwd_ws_bytes(T, 2048, 1024) == most
+    for T in (64, 8000):
+        assert moe.moe_gated_ffn_bwd_ws_bytes(T, 4096, 2048, 0, False, True) == needed(
+            lib, T, 4096, 2048, 0, 0, 1)

@@ -60,13 +60,15 @@ _lib = None
 
 
 def load_library():
-    """Load libmoe_wq.so; raise if it has not been built."""
+    """Load libmoe_wq.so (and with it libmoe_wq_i8.so beside it); raise if they have
+    not been built."""
     global _lib
     if _lib is not None:
         return _lib
-    if not os.path.exists(LIB_PATH):
-        raise RuntimeError(f"{LIB_PATH} not built: run "
-                           "quantized_mixture_experts_fp32_amd.build.build()")
+    for path in (LIB_PATH, os.path.join(os.path.dirname(LIB_PATH), "libmoe_wq_i8.so")):
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} not built: run "
+                               "quantized_mixture_experts_fp32_amd.build.build()")
     lib = ctypes.CDLL(LIB_PATH)
     i32, vp, sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
     lib.moe_status_str.argtypes, lib.moe_status_str.restype = [i32], ctypes.c_char_p

@@ -36,16 +36,15 @@ def _run(what, cmd):
 
 
 def _link(lib, objects, *more):
-    tmp = lib + ".tmp"
     _run(f"{os.path.basename(lib)} link",
-         [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objects, *more])
-    os.replace(tmp, lib)
+         [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", lib, *objects, *more])
 
 
 def build(verbose: bool = False) -> str:
     sources = SOURCES + SOURCES_I8
-    with tempfile.TemporaryDirectory() as objects:
-        out = [os.path.join(objects, s + ".o") for s in sources]
+    # beside the libraries, which are both replaced when both are there
+    with tempfile.TemporaryDirectory(dir=os.path.dirname(LIB), prefix=".build_") as made:
+        out = [os.path.join(made, s + ".o") for s in sources]
 
         def compile_one(s, o):
             return _run(f"{s} build", [HIPCC, *FLAGS, "-c", os.path.join(CSRC, s), "-o", o])
@@ -56,9 +55,12 @@ def build(verbose: bool = False) -> str:
                 if verbose:
                     print(said)
         n = len(SOURCES)
-        _link(LIB_I8, out[n:], "-Wl,-soname," + os.path.basename(LIB_I8))
+        lib, lib_i8 = (os.path.join(made, os.path.basename(p)) for p in (LIB, LIB_I8))
+        _link(lib_i8, out[n:], "-Wl,-soname," + os.path.basename(LIB_I8))
         # found beside the library, here and wherever both are copied
-        _link(LIB, out[:n], LIB_I8, "-Wl,-rpath,$ORIGIN")
+        _link(lib, [*out[:n], lib_i8], "-Wl,-rpath,$ORIGIN")
+        os.replace(lib_i8, LIB_I8)
+        os.replace(lib, LIB)
     return LIB
 
 

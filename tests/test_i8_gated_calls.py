@@ -1,22 +1,23 @@
 """CPU tests of the shared expert's calls around their kernels: what is recorded
-on a side stream, which kernel takes the largest sizes, and what a workspace
-holds."""
+on a side stream, which kernel takes the largest sizes, what a workspace holds,
+and the two libraries."""
 import contextlib
 import ctypes
 import os
 import re
+import shutil
 
 import pytest
 import torch
 
 import quantized_mixture_experts_fp32_amd as moe
+from quantized_mixture_experts_fp32_amd import build as package_build
 
 
 @pytest.fixture(scope="module")
 def lib():
     if not os.path.exists(moe.LIB_PATH):
-        from quantized_mixture_experts_fp32_amd import build
-        build.build()
+        package_build.build()
     return moe.load_library()
 
 
@@ -118,3 +119,42 @@ def test_a_workspace_is_not_larger_than_needed(lib):
     for T in (64, 8000):
         assert moe.moe_gated_ffn_bwd_ws_bytes(T, 4096, 2048, 0, False, True) == needed(
             lib, T, 4096, 2048, 0, 0, 1)
+
+
+# ---------------------------------------------------------- the two libraries
+@pytest.mark.parametrize("there", [(), ("libmoe_wq.so",), ("libmoe_wq_i8.so",)])
+def test_a_missing_library_is_named(lib, tmp_path, monkeypatch, there):
+    for name in there:
+        shutil.copy(os.path.join(moe.HERE, name), tmp_path / name)
+    monkeypatch.setattr(moe, "_lib", None)
+    monkeypatch.setattr(moe, "LIB_PATH", str(tmp_path / "libmoe_wq.so"))
+    missing = "libmoe_wq_i8.so" if there == ("libmoe_wq.so",) else "libmoe_wq.so"
+    with pytest.raises(RuntimeError, match=f"{missing} not built: run"):
+        moe.load_library()
+
+
+@pytest.mark.parametrize("fails", ["linear_i8.hip build", "libmoe_wq_i8.so link",
+                                   "libmoe_wq.so link", None])
+def test_a_failed_build_replaces_neither_library(tmp_path, monkeypatch, fails):
+    """The libraries are of one build: both new, or both as they were."""
+    libs = [tmp_path / "libmoe_wq.so", tmp_path / "libmoe_wq_i8.so"]
+    for p in libs:
+        p.write_text("old")
+
+    def run(what, cmd):
+        if what == fails:
+            raise RuntimeError(what)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("new")
+        return ""
+
+    monkeypatch.setattr(package_build, "_run", run)
+    monkeypatch.setattr(package_build, "LIB", str(libs[0]))
+    monkeypatch.setattr(package_build, "LIB_I8", str(libs[1]))
+    if fails:
+        with pytest.raises(RuntimeError, match=fails):
+            package_build.build()
+    else:
+        package_build.build()
+    assert [p.read_text() for p in libs] == ["old" if fails else "new"] * 2
+    assert sorted(os.listdir(tmp_path)) == ["libmoe_wq.so", "libmoe_wq_i8.so"]

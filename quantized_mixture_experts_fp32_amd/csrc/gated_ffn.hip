@@ -157,7 +157,7 @@ __global__ __launch_bounds__(256) void gated_bwd_kernel(const float* __restrict_
   const int per = epi.f / 8;
   if (i >= (long long)T * per) return;
   const int m = (int)(i / per), n = 8 * (int)(i % per);
-  epi(m, n, load_as<f32x8>(dh, 1, 8 * (size_t)i), {}, epi.ahead(m, n));
+  epi(m, n, load_f32<f32x8>(dh, 8 * (size_t)i), {}, epi.ahead(m, n));
 }
 
 // fp32 rows to bf16, eight values a thread.
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(256) void to_bf16_kernel(const float* __restrict__ 
                                                       uint16_t* __restrict__ out) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   if (i >= chunks) return;
-  store_as(out, 0, 8 * (size_t)i, load_as<f32x8>(x, 1, 8 * (size_t)i));
+  store_as(out, 0, 8 * (size_t)i, load_f32<f32x8>(x, 8 * (size_t)i));
 }
 
 size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }

@@ -36,7 +36,9 @@ struct ScaleStore {
     static constexpr int kRegs = 1;
     float s;
   };
-  __device__ __forceinline__ Columns columns(int n) const { return {load_as<f32x8>(sw, 1, n), bias_at<f32x8>(n)}; }
+  __device__ __forceinline__ Columns columns(int n) const {
+    return {load_f32<f32x8>(sw, n), bias_at<f32x8>(n)};
+  }
   __device__ __forceinline__ Ahead ahead(int m, int) const { return {sx[m]}; }
   __device__ __forceinline__ void operator()(int m, int n, i32x8 a, const Columns& c,
                                              const Ahead& r) const {
@@ -44,11 +46,11 @@ struct ScaleStore {
   }
   // (the kernel for few tokens: four columns, read in place)
   __device__ __forceinline__ void operator()(int m, int n, i32x4 a) const {
-    put(m, n, a, sx[m], load_as<f32x4>(sw, 1, n), bias_at<f32x4>(n));
+    put(m, n, a, sx[m], load_f32<f32x4>(sw, n), bias_at<f32x4>(n));
   }
   template <typename V>
   __device__ __forceinline__ V bias_at(int n) const {
-    return bias ? load_as<V>(bias, 1, n) : V(0.0f);
+    return bias ? load_f32<V>(bias, n) : V(0.0f);
   }
   template <typename I, typename V>
   __device__ __forceinline__ void put(int m, int n, I a, float s, V w, V b) const {

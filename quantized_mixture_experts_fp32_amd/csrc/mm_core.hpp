@@ -39,8 +39,6 @@ namespace mm {
 using row::f32x8;
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
-typedef int16_t i16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStageBytes = 128;  // bytes of k a stage, K-inner
 constexpr int kStageK = 64;       // rows of k a stage, K-outer
@@ -214,18 +212,14 @@ struct I8 {
   }
 };
 
-// Four or eight consecutive values (V: f32x4, f32x8) of an array that is fp32 or
-// bf16 (stored: round to nearest even).
+// Four or eight consecutive values (V: f32x4, f32x8) of an fp32 array, and to one that
+// is fp32 or bf16 (round to nearest even).
 template <typename V>
-__device__ __forceinline__ V load_as(const void* p, int f32, size_t i) {
-  if constexpr (sizeof(V) == 32) {
-    return f32 ? row::load8<true>(p, i) : row::load8<false>(p, i);
-  } else {
-    if (f32) return *(const V*)((const float*)p + i);
-    const u32x2 w = *(const u32x2*)((const uint16_t*)p + i);
-    return V{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
-             __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u)};
-  }
+__device__ __forceinline__ V load_f32(const float* p, size_t i) {
+  if constexpr (sizeof(V) == 32)
+    return row::load8<true>(p, i);
+  else
+    return *(const V*)(p + i);
 }
 template <typename V>
 __device__ __forceinline__ void store_as(void* p, int f32, size_t i, V v) {

@@ -706,7 +706,8 @@ int moe_linear_i8(const void *x, const float *x_scales, int T, int N, int K,
  * dw_gate_up [2f][d] and dw_down [d][f] of dw_dtype (overwritten, zeros for
  * T == 0).
  *   x: bf16 [T][d], or (x_scales not NULL) codes of moe_quantize_i8 with
- *     group_size 128, restored and rounded to bf16.
+ *     group_size 128: pre-activations are of the restored rows as they are, the
+ *     product of dw_gate_up takes them rounded to bf16.
  *   gate_up: as the forward call left it, or NULL: computed again from x.
  * dg, du and h are rounded to bf16 between the products.  The sizes and the
  * outputs that are asked for choose the kernels, and so the order of the fp32

@@ -10,10 +10,14 @@
 //   dh = dout Wd
 //   du = dh g s,  dg = dh u s (1 + g (1 - s)),  h = g s u       (its epilogue)
 //   dx = [dg du] Wgu,  dWgu = [dg du]^T x,  dWd = dout^T h
-// dg, du and h are rounded to bf16, the matrix cores' operand type, and so are a
-// restored checkpoint of x and an fp32 dout, which are operands too: results are
-// 2.4e-3 (bf16's own rounding is 1.7e-3) from 64 bits, from a checkpoint 3.4e-3;
-// products with what x's rounding leaves would double the two largest of the five.
+// dg, du and h are rounded to bf16, the matrix cores' operand type, and so is an fp32
+// dout, which is an operand too: results are 2.4e-3 (bf16's own rounding is 1.7e-3)
+// from 64 bits.  g and u of an 8-bit checkpoint are formed from its codes and the
+// scales (mm_core.hpp, kScaled), so that its rows are rounded to bf16 for dWgu alone,
+// which is 2.9e-3 from 64 bits: there the scale changes along the sum, from token to
+// token, and a second product with what the rounding leaves would cost a fifth of the
+// gradient's time.  (Rounded for all of them: 3.0e-3, 3.4e-3 and 3.3e-3 for dx, dWgu and
+// dWd.  Scaling sums costs 1 to 5 %: 4093 tokens of 2048 through 1024 164 -> 170 us.)
 // All sums are fp32 in a fixed order, and g and u that are computed again stay fp32.
 //
 // Bound by the matrix cores for prompts and training, by the weights' bytes and the
@@ -22,7 +26,7 @@
 // us (1.1), of which the product with the activation's gradient takes a quarter: its
 // epilogue moves 84 MB that no other block's products hide.  Pre-activations
 // computed again: 131 tokens of 2048 through 1024 29 us in three launches (five,
-// product by product: 46 us), 4093 tokens from a checkpoint 161 us.
+// product by product: 44 us), 4093 tokens from a checkpoint 167 to 175 us.
 #include "moe_wq.h"
 #include "mm_launch.hpp"
 
@@ -133,7 +137,7 @@ struct KeptBwdStore {
 
 // Gate, up and dh of a tile, one after the other in one block, so that the
 // pre-activations that are computed again stay in registers.
-template <typename ShG, typename ShH>
+template <typename ShG, typename ShH, bool kScaled>
 __global__ __launch_bounds__(ShG::kThreads, ShG::kThreads / 256) void recompute_kernel(
     const Problem gu, const Problem dh, uint16_t* __restrict__ dgu, uint16_t* __restrict__ h,
     int f) {
@@ -143,10 +147,11 @@ __global__ __launch_bounds__(ShG::kThreads, ShG::kThreads / 256) void recompute_
   constexpr int kR = ShG::BM / ShG::WM / 16 * ((16 + kPass - 1) / kPass);
   extern __shared__ __align__(1024) char lds[];
   Kept<kR> kept;
-  product_block<Bf16, ShG, false, false, true>(gu, KeepStore<kR>{kept}, lds, blockIdx.x, 0);
+  product_block<Bf16, ShG, false, false, true, kScaled>(gu, KeepStore<kR>{kept}, lds, blockIdx.x,
+                                                        0);
   __syncthreads();  // every wave's rows are turned around
-  product_block<Bf16, ShH, false, true, false>(dh, KeptBwdStore<kR>{kept, dgu, h, f}, lds,
-                                               blockIdx.x, 0);
+  product_block<Bf16, ShH, false, true, false, false>(dh, KeptBwdStore<kR>{kept, dgu, h, f}, lds,
+                                                      blockIdx.x, 0);
 }
 
 // dh -> dg, du and h where dh and the pre-activations come from one launch; eight
@@ -263,7 +268,7 @@ size_t sums_bytes(int d, int f, int stages) {
 
 // Workspace of the gradient, in bytes from its start; again: plan_recompute's.
 struct BwdSpace {
-  size_t dgu, h, gate_up, x, dout, dh, part;
+  size_t dgu, h, gate_up, x, whole, unit, dout, dh, part;
   BwdSpace(int T, int d, int f, int do_f32, int x_i8, int kept, int again) {
     size_t at = 0;
     auto take = [&](bool wanted, size_t values, size_t size = 2) {
@@ -276,6 +281,8 @@ struct BwdSpace {
     // fp32: not rounded on the way
     gate_up = take(!kept && again < kJointChoices, (size_t)T * 2 * f, 4);
     x = take(x_i8, (size_t)T * d);
+    whole = take(x_i8 && !kept, (size_t)T * d);
+    unit = take(x_i8 && !kept, (size_t)T * up(d, 128), 4);
     dout = take(do_f32, (size_t)T * d);
     dh = take(!kept && again >= 0 && again < kJointChoices, (size_t)T * f, 4);
     part = at;  // (the last)
@@ -348,22 +355,34 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
       if ((e = hipGetLastError()) != hipSuccess) return e;
       dout = place(at.dout);
     }
+    Operand tokens = rows(x, d, T);  // of gate and up
     if (a.x_scales && (!a.gate_up || a.dw_gate_up)) {
-      e = launch_dequantize_i8((const int8_t*)a.x, a.x_scales, T, d, 0, place(at.x), 0, s);
+      uint16_t *whole = a.gate_up ? nullptr : place(at.whole),
+               *restored = a.dw_gate_up ? place(at.x) : nullptr;
+      float* unit = (float*)place(at.unit);
+      e = launch_unpack_i8((const int8_t*)a.x, a.x_scales, T, d, whole, unit, restored, s);
       if (e != hipSuccess) return e;
-      x = place(at.x);
+      tokens = {(const char*)whole, nullptr, 2LL * d, T, unit};
+      x = restored;
     }
+    // the choice's call of a kernel whose tokens are an 8-bit checkpoint's, or not
+    auto by_tokens = [&](auto call) {
+      return a.x_scales ? call(std::true_type{}) : call(std::false_type{});
+    };
     const Operand m = rows(dout, d, T), w = rows(a.w_down, f, f);
     if (again >= kJointChoices) {
       auto go = [&](auto shape_g, auto shape_h) {
         typedef decltype(shape_g) G;
         typedef decltype(shape_h) H;
         const Problem gu =
-            part_of<G, kInner, true>(rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d, 0).p;
+            part_of<G, kInner, true>(tokens, pairs(a.w_gate_up, d, f), T, f, d, 0).p;
         const Problem dh = part_of<H, kOuterB, false>(m, w, T, f, d, 0).p;
-        hipLaunchKernelGGL((recompute_kernel<G, H>), dim3(gu.nm * gu.nn), dim3(G::kThreads),
-                           std::max(G::kLds, H::kLds), s, gu, dh, dgu, h, f);
-        return hipGetLastError();
+        return by_tokens([&](auto scaled) {
+          hipLaunchKernelGGL((recompute_kernel<G, H, decltype(scaled)::value>),
+                             dim3(gu.nm * gu.nn), dim3(G::kThreads), std::max(G::kLds, H::kLds), s,
+                             gu, dh, dgu, h, f);
+          return hipGetLastError();
+        });
       };
       if (again == kJointChoices)  // (as kFused has them)
         e = go(Shape<128, 128, 2, 2, 2, 1, 1>{}, Shape<128, 64, 2, 2, 2, 1, 1>{});
@@ -372,12 +391,15 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
     } else if (again >= 0) {
       auto go = [&](auto tile) {
         typedef typename TileShape<decltype(tile)::value>::Type Sh;
-        const auto gu = part_of<Sh, kInner, true>(rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d,
-                                                  GatedStore{nullptr, place(at.gate_up), 1, f});
         const auto dh = part_of<Sh, kOuterB, false>(m, w, T, f, d, Store{place(at.dh), f, 1});
         auto none = dh;
         none.blocks = 0;
-        return launch_joint(gu, dh, none, s);
+        return by_tokens([&](auto scaled) {
+          const auto gu = part_of<Sh, kInner, true, decltype(scaled)::value>(
+              tokens, pairs(a.w_gate_up, d, f), T, f, d,
+              GatedStore{nullptr, place(at.gate_up), 1, f});
+          return launch_joint(gu, dh, none, s);
+        });
       };
       switch (again) {  // (as kRecompute has them)
         case 0: e = go(Tile<7>{}); break;
@@ -394,9 +416,11 @@ hipError_t launch_gated_ffn_bwd(const GatedBwdArgs& a, void* ws, hipStream_t s) 
       e = launch_product<Bf16, kOuterB, false>(
           m, w, T, f, d, 2, GatedBwdStore<false>{a.gate_up, dgu, h, f}, nullptr, s);
     } else {
-      e = launch_product<Bf16, kInner, true>(
-          rows(x, d, T), pairs(a.w_gate_up, d, f), T, f, d, 2,
-          GatedStore{nullptr, place(at.gate_up), 1, f}, nullptr, s);
+      e = by_tokens([&](auto scaled) {
+        return launch_product<Bf16, kInner, true, decltype(scaled)::value>(
+            tokens, pairs(a.w_gate_up, d, f), T, f, d, 2,
+            GatedStore{nullptr, place(at.gate_up), 1, f}, nullptr, s);
+      });
       if (e != hipSuccess) return e;
       e = launch_product<Bf16, kOuterB, false>(
           m, w, T, f, d, 2, GatedBwdStore<true>{place(at.gate_up), dgu, h, f}, nullptr, s);

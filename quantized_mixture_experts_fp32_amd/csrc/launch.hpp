@@ -203,6 +203,12 @@ hipError_t launch_quantize_i8(const void* x, int x_f32, int T, int K, int by_row
                               float* scales, hipStream_t s);
 hipError_t launch_dequantize_i8(const int8_t* codes, const float* scales, int T, int K, int by_row,
                                 void* out, int out_f32, hipStream_t s);
+// An 8-bit checkpoint (a scale for each 128) as what the gated block's gradient
+// multiplies: whole = code * 2^e, exact in bf16, in units of unit = scale / 2^e in
+// [1, 2), [ceil(K/128)][T]; restored = code * scale rounded to bf16.  whole (with unit)
+// or restored null: not wanted.
+hipError_t launch_unpack_i8(const int8_t* codes, const float* scales, int T, int K,
+                            uint16_t* whole, float* unit, uint16_t* restored, hipStream_t s);
 
 // Linear map in 8-bit integers (quant_i8.hip).  x_scales null: x is bf16 and
 // quantised by row, into ws or (product_i8_quantizes) on its way into the product.

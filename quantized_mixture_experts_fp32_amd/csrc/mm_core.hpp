@@ -21,6 +21,11 @@
 //     8192^3 with both operands outer 888 us, this way 828 us).  Sixteen-byte chunk c
 //     lies at c ^ s(k), which keeps the four octets of k on different banks.
 //
+// kScaled: A (K-inner) holds whole numbers of a unit in [1, 2) for each 128 values of
+// a row, two stages.  Sums are in the unit of their last stage: a ratio of two units
+// takes them from one to the next, and they are multiplied by the last one at the
+// end.  So rows restored from 8-bit codes are not rounded to bf16 on their way here.
+//
 // Bound by the matrix cores where a launch fills the chip and k is long: bf16, the
 // gated block's two products of 8192 tokens of 8192 values through 4096 features
 // 1172 us, 1.41 PFLOP/s (the library's product 8192^3 713 us, 1.54, on the same
@@ -50,6 +55,7 @@ struct Operand {
   const char* p2;      // second matrix, interleaved by 16 rows (pair form), or null
   long long stride;    // bytes between rows
   int rows;            // rows of the product (m or n), per matrix
+  const float* unit = nullptr;  // (kScaled) of each two stages of a row, [..][rows]
 };
 
 typedef __attribute__((address_space(3))) void* Lds;
@@ -201,6 +207,7 @@ struct Bf16 {
   static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
     return mfma16(as_bf16x8(a), as_bf16x8(b), c);
   }
+  static __device__ __forceinline__ f32x4 times(f32x4 c, float f) { return c * f; }
 };
 struct I8 {
   typedef int32_t Value;
@@ -210,6 +217,7 @@ struct I8 {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
                                                  __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
   }
+  static __device__ __forceinline__ Acc times(Acc c, float) { return c; }  // (not called)
 };
 
 // Four or eight consecutive values (V: f32x4, f32x8) of an fp32 array, and to one that
@@ -304,7 +312,8 @@ struct ByRound<Epi, std::void_t<decltype(Epi::kRounds)>> : std::true_type {};
 // direct kernel: four), or in the pair form operator()(m, n, first, second).
 // With Epi::Ahead: operator()(m, n, v, columns(n), ahead(m, n)).
 // id: the block's among the tiles' blocks; part: its share of k.
-template <typename Mma, typename Sh, bool kAOuter, bool kBOuter, bool kPair, typename Epi>
+template <typename Mma, typename Sh, bool kAOuter, bool kBOuter, bool kPair, bool kScaled,
+          typename Epi>
 __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, char* lds, int id,
                                               int part) {
   constexpr int TM = Sh::BM / Sh::WM, TN = Sh::BN / Sh::WN, MI = TM / 16, NI = TN / 16;
@@ -369,14 +378,51 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
     else
       ra.read(f.a, ring + at_a.get * kA, r - kReadsB, ks);
   };
+  // A lane has the units of rows lane, lane + 64 of the wave's.
+  constexpr int kUnits = kScaled ? (TM + 63) / 64 : 1;
+  struct Units {
+    float v[kUnits];
+  } unit, after_unit, ahead;  // of the sums, of the next stage, of the one after it
+  float factor[MI];           // from the first to the second, of a fragment's rows
+  auto units_of = [&](int kt) {
+    const int stage = min(stage0 + Sh::G * kt, p.stages - 1);
+    Units u;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      int row = m0 + wm * TM + 64 * i + lane;
+      asm volatile("" : "+v"(row));  // (not kept in a register)
+      row = min(row, p.M - 1);
+      u.v[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          rsrc_of((const char*)p.a.unit), 4 * row, 4 * p.M * (stage >> 1), 0));
+    }
+    return u;
+  };
+  auto by_fragment = [&](const Units& u) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      factor[i] = __shfl(u.v[16 * i / 64], (16 * i + (lane & 15)) & 63, kWave);
+  };
+  if constexpr (kScaled) {
+    unit = after_unit = units_of(0);
+    ahead = units_of(1);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) factor[i] = 1.0f;
+  }
   // The products of one k step; between its rows the fragments of the next step
   // are asked for (in its first rows) and, `loads`, the next stage's loads: all
   // at once they would hold the wave up while the memory pipe takes them in.
   constexpr int kHalf = (MI + 1) / 2;
   // An outer operand's fragments are made one row of products ahead.
   u32x4 b[NI], a;
-  auto multiply = [&](const Frags& f, Frags& next, int ks, auto from, auto to) {
+  // Rows of sums that go to another unit first do so behind the products of the row
+  // before them.
+  auto multiply = [&](const Frags& f, Frags& next, int ks, auto from, auto to, auto rescale) {
     constexpr int kFrom = decltype(from)::value, kMore = decltype(to)::value - kFrom;
+    constexpr bool kRescale = decltype(rescale)::value;
+    if constexpr (kRescale) {
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[0][j] = Mma::times(acc[0][j], factor[0]);
+    }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       if (i < kHalf)
@@ -392,6 +438,10 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
         acc[i][j] = Mma::mma(b[j], a, acc[i][j]);
+        if constexpr (kRescale) {
+          if (i + 1 < MI) acc[i + 1][j] = Mma::times(acc[i + 1][j], factor[i + 1]);
+          if (MI < 8) __builtin_amdgcn_sched_barrier(0);  // (256 x 256 would spill)
+        }
         if constexpr (kAOuter) {
 #pragma unroll
           for (int q = j * 4 / NI; q < (j + 1) * 4 / NI; ++q)
@@ -426,12 +476,15 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
   a = ra.get(f0.a, 0);
 #pragma unroll
   for (int j = 0; j < NI; ++j) b[j] = rb.get(f0.b, j);
-  for (int kt = 0; kt < count; ++kt) {
+  // One stage.  kScaled: the first or the last of its group, of this wave's stages.
+  constexpr std::false_type kNo{};
+  auto step = [&](int kt, auto first, auto last) __attribute__((always_inline)) {
+    if constexpr (decltype(first)::value) unit = after_unit;
     if constexpr (kApart) {
-      multiply(f0, f1, 1, kBetween, kLast);
+      multiply(f0, f1, 1, kBetween, kLast, first);
       asked_b();
     } else {
-      multiply(f0, f1, 1, kFirst, kFirst);
+      multiply(f0, f1, 1, kFirst, kFirst, first);
     }
     // this wave's loads of the next stage are through (behind them are S - 2
     // stages' loads, or B's loads of this half), and its reads of the one that
@@ -441,13 +494,36 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
     __builtin_amdgcn_sched_barrier(0);
     at_a.get = after(at_a.get, Sh::S);
     at_b.get = after(at_b.get, Sh::SB);
+    // (units are asked for between two stages' loads, so that no wait is longer)
+    if constexpr (decltype(last)::value) {
+      after_unit = ahead;
+      Units ratio;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+        ratio.v[i] = unit.v[i] * __builtin_amdgcn_rcpf(after_unit.v[i]);
+      by_fragment(ratio);
+    }
+    if constexpr (decltype(first)::value && !kApart) ahead = units_of(kt + 2);
+    if constexpr (kScaled) __builtin_amdgcn_sched_barrier(0);
     if constexpr (kApart) {
-      multiply(f1, f0, 0, kFirst, kBetween);
+      multiply(f1, f0, 0, kFirst, kBetween, kNo);
     } else {
-      multiply(f1, f0, 0, kFirst, kLast);
+      multiply(f1, f0, 0, kFirst, kLast, kNo);
       asked_b();
     }
     asked_a();
+    if constexpr (decltype(first)::value && kApart) ahead = units_of(kt + 2);
+  };
+  if constexpr (kScaled) {
+    constexpr std::true_type kYes{};
+    constexpr std::integral_constant<bool, (Sh::G > 1)> kEach{};  // (a group a stage)
+    for (int kt = 0; kt < count; kt += 2) {
+      step(kt, kYes, kEach);
+      if (kt + 1 == count) break;
+      step(kt + 1, kEach, kYes);
+    }
+  } else {
+    for (int kt = 0; kt < count; ++kt) step(kt, kNo, kNo);
   }
   typedef typename Mma::Acc8 Acc8;
   constexpr int kRow = TN * 4 + 16, kWidth = kPair ? TN / 2 : TN;  // features of the wave
@@ -477,6 +553,13 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) asm volatile("" : "+v"(acc[i][j]));
+  if constexpr (kScaled) {
+    by_fragment(unit);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = Mma::times(acc[i][j], factor[i]);
+  }
   if constexpr (Sh::G > 1) {
     typedef typename Mma::Acc Quad;
     Quad* red = (Quad*)lds + wave * (MI * NI * 64) + lane;
@@ -547,16 +630,17 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
   }
 }
 
-template <typename Mma, typename Sh, bool kAOuter, bool kBOuter, bool kPair, typename Epi>
+template <typename Mma, typename Sh, bool kAOuter, bool kBOuter, bool kPair, bool kScaled,
+          typename Epi>
 __global__ __launch_bounds__(Sh::kThreads, Sh::kThreads / 256) void product_kernel(
     const Problem p, const Epi epi) {
   extern __shared__ __align__(1024) char lds[];
-  product_block<Mma, Sh, kAOuter, kBOuter, kPair>(p, epi, lds, blockIdx.x, blockIdx.y);
+  product_block<Mma, Sh, kAOuter, kBOuter, kPair, kScaled>(p, epi, lds, blockIdx.x, blockIdx.y);
 }
 
 // Products that do not wait for each other, in one launch: one of the first kind
 // and up to two of the second, whose blocks follow.
-template <typename Shape_, bool kAOuter, bool kBOuter, bool kPair, typename Epi_>
+template <typename Shape_, bool kAOuter, bool kBOuter, bool kPair, bool kScaled, typename Epi_>
 struct Part {
   typedef Shape_ Sh;
   typedef Epi_ Epi;
@@ -564,7 +648,8 @@ struct Part {
   Epi epi;
   int blocks;  // a multiple of 8, so that a tile's XCD is the one it has alone
   __device__ __forceinline__ void run(char* lds, int id) const {
-    if (id < p.nm * p.nn) product_block<Bf16, Sh, kAOuter, kBOuter, kPair>(p, epi, lds, id, 0);
+    if (id < p.nm * p.nn)
+      product_block<Bf16, Sh, kAOuter, kBOuter, kPair, kScaled>(p, epi, lds, id, 0);
   }
 };
 

@@ -82,14 +82,17 @@ struct Plan {
 // Blocks that may share so many stages of k: 16, of eight stages each or more.
 inline int splits_most(int stages) { return std::min(16, std::max(1, stages / 8)); }
 
-// M rows and N columns (of B, so 2 f of the pair form), `stages` of k.
-inline Plan plan_product(Layout l, bool i8, long long M, long long N, int stages) {
+// M rows and N columns (of B, so 2 f of the pair form), `stages` of k.  scaled: A's
+// rows have units: tiles of 32 rows are left out (a joint launch is faster where they
+// would be chosen).
+inline Plan plan_product(Layout l, bool i8, long long M, long long N, int stages,
+                         bool scaled = false) {
   constexpr int kCUs = 256;
   const int kind = l == kInner ? i8 : l == kOuterB ? 2 : 3;
   Plan best = {0, 1, stages, 1e30f};
   for (int t = 0; t < kTileKernels; ++t) {
     const auto& c = kTileCosts[t].of[kind];
-    if (c.one == 0) continue;
+    if (c.one == 0 || (scaled && kTileCosts[t].bm == 32)) continue;
     const long long tiles = up(M, kTileCosts[t].bm) * up(N, kTileCosts[t].bn);
     for (int k = 1; k <= (l == kOuterBoth ? splits_most(stages) : 1); k *= 2) {
       const int per = std::max((int)up(stages, k), 1), splits = std::max((int)up(stages, per), 1);
@@ -140,20 +143,20 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ ws,
   epi(m, n, v);
 }
 
-template <typename Mma, Layout kL, bool kPair, typename Epi, int... kShape>
+template <typename Mma, Layout kL, bool kPair, bool kScaled, typename Epi, int... kShape>
 inline void launch_shape(Problem p, const Plan& plan, const Epi& epi, hipStream_t s,
                          std::integer_sequence<int, kShape...>) {
   typedef Shape<kShape...> Sh;
   p.nm = (int)up(p.M, Sh::BM);
   p.nn = (int)up(kPair ? 2LL * p.N : p.N, Sh::BN);
   p.per_group = (int)up(plan.per, Sh::G);
-  hipLaunchKernelGGL((product_kernel<Mma, Sh, kL == kOuterBoth, kL != kInner, kPair, Epi>),
+  hipLaunchKernelGGL((product_kernel<Mma, Sh, kL == kOuterBoth, kL != kInner, kPair, kScaled, Epi>),
                      dim3(p.nm * p.nn, plan.splits), dim3(Sh::kThreads), Sh::kLds, s, p, epi);
 }
 
-template <typename Mma, Layout kL, bool kPair, typename Epi>
+template <typename Mma, Layout kL, bool kPair, bool kScaled, typename Epi>
 inline void launch_tiles(const Problem& p, const Plan& plan, const Epi& epi, hipStream_t s) {
-  auto go = [&](auto shape) { launch_shape<Mma, kL, kPair>(p, plan, epi, s, shape); };
+  auto go = [&](auto shape) { launch_shape<Mma, kL, kPair, kScaled>(p, plan, epi, s, shape); };
   using std::integer_sequence;
   constexpr bool kIn = kL == kInner, kB = kL == kOuterB, kBoth = kL == kOuterBoth;
   switch (plan.tile) {  // (as kTileCosts has them)
@@ -172,14 +175,14 @@ inline void launch_tiles(const Problem& p, const Plan& plan, const Epi& epi, hip
     case 5: return go(integer_sequence<int, 64, 128, 1, 4, 3>{});
     case 6: return go(integer_sequence<int, 64, 64, 2, 2, 3>{});
     case 7:
-      if constexpr (!kBoth) go(integer_sequence<int, 32, 64, 2, 2, 4>{});
+      if constexpr (!kBoth && !kScaled) go(integer_sequence<int, 32, 64, 2, 2, 4>{});
       return;
     case 8:
-      if constexpr (kB || (kIn && std::is_same_v<Mma, Bf16>))
+      if constexpr (kB || (kIn && !kScaled && std::is_same_v<Mma, Bf16>))
         go(integer_sequence<int, 32, 64, 2, 2, 3, 4>{});
       return;
     case 9:
-      if constexpr (kIn) go(integer_sequence<int, 32, 32, 2, 1, 4, 2>{});
+      if constexpr (kIn && !kScaled) go(integer_sequence<int, 32, 32, 2, 1, 4, 2>{});
       return;
     case 10:
       if constexpr (!kBoth) go(integer_sequence<int, 160, 256, 2, 4, 2, 1, 1>{});
@@ -202,19 +205,20 @@ inline Problem problem_of(const Operand& a, const Operand& b, int M, int N, int 
 
 // C = A B^T with the epilogue; k values a row.  ws: partial_bytes of it (both
 // operands outer).
-template <typename Mma, Layout kL, bool kPair, typename Epi>
+template <typename Mma, Layout kL, bool kPair, bool kScaled = false, typename Epi>
 inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int N, int k,
                                  int elem_bytes, const Epi& epi, void* ws, hipStream_t s) {
   const Problem p = problem_of(a, b, M, N, k, elem_bytes);
-  if constexpr (kL == kInner) {
+  if constexpr (kL == kInner && !kScaled) {
     if (direct_applies(M, N, b.stride, kPair))
       return launch_direct<Mma, kPair, false>({a.p, b.p, a.stride, b.stride, M, N, p.kbytes, 0},
                                               epi, s);
   }
-  const Plan plan = plan_product(kL, std::is_same_v<Mma, I8>, M, kPair ? 2LL * N : N, p.stages);
+  const Plan plan =
+      plan_product(kL, std::is_same_v<Mma, I8>, M, kPair ? 2LL * N : N, p.stages, kScaled);
   if constexpr (kL == kOuterBoth) {
     if (plan.splits > 1) {
-      launch_tiles<Mma, kL, kPair>(p, plan, StorePartial{(float*)ws, M, N}, s);
+      launch_tiles<Mma, kL, kPair, kScaled>(p, plan, StorePartial{(float*)ws, M, N}, s);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL((join_kernel<Epi>), dim3((uint32_t)up((long long)M * (N / 8), 256)),
@@ -223,7 +227,7 @@ inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int 
       return hipGetLastError();
     }
   }
-  launch_tiles<Mma, kL, kPair>(p, plan, epi, s);
+  launch_tiles<Mma, kL, kPair, kScaled>(p, plan, epi, s);
   return hipGetLastError();
 }
 
@@ -303,9 +307,10 @@ template <> struct TileShape<8> { typedef Shape<32, 64, 2, 2, 3, 4> Type; };
 template <> struct TileShape<11> { typedef Shape<128, 128, 4, 4, 2> Type; };
 
 // A product as a part of a launch.
-template <typename Sh, Layout kL, bool kPair, typename Epi>
+template <typename Sh, Layout kL, bool kPair, bool kScaled = false, typename Epi>
 inline auto part_of(const Operand& a, const Operand& b, int M, int N, int k, const Epi& epi) {
-  Part<Sh, kL == kOuterBoth, kL != kInner, kPair, Epi> part{problem_of(a, b, M, N, k, 2), epi, 0};
+  Part<Sh, kL == kOuterBoth, kL != kInner, kPair, kScaled, Epi> part{
+      problem_of(a, b, M, N, k, 2), epi, 0};
   Problem& p = part.p;
   p.nm = (int)up(M, Sh::BM);
   p.nn = (int)up(kPair ? 2LL * N : N, Sh::BN);

@@ -100,7 +100,40 @@ __global__ __launch_bounds__(256) void dequantize_i8(const int8_t* __restrict__ 
   store8<kF32>(out, 8 * (size_t)i, i8x8_to_f32(*(const u32x2*)(codes + 8 * (size_t)i)) * s);
 }
 
+// Checkpoint rows as the gated block's gradient multiplies them (launch_unpack_i8); a
+// block takes a group of 16 rows, so that their units are stored together.  A code has
+// seven bits: its product with a power of two is exact in bf16.
+__global__ __launch_bounds__(256) void unpack_i8(const int8_t* __restrict__ codes,
+                                                 const float* __restrict__ scales, int T, int K,
+                                                 int G, uint16_t* __restrict__ whole,
+                                                 float* __restrict__ unit,
+                                                 uint16_t* __restrict__ restored) {
+  const int g = blockIdx.x % G, row = blockIdx.x / G * 16 + (threadIdx.x >> 4);
+  const int l = threadIdx.x & 15, at = g * 128 + 8 * l;
+  if (row >= T || at >= K) return;
+  const size_t p = (size_t)row * K + at;
+  const float s = scales[(size_t)row * G + g];
+  const f32x8 q = i8x8_to_f32(*(const u32x2*)(codes + p));
+  if (whole) {
+    // s = m 2^e with m in [0.5, 1); a scale of 0 (its codes are zeros) has unit 1, and
+    // NaN stays in the unit
+    const int e = __builtin_amdgcn_frexp_expf(s) - 1;
+    store8<false>(whole, p, q * __builtin_ldexpf(1.0f, e));
+    if (l == 0)
+      unit[(size_t)g * T + row] = s == 0.0f ? 1.0f : 2.0f * __builtin_amdgcn_frexp_mantf(s);
+  }
+  if (restored) store8<false>(restored, p, q * s);
+}
+
 }  // namespace
+
+hipError_t launch_unpack_i8(const int8_t* codes, const float* scales, int T, int K,
+                            uint16_t* whole, float* unit, uint16_t* restored, hipStream_t s) {
+  const int G = (K + 127) / 128;
+  hipLaunchKernelGGL(unpack_i8, dim3((uint32_t)(((long long)T + 15) / 16 * G)), dim3(256), 0, s,
+                     codes, scales, T, K, G, whole, unit, restored);
+  return hipGetLastError();
+}
 
 hipError_t launch_quantize_i8(const void* x, int x_f32, int T, int K, int by_row, int8_t* codes,
                               float* scales, hipStream_t s) {

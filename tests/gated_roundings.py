@@ -74,8 +74,9 @@ def out_of(x, w, v, f32):
     return y, e if f32 else e + rounding(y), n
 
 
-def gradients_of(dout, x, w, v, gate_up, dw_f32):
-    """{name: (gradient, variance, independent values)}, all fp64."""
+def gradients_of(dout, x, w, v, gate_up, dw_f32, x_rounded=None):
+    """{name: (gradient, variance, independent values)}, all fp64.  x_rounded: what
+    dw_gate_up multiplies in x's place (a checkpoint's rows, rounded to bf16)."""
     T, d = x.shape
     f = v.shape[1]
     if gate_up is None:
@@ -92,6 +93,7 @@ def gradients_of(dout, x, w, v, gate_up, dw_f32):
                       a * a * edh + (1.1 * dh) ** 2 * eg), 1)
     var = rounded + more
     eh = vh + (1.1 * u) ** 2 * eg + a * a * eu
+    x = x if x_rounded is None else x_rounded
     dx, dw, dv = dgu @ w, t_(dgu) @ x, t_(dout) @ h
     edx = var @ (w * w) + sums(dgu, w) + rounding(dx)
     edw = t_(var) @ (x * x) + sums(t_(dgu), x)

@@ -72,6 +72,21 @@ def test_mistakes_are_refused(T, d, f, dw_f32, wrong, seen):
     assert set(refused(random_inputs(T, d, f), None, dw_f32, wrong)) == seen
 
 
+@pytest.mark.parametrize("T,d,f", SIZES)
+def test_a_checkpoint_rounded_throughout_is_refused(T, d, f):
+    """Rows that are not bf16's, rounded before the pre-activations too."""
+    p = random_inputs(T, d, f)
+    g = torch.Generator().manual_seed(T)
+    rows = p["x"].to(F64) * (1 + torch.rand(T, d, generator=g, dtype=F64))
+    p["x"] = rows.to(BF16)
+    want = gr.gradients_of(*(t.to(F64) for t in (p["dout"], rows, p["w"], p["v"])), None, True,
+                           p["x"].to(F64))
+    got = gr.emulated(p, dw_f32=True)
+    for name in GRADS:
+        with pytest.raises(AssertionError, match=name):
+            gr.check(name, got[name], want[name])
+
+
 @pytest.mark.parametrize("T,d,f", SIZES + [(1, 8, 8), (5, 16, 8)])
 def test_exact_data(T, d, f):
     """The stated arithmetic gives the exact results, whatever the order of a sum."""

@@ -85,23 +85,82 @@ def test_errors_are_the_stated_roundings(product):
                 gr.check(n, y, want[n])
 
 
-@pytest.mark.parametrize("T,d,f", [(40, 264, 136), (700, 520, 264), (2600, 1024, 512)])
-def test_fp32_dout_and_checkpoints(T, d, f):
-    """Both are rounded to bf16 once, as the calls state, and to nothing less."""
-    print(f"sources T={T} d={d} f={f}", flush=True)
+# checkpoint calls by the kernel that forms gate and up again
+CHECKPOINTS = {**JOINT["recompute"],
+               "apart 128x128": (7374, 2016, 264), "apart 128x128 k2": (7647, 5912, 136),
+               "apart 160x256": (5047, 752, 776), "apart 192x256": (3236, 664, 1920),
+               "apart 256x256": (1167, 600, 5048), "apart 64x128": (391, 2736, 4136),
+               "apart 64x64": (4717, 1376, 416)}
+
+
+@pytest.mark.parametrize("T,d,f", [(1, 264, 136), (40, 264, 136), (700, 520, 264),
+                                   (2600, 1024, 512)])
+def test_fp32_dout(T, d, f):
+    """Rounded to bf16 once, as the call states, and to nothing less."""
+    print(f"fp32 dout T={T} d={d} f={f}", flush=True)
     p = gr.exact_inputs(T, d, f, device=DEV)
     want = gr.exact_results(p)
-    codes = p["x"].to(torch.int8)
-    scales = torch.ones(T, -(-d // 128), device=DEV)
-    got = gradients(p, x=codes, x_scales=scales, dout=p["dout"].float())
-    for n, y in got.items():
+    for n, y in gradients(p, dout=p["dout"].float()).items():
         assert torch.equal(y, want[n].float().to(y.dtype)), n
     p = random_inputs(T, d, f)
     dout = p["dout"].float() * 1.001
-    codes, scales = moe.moe_quantize_i8(p["x"])
-    x = moe.moe_dequantize_i8(codes, scales)  # bf16
-    got = gradients(p, x=codes, x_scales=scales, dout=dout)
-    want = gr.gradients_of(dout.to(BF16).to(F64), x.to(F64), p["w"].to(F64), p["v"].to(F64), None,
-                           True)
-    for n, y in got.items():
+    want = gr.gradients_of(dout.to(BF16).to(F64), *(p[k].to(F64) for k in "xwv"), None, True)
+    for n, y in gradients(p, dout=dout).items():
         gr.check(n, y, want[n])
+
+
+@pytest.mark.parametrize("name", CHECKPOINTS)
+def test_checkpoints(name):
+    """Gate and up are of the restored rows themselves, whose scales differ from group
+    to group; only what dw_gate_up multiplies is rounded to bf16."""
+    T, d, f = CHECKPOINTS[name]
+    print(f"checkpoint {name} T={T} d={d} f={f}", flush=True)
+    p = gr.exact_inputs(T, d, f, device=DEV)
+    want = gr.exact_results(p)
+    ones = torch.ones(T, -(-d // 128), device=DEV)
+    for n, y in gradients(p, x=p["x"].to(torch.int8), x_scales=ones).items():
+        assert torch.equal(y, want[n].float().to(y.dtype)), n
+    p = random_inputs(T, d, f)
+    g = torch.Generator(DEV).manual_seed(T)
+    size = torch.exp2(2 * torch.randn(T, -(-d // 128), generator=g, device=DEV))
+    x = p["x"].float() * size.repeat_interleave(128, 1)[:, :d] / 4
+    codes, scales = moe.moe_quantize_i8(x)
+    restored = codes.to(F64) * scales.to(F64).repeat_interleave(128, 1)[:, :d]
+    rounded = moe.moe_dequantize_i8(codes, scales).to(F64)
+    want = gr.gradients_of(*(t.to(F64) for t in (p["dout"], restored, p["w"], p["v"])), None, True,
+                           rounded)
+    for n, y in gradients(p, x=codes, x_scales=scales).items():
+        gr.check(n, y, want[n])
+
+
+@pytest.mark.parametrize("T,d,f", [(3, 392, 16), (70, 648, 72), (600, 1160, 136),
+                                   (4000, 264, 520)])
+def test_checkpoint_rows_of_any_scale(T, d, f):
+    """Groups of zeros, of 2^-100 and of 2^60 beside each other, and one that is not
+    finite: sums go from unit to unit without loss, and a row that is not finite
+    touches its own row of dx alone."""
+    print(f"checkpoint rows T={T} d={d} f={f}", flush=True)
+    p = random_inputs(T, d, f)
+    G = -(-d // 128)
+    g = torch.Generator(DEV).manual_seed(T)
+    at = torch.randint(0, 4, (T, G), generator=g, device=DEV)
+    at[:, 0] = 1
+    size = torch.tensor([0.0, 1.0, 2.0 ** -100, 2.0 ** 60], device=DEV)[at]
+    x = p["x"].float() * size.repeat_interleave(128, 1)[:, :d]
+    w = p["w"].clone()
+    big = (at == 3).any(0).repeat_interleave(128)[:d]
+    w[:, big] = (w[:, big].float() * 2.0 ** -62).to(BF16)
+    codes, scales = moe.moe_quantize_i8(x)
+    p["w"] = w
+    restored = codes.to(F64) * scales.to(F64).repeat_interleave(128, 1)[:, :d]
+    rounded = moe.moe_dequantize_i8(codes, scales).to(F64)
+    want = gr.gradients_of(*(t.to(F64) for t in (p["dout"], restored, w, p["v"])), None, True,
+                           rounded)
+    clean = gradients(p, x=codes, x_scales=scales)
+    for n, y in clean.items():
+        gr.check(n, y, want[n])
+    scales[T // 2, G - 1] = float("nan")
+    codes[T // 2, 128 * (G - 1):] = 0
+    got = gradients(p, x=codes, x_scales=scales)["dx"]
+    keep = torch.arange(T, device=DEV) != T // 2
+    assert torch.isnan(got[T // 2]).all() and torch.equal(got[keep], clean["dx"][keep])

@@ -15,15 +15,15 @@
 // from 64 bits.  g and u of an 8-bit checkpoint are formed from its codes and the
 // scales (mm_core.hpp, kScaled), so that its rows are rounded to bf16 for dWgu alone,
 // which is 2.9e-3 from 64 bits: there the scale changes along the sum, from token to
-// token, and a second product with what the rounding leaves would cost a fifth of the
-// gradient's time.  (Rounded for all of them: 3.0e-3, 3.4e-3 and 3.3e-3 for dx, dWgu and
+// token, and a second product with what the rounding leaves would be a quarter more
+// operations.  (Rounded for all of them: 3.0e-3, 3.4e-3 and 3.3e-3 for dx, dWgu and
 // dWd.  Scaling sums costs 1 to 5 %: 4093 tokens of 2048 through 1024 164 -> 170 us.)
 // All sums are fp32 in a fixed order, and g and u that are computed again stay fp32.
 //
 // Bound by the matrix cores for prompts and training, by the weights' bytes and the
 // launches' latency for few tokens.  bf16: 2501 tokens of 4096 through 2048 features
-// 110 us (1.15 PFLOP/s), 4096 tokens 159 us (1.30); the gradient of 4096 tokens 369
-// us (1.1), of which the product with the activation's gradient takes a quarter: its
+// 116 us (1.09 PFLOP/s), 4096 tokens 159 us (1.30); the gradient of 4096 tokens 370
+// us (1.1; from an fp32 dout, into fp32 gradients of the weights 395), of which the product with the activation's gradient takes a quarter: its
 // epilogue moves 84 MB that no other block's products hide.  Pre-activations
 // computed again: 131 tokens of 2048 through 1024 29 us in three launches (five,
 // product by product: 44 us), 4093 tokens from a checkpoint 167 to 175 us.
@@ -240,8 +240,8 @@ const FusedTiles kFused[] = {{128, 128, 2.7f, 1.9f, {0.63f, 0.37f}, {0.51f, 0.36
 
 // -1: one by one; of kRecompute; behind them of kFused.  Over 60 random sizes (30 to
 // 8192 tokens) 0.2 % above the fastest and 4 % less of the gradient's time than
-// without the fused kernels: 7114 tokens of 256 through 1824 136 us one by one, 107
-// fused; 131 of 2048 through 1024 29 us jointly, 38 fused.
+// without the fused kernels: 7114 tokens of 256 through 1824 133 us one by one, 102
+// fused; 131 of 2048 through 1024 29 us jointly, 44 fused.
 int plan_recompute(int T, int d, int f) {
   const JointItem items[] = {{kInner, T, 2LL * f, stages_of(d)}, {kOuterB, T, f, stages_of(d)}};
   float us;

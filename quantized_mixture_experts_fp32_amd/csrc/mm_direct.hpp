@@ -16,13 +16,13 @@
 // codes on their way to LDS, while the weights are in flight.
 //
 // Bytes: one token of 4096 values through 14336 features (both products of the
-// gated block) 75 us, 4.7 TB/s, the rate of a large copy; smaller calls are bound
+// gated block) 69 us, 5.1 TB/s, the rate of a large copy; smaller calls are bound
 // by the latency of a launch and of the first loads, and by the tokens' way to
 // LDS, which 16 long tokens take as long for as the weights: 2048 through 1024
-// features 9.3 us for one token and 11.2 for 16, 4096 through 2048 15.4 and 18.6.
+// features 8.6 us for one token and 10.6 for 16, 4096 through 2048 15.0 and 18.2.
 // Eight waves a block share k, so that 16 weight rows a block still keep enough
 // loads in flight; the first group of weights is asked for ahead of the tokens
-// (16 tokens, 2048 through 1024: 11.2 us, behind them 12.3).
+// (16 tokens, 2048 through 1024: 1.1 us less than behind them).
 #pragma once
 #include "i8.hpp"
 #include "mm_core.hpp"

@@ -20,7 +20,7 @@ enum Layout { kInner, kOuterB, kOuterBoth };
 // of a stage where a block is alone on its CU, each: its share of a full CU.
 // Fitted by kind of product to 140 to 180 random sizes each (1 to 8192 rows, 64
 // to 50304 columns, k 8 to 8192); on 70 others of each kind the choice took 0.2 to
-// 0.7 % longer than the fastest tile on average, 13 % at most
+// 0.7 % longer than the fastest tile on average, 12 % at most
 // (profiles/product_choice.txt).
 struct TileCost {
   int bm, bn;
@@ -238,8 +238,8 @@ inline hipError_t launch_product(const Operand& a, const Operand& b, int M, int 
 //   max(longest, work) + overlap * min(longest, work)
 // with the longest block's time alone on a CU, and all blocks' shares of a full
 // CU over the 256 CUs; overlap 0.2, or 0.5 where a block has its CU to itself and
-// is there for few blocks with a long k (tokens 1, d 896, f 1952: 27.6 us with tiles
-// of four waves, 21.3 with 16; 131, 2048, 1024: 26.4 and 29.3); one by one they take
+// is there for few blocks with a long k (the gradient of 1 token, d 896, f 1952 28.3 us
+// with tiles of four waves, 25.1 with 16; 131, 2048, 1024: 29.9 and 31.0); one by one they take
 // the sum of their plans.  Over 80 random sizes of a gradient (1 to 8192 tokens,
 // 128 to 4096 values) the choice took 1.6 % longer than the best and 26 % less than
 // one by one; 5000 tokens of 2560 through 2560 features 350 us together and 385 us

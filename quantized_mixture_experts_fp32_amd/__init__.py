@@ -1547,6 +1547,8 @@ class GatedFfn:
         """Gradient of forward_block at the checkpointed residual, for dout
         [T][d] in the residual's type -> (dresidual in that type, dgain fp32 [d]
         or None, dw_gate_up, dw_down)."""
+        if kept is None:
+            raise ValueError("backward_block: kept is None (forward_block ran with keep=False)")
         codes, scales = kept
         if stream is not None:
             with self._stream_of("backward_block", dout, stream, gain, codes, scales):

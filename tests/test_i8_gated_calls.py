@@ -57,6 +57,11 @@ def test_shared_weights_are_recorded_on_the_stream(monkeypatch, with_shared):
     assert {id(t) for t in seen} == {id(t) for t in want}
 
 
+def test_a_block_that_kept_nothing():
+    with pytest.raises(ValueError, match="keep=False"):
+        shared_block(128, 16).backward_block(torch.zeros(4, 128), None)
+
+
 # ---------------------------------------------------------- the largest launches
 def threads(name, T, N):
     """Of the linear map's launch: 512 for 16 features (few tokens), or a tile's

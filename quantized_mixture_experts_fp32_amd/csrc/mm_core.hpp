@@ -382,8 +382,9 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
   constexpr int kUnits = kScaled ? (TM + 63) / 64 : 1;
   struct Units {
     float v[kUnits];
-  } unit, after_unit, ahead;  // of the sums, of the next stage, of the one after it
-  float factor[MI];           // from the first to the second, of a fragment's rows
+  } unit, after_unit, later_unit;  // of the sums, of the next group, as asked for
+  float factor[MI];                // from the first to the second, of a fragment's rows
+  static_assert(!kScaled || !kAOuter, "rows of a K-inner operand, k not split");
   auto units_of = [&](int kt) {
     const int stage = min(stage0 + Sh::G * kt, p.stages - 1);
     Units u;
@@ -404,7 +405,7 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
   };
   if constexpr (kScaled) {
     unit = after_unit = units_of(0);
-    ahead = units_of(1);
+    later_unit = units_of(1);
 #pragma unroll
     for (int i = 0; i < MI; ++i) factor[i] = 1.0f;
   }
@@ -496,14 +497,14 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
     at_b.get = after(at_b.get, Sh::SB);
     // (units are asked for between two stages' loads, so that no wait is longer)
     if constexpr (decltype(last)::value) {
-      after_unit = ahead;
+      after_unit = later_unit;
       Units ratio;
 #pragma unroll
       for (int i = 0; i < kUnits; ++i)
         ratio.v[i] = unit.v[i] * __builtin_amdgcn_rcpf(after_unit.v[i]);
       by_fragment(ratio);
     }
-    if constexpr (decltype(first)::value && !kApart) ahead = units_of(kt + 2);
+    if constexpr (decltype(first)::value && !kApart) later_unit = units_of(kt + 2);
     if constexpr (kScaled) __builtin_amdgcn_sched_barrier(0);
     if constexpr (kApart) {
       multiply(f1, f0, 0, kFirst, kBetween, kNo);
@@ -512,7 +513,7 @@ __device__ __forceinline__ void product_block(const Problem& p, const Epi& epi, 
       asked_b();
     }
     asked_a();
-    if constexpr (decltype(first)::value && kApart) ahead = units_of(kt + 2);
+    if constexpr (decltype(first)::value && kApart) later_unit = units_of(kt + 2);
   };
   if constexpr (kScaled) {
     constexpr std::true_type kYes{};

@@ -25,6 +25,9 @@
 // a row, two stages.  Sums are in the unit of their last stage: a ratio of two units
 // takes them from one to the next, and they are multiplied by the last one at the
 // end.  So rows restored from 8-bit codes are not rounded to bf16 on their way here.
+// Each row of sums is multiplied behind the matrix instructions of the row before: the
+// gradient of 2048 tokens of 2048 through 1024 114.6 us, all of them between two stages
+// 121, without units 112.
 //
 // Bound by the matrix cores where a launch fills the chip and k is long: bf16, the
 // gated block's two products of 8192 tokens of 8192 values through 4096 features

@@ -102,7 +102,8 @@ __global__ __launch_bounds__(256) void dequantize_i8(const int8_t* __restrict__ 
 
 // Checkpoint rows as the gated block's gradient multiplies them (launch_unpack_i8); a
 // block takes a group of 16 rows, so that their units are stored together.  A code has
-// seven bits: its product with a power of two is exact in bf16.
+// seven bits: its product with a power of two is exact in bf16.  HBM-bound, two bf16
+// arrays from one of codes: 4093 x 2048 11.9 us, 3.5 TB/s (the rounded one alone 7.5).
 __global__ __launch_bounds__(256) void unpack_i8(const int8_t* __restrict__ codes,
                                                  const float* __restrict__ scales, int T, int K,
                                                  int G, uint16_t* __restrict__ whole,

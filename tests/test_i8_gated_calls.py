@@ -96,8 +96,7 @@ def needed(lib, T, d, f, do_f32, x_i8, kept):
     p = ctypes.c_void_p(0x10000)
     rc = lib.moe_gated_ffn_bwd(p, int(do_f32), p, p if x_i8 else None, p if kept else None, p, p,
                                T, d, f, p, p, p, 0, p, 0, None)
-    if rc == moe.MOE_OK or rc != moe.MOE_ERR_WORKSPACE:
-        raise AssertionError(rc)
+    assert rc == moe.MOE_ERR_WORKSPACE, rc
     return int(re.search(rb"< (\d+) bytes", lib.moe_last_error())[1])
 
 
